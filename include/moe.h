@@ -307,6 +307,62 @@ int moe_layer(const moe_slot_pool* pool, const float* d_logits, const uint8_t* d
  * cols must be a positive multiple of 128. */
 int moe_quant_act(const uint16_t* d_x, int rows, int cols, uint8_t* d_codes, uint8_t* d_exps, void* stream);
 
+/* ---------------------------------------------------------------- norm
+ * The rows the layer reads: x of moe_layer / moe_expert_ffn / moe_route_gemm
+ * and the 8-bit rows of the dense products below. Per row of cols values, in
+ * fp32:
+ *    v = x (+ res),  r = 1 / sqrt(mean(v^2) + eps),  y = v * r (* weight).
+ * Written as asked for, each rounded once from the fp32 values:
+ *  d_sum bf16 [rows, cols]: v, the residual stream going on; d_y bf16
+ *  [rows, cols]: y; and with qmode
+ *   MOE_Q_I8_ROW: d_codes i8 [rows, cols] and d_scales f32 [rows]; with
+ *     m = max(max|y|, 2^-100): scale = m / 127, code = rint(y * (127 / m))
+ *     (ties to even), all in fp32; code * scale stands for y;
+ *   MOE_Q_FP8_G128_POW2: d_codes u8 [rows, cols] and d_scales u8
+ *     [rows, cols / 128]: the e4m3 codes and E8M0 bytes of moe_quant_act, of
+ *     the unrounded y (cols % 128 == 0, every pointer 16-byte aligned);
+ *   MOE_Q_NONE: neither (both NULL).
+ *  d_x bf16 [rows, cols]; d_res the same or NULL; d_weight f32 [cols] or NULL
+ *  (ones); d_sum and d_y may be NULL, but something has to be written.
+ * d_sum and d_y may each be d_x or d_res itself (not the same one); no other
+ * overlap is allowed. A row (FP8: a group) of y that holds infinity or NaN
+ * gets codes 0 and a NaN scale (FP8: the E8M0 NaN byte 255); a row whose sum
+ * of squares overflows fp32 gives y = 0, as the formula does in fp32.
+ * Limits: 1 <= rows, 1 <= cols <= 16384, eps > 0 and finite.
+ * moe_quant_rows: MOE_Q_I8_ROW of the rows of d_x themselves. */
+enum { MOE_Q_NONE = 0, MOE_Q_I8_ROW = 1, MOE_Q_FP8_G128_POW2 = 2 };
+int moe_norm(const uint16_t* d_x, const uint16_t* d_res, const float* d_weight, float eps, int rows, int cols,
+             int qmode, uint16_t* d_sum, uint16_t* d_y, uint8_t* d_codes, void* d_scales, void* stream);
+int moe_quant_rows(const uint16_t* d_x, int rows, int cols, int8_t* d_codes, float* d_scales, void* stream);
+
+/* ---------------------------------------------------------------- int8 products
+ * The dense products that run for every token beside the routed experts (a
+ * shared expert, the projections around the layer), on int8 matrix cores:
+ *    out[m][n] = (sum_k a[m][k] * b[n][k]) * sa[m] * sb[n] (+ bias[n]) (+ add[m][n]);
+ * the sum is an exact int32, the rest fp32, one rounding to the output type.
+ *  d_a i8 [M, K], d_sa f32 [M]: rows and scales as moe_norm and
+ *  moe_quant_rows write them (a factor per token, such as a shared expert's
+ *  gate, can be multiplied into d_sa); d_b i8 [N, K], d_sb f32 [N];
+ *  d_bias f32 [N] or NULL; d_add [M, N] of the output's type or NULL (it may
+ *  be d_out itself); d_out bf16 [M, N] (MOE_OUT_BF16) or f32 (MOE_OUT_F32).
+ * moe_glu_i8, a shared expert's first half in one kernel: with g and u the
+ * products of a with rows [0, I) (gate) and [I, 2I) (up) of d_w13 i8 [2I, K]
+ * and their scales d_s13 f32 [2I], h = silu(g) * u, d_h bf16 [M, I].
+ * Codes are any int8 (-128 included). The results do not depend on how the
+ * work is split and repeat bit for bit.
+ * Limits: 1 <= M, N, I <= 2^30; K a multiple of 16, 16 <= K <= 131056; fewer than
+ * 2^31 tiles of 16 x 8 outputs; d_a, d_b and d_w13 16-byte aligned.
+ * The workspace holds the call's workspace_bytes bytes (it may be NULL where
+ * that is 0; the query gives 0 for invalid sizes too). */
+enum { MOE_OUT_BF16 = 0, MOE_OUT_F32 = 1 };
+size_t moe_gemm_i8_workspace_bytes(int M, int N, int K);
+int moe_gemm_i8(const int8_t* d_a, const float* d_sa, const int8_t* d_b, const float* d_sb, const float* d_bias,
+                const void* d_add, int M, int N, int K, int out_type, void* d_out, void* d_ws, size_t ws_bytes,
+                void* stream);
+size_t moe_glu_i8_workspace_bytes(int M, int I, int K);
+int moe_glu_i8(const int8_t* d_a, const float* d_sa, const int8_t* d_w13, const float* d_s13, int M, int I, int K,
+               uint16_t* d_h, void* d_ws, size_t ws_bytes, void* stream);
+
 /* ---------------------------------------------------------------- pool check
  * [VEP] "hierarchical paging of expert weights": slots are refilled while
  * the model runs. Every FFN call treats a slot as not resident (its pairs add

@@ -6,6 +6,7 @@ allocated with torch before the call. If the library is missing the first
 call raises: there is no other implementation to fall back to.
 """
 import ctypes
+import functools
 import os
 import re
 from ctypes import c_int, c_size_t, c_void_p
@@ -17,6 +18,8 @@ HEADER = os.path.join(os.path.dirname(HERE), "include", "moe.h")
 MOE_OK, MOE_EINVAL, MOE_EHIP = 0, -1, -2
 FMT_FP8_E4M3_ROW, FMT_INT4_G128 = 0, 1
 ACT_BF16, ACT_FP8_G128_POW2 = 0, 1
+Q_NONE, Q_I8_ROW, Q_FP8_G128_POW2 = 0, 1, 2
+OUT_BF16, OUT_F32 = 0, 1
 
 
 class MoeError(RuntimeError):
@@ -68,6 +71,12 @@ def _declare(lib):
                               P, P, P, P, P, P, P, P, P, P, c_size_t, P]),
         "moe_dequant_slot": (c_int, [ctypes.POINTER(moe_slot_pool), c_int, P, P, P]),
         "moe_quant_act": (c_int, [P, c_int, c_int, P, P, P]),
+        "moe_norm": (c_int, [P, P, P, ctypes.c_float, c_int, c_int, c_int, P, P, P, P, P]),
+        "moe_quant_rows": (c_int, [P, c_int, c_int, P, P, P]),
+        "moe_gemm_i8_workspace_bytes": (c_size_t, [c_int, c_int, c_int]),
+        "moe_gemm_i8": (c_int, [P, P, P, P, P, P, c_int, c_int, c_int, c_int, P, P, c_size_t, P]),
+        "moe_glu_i8_workspace_bytes": (c_size_t, [c_int, c_int, c_int]),
+        "moe_glu_i8": (c_int, [P, P, P, P, c_int, c_int, c_int, P, P, c_size_t, P]),
         "moe_pool_check": (c_int, [ctypes.POINTER(moe_slot_pool), P, P, P]),
         "moe_debug_poison": (c_int, [c_int]),
         "moe_bitwidth_plan": (c_int, [P, c_int, c_int, P]),
@@ -426,6 +435,178 @@ def quant_act(x, codes=None, exps=None, stream=None):
     _check(lib().moe_quant_act(_ptr(x, torch.bfloat16, R * C, "x"), R, C, _ptr(codes, torch.uint8, R * C, "codes"),
                                _ptr(exps, torch.uint8, R * (C // 128), "exps"), _stream(stream)))
     return codes, exps
+
+
+# ---------------------------------------------------------------- norm, int8 products
+def _on_stream(f):
+    """Runs f with its `stream` argument as the current stream, so that what f
+    allocates (outputs, workspaces, intermediates freed when it returns) belongs
+    to that stream too and is not handed out again while it is in use there."""
+    @functools.wraps(f)
+    def call(*args, stream=None, **kwargs):
+        if stream is None:
+            return f(*args, **kwargs)
+        import torch
+        for t in (*args, *kwargs.values()):
+            if isinstance(t, torch.Tensor) and t.device != stream.device:
+                raise MoeError(f"the stream is on {stream.device}, a tensor on {t.device}")
+        with torch.cuda.stream(stream):
+            return f(*args, **kwargs)
+    return call
+
+
+def _one_device(dev, *tensors):
+    """The current stream of the device that all tensors of a call have to be on."""
+    import torch
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise MoeError(f"tensors of one call are on {dev} and {t.device}")
+    if dev.type != "cuda":
+        raise MoeError("tensors must be device tensors")
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+def _shape(t, shape, dtype, name):
+    """Address of a contiguous tensor of exactly this shape and type (None passes)."""
+    if t is None:
+        return None
+    if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
+        raise MoeError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}, "
+                       f"got {t.dtype} {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _rows2d(t, name):
+    if t.dim() != 2 or t.shape[0] < 1 or t.shape[1] < 1:
+        raise MoeError(f"{name} must be a non-empty matrix, got shape {tuple(t.shape)}")
+    return t.shape
+
+
+def _launch(dev, fn, *args):
+    """The call with `dev` as the current device (streams and kernels belong to one)."""
+    import torch
+    if torch.cuda.current_device() == dev.index:
+        status = fn(*args)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args)
+    if status != MOE_OK:
+        _check(status)
+
+
+@_on_stream
+def norm(x, weight=None, eps=1e-6, res=None, q_mode=Q_NONE, with_y=True, sum=None, y=None, codes=None, scales=None):
+    """moe_norm: RMS norm of the rows of x (+ res) with optional 8-bit rows.
+
+    Returns (y, sum, codes, scales): y bf16 (None with with_y=False), sum the
+    bf16 residual stream x + res (None without res), codes and scales as q_mode
+    says (Q_I8_ROW: int8 codes, fp32 scale per row; Q_FP8_G128_POW2: e4m3
+    bytes, E8M0 byte per 128 columns; Q_NONE: None). Outputs not passed are
+    allocated; sum and y may be x or res themselves."""
+    import torch
+    T, H = shape = _rows2d(x, "x")
+    dev = x.device
+    st = _one_device(dev, weight, res, sum, y, codes, scales)
+    if with_y and y is None:
+        y = torch.empty_like(x)
+    if res is not None and sum is None:
+        sum = torch.empty_like(x)
+    ct, ss, sd = torch.int8, (T,), torch.float32
+    if q_mode == Q_FP8_G128_POW2:
+        ct, ss, sd = torch.uint8, (T, H // 128), torch.uint8
+    if q_mode != Q_NONE:
+        codes = torch.empty(shape, dtype=ct, device=dev) if codes is None else codes
+        scales = torch.empty(ss, dtype=sd, device=dev) if scales is None else scales
+    bf = torch.bfloat16
+    _launch(dev, lib().moe_norm, _shape(x, shape, bf, "x"), _shape(res, shape, bf, "res"),
+            _shape(weight, (H,), torch.float32, "weight"), eps, T, H, q_mode, _shape(sum, shape, bf, "sum"),
+            _shape(y, shape, bf, "y") if with_y else None, _shape(codes, shape, ct, "codes"),
+            _shape(scales, ss, sd, "scales"), st)
+    return (y if with_y else None), sum, codes, scales
+
+
+@_on_stream
+def quant_rows(x, codes=None, scales=None):
+    """moe_quant_rows: (int8 codes [rows, cols], fp32 scales [rows]) of the bf16 rows of x."""
+    import torch
+    T, H = shape = _rows2d(x, "x")
+    dev = x.device
+    st = _one_device(dev, codes, scales)
+    codes = torch.empty(shape, dtype=torch.int8, device=dev) if codes is None else codes
+    scales = torch.empty(T, dtype=torch.float32, device=dev) if scales is None else scales
+    _launch(dev, lib().moe_quant_rows, _shape(x, shape, torch.bfloat16, "x"), T, H,
+            _shape(codes, shape, torch.int8, "codes"), _shape(scales, (T,), torch.float32, "scales"), st)
+    return codes, scales
+
+
+def gemm_i8_workspace_bytes(M, N, K):
+    return int(lib().moe_gemm_i8_workspace_bytes(M, N, K))
+
+
+@_on_stream
+def gemm_i8(a, sa, b, sb, bias=None, add=None, out=None, out_dtype=None, ws=None):
+    """moe_gemm_i8: (a @ b.T) * sa[:, None] * sb (+ bias) (+ add) of int8 a
+    [M, K] and b [N, K]; out bf16 (default) or fp32 [M, N]; add has out's type
+    and may be out itself."""
+    import torch
+    M, K = _rows2d(a, "a")
+    N = _rows2d(b, "b")[0]
+    dev = a.device
+    st = _one_device(dev, sa, b, sb, bias, add, out, ws)
+    if out is None:
+        out = torch.empty((M, N), dtype=torch.bfloat16 if out_dtype is None else out_dtype, device=dev)
+    ot = out.dtype
+    if ot not in (torch.bfloat16, torch.float32) or (out_dtype is not None and ot != out_dtype):
+        raise MoeError(f"out must be bfloat16 or float32 (and out_dtype, if given), got {ot}")
+    L = lib()
+    need = L.moe_gemm_i8_workspace_bytes(M, N, K)
+    if need and ws is None:
+        ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    f32 = torch.float32
+    _launch(dev, L.moe_gemm_i8, _shape(a, (M, K), torch.int8, "a"), _shape(sa, (M,), f32, "sa"),
+            _shape(b, (N, K), torch.int8, "b"), _shape(sb, (N,), f32, "sb"), _shape(bias, (N,), f32, "bias"),
+            _shape(add, (M, N), ot, "add"), M, N, K, OUT_F32 if ot == f32 else OUT_BF16,
+            _shape(out, (M, N), ot, "out"), _ptr(ws, torch.uint8, need, "ws"), 0 if ws is None else ws.numel(), st)
+    return out
+
+
+def glu_i8_workspace_bytes(M, I, K):
+    return int(lib().moe_glu_i8_workspace_bytes(M, I, K))
+
+
+@_on_stream
+def glu_i8(a, sa, w13, s13, out=None, ws=None):
+    """moe_glu_i8: silu(g) * u in bf16 [M, I], with g and u the int8 products
+    of a [M, K] with rows [0, I) and [I, 2I) of w13 [2I, K], scaled."""
+    import torch
+    M, K = _rows2d(a, "a")
+    N = _rows2d(w13, "w13")[0]
+    if N % 2:
+        raise MoeError(f"w13 holds gate and up rows, as many of each: got {N} rows")
+    I = N // 2
+    dev = a.device
+    st = _one_device(dev, sa, w13, s13, out, ws)
+    out = torch.empty((M, I), dtype=torch.bfloat16, device=dev) if out is None else out
+    L = lib()
+    need = L.moe_glu_i8_workspace_bytes(M, I, K)
+    if need and ws is None:
+        ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    _launch(dev, L.moe_glu_i8, _shape(a, (M, K), torch.int8, "a"), _shape(sa, (M,), torch.float32, "sa"),
+            _shape(w13, (N, K), torch.int8, "w13"), _shape(s13, (N,), torch.float32, "s13"), M, I, K,
+            _shape(out, (M, I), torch.bfloat16, "out"), _ptr(ws, torch.uint8, need, "ws"),
+            0 if ws is None else ws.numel(), st)
+    return out
+
+
+@_on_stream
+def shared_expert_i8(a, sa, w13, s13, w2, s2, add=None, out=None):
+    """A shared expert that runs for every token beside the routed ones: gated
+    product, row quantizer, down product (+ add, the routed experts' output; out
+    may be add itself). a int8 [T, H] and sa as norm or quant_rows give them;
+    w13 int8 [2I, H], w2 int8 [H, I] with I a multiple of 16. Returns bf16 [T, H]."""
+    h = glu_i8(a, sa, w13, s13)
+    hq, hs = quant_rows(h)
+    return gemm_i8(hq, hs, w2, s2, add=add, out=out)
 
 
 def pool_check(pool, err=None, status=None, stream=None):

@@ -87,6 +87,17 @@ bool pool_args(const moe_slot_pool* pool, moe::PoolArgs* pa) {
     return true;
 }
 
+template <typename... P>
+bool aligned16(const P*... p) {
+    return (((uintptr_t)p | ... | (uintptr_t)0) & 15) == 0;
+}
+
+// sizes of an int8 product: int32 sums cannot overflow, and tile counts fit an int
+bool valid_product(int M, int N, int K) {
+    if (M < 1 || M > (1 << 30) || N < 1 || N > (1 << 30) || K < 16 || K % 16 || K > 131056) return false;
+    return ((long long)M + 15) / 16 * (((long long)N + 7) / 8) < (1LL << 31);
+}
+
 int capacity(int T, int k, int E, int bm) {
     long long np = (long long)T * k;
     long long n = np + (np < E ? np : E) * (long long)(bm - 1);
@@ -309,6 +320,57 @@ int moe_quant_act(const uint16_t* d_x, int rows, int cols, uint8_t* d_codes, uin
     if ((long long)rows * (cols / MOE_ACT_G) >= (1LL << 31)) return MOE_EINVAL;
     clear_stale_error();
     return hip_status(moe::launch_quant_act(d_x, rows, cols, d_codes, d_exps, (hipStream_t)stream));
+}
+
+int moe_norm(const uint16_t* d_x, const uint16_t* d_res, const float* d_weight, float eps, int rows, int cols,
+             int qmode, uint16_t* d_sum, uint16_t* d_y, uint8_t* d_codes, void* d_scales, void* stream) {
+    if (!d_x || rows < 1 || cols < 1 || cols > moe::norm_max_cols()) return MOE_EINVAL;
+    if (!(eps > 0.f) || eps > 3.4028235e38f) return MOE_EINVAL;
+    if (qmode < MOE_Q_NONE || qmode > MOE_Q_FP8_G128_POW2) return MOE_EINVAL;
+    if (qmode == MOE_Q_NONE ? (d_codes || d_scales || (!d_sum && !d_y)) : (!d_codes || !d_scales)) return MOE_EINVAL;
+    if (d_sum && d_sum == d_y) return MOE_EINVAL;
+    const bool vec = cols % 8 == 0 && aligned16(d_x, d_res, d_weight, d_sum, d_y, d_codes);
+    if (qmode == MOE_Q_FP8_G128_POW2 && (cols % MOE_ACT_G || !vec)) return MOE_EINVAL;
+    clear_stale_error();
+    return hip_status(moe::launch_norm(d_x, d_res, d_weight, eps, rows, cols, qmode, d_sum, d_y, d_codes, d_scales,
+                                       vec, (hipStream_t)stream));
+}
+
+int moe_quant_rows(const uint16_t* d_x, int rows, int cols, int8_t* d_codes, float* d_scales, void* stream) {
+    if (!d_x || !d_codes || !d_scales || rows < 1 || cols < 1 || cols > moe::norm_max_cols()) return MOE_EINVAL;
+    const bool vec = cols % 8 == 0 && aligned16(d_x, d_codes);
+    clear_stale_error();
+    return hip_status(moe::launch_quant_rows(d_x, rows, cols, d_codes, d_scales, vec, (hipStream_t)stream));
+}
+
+size_t moe_gemm_i8_workspace_bytes(int M, int N, int K) {
+    (void)M, (void)N, (void)K;
+    return 0;
+}
+
+int moe_gemm_i8(const int8_t* d_a, const float* d_sa, const int8_t* d_b, const float* d_sb, const float* d_bias,
+                const void* d_add, int M, int N, int K, int out_type, void* d_out, void* d_ws, size_t ws_bytes,
+                void* stream) {
+    if (!d_a || !d_sa || !d_b || !d_sb || !d_out || !valid_product(M, N, K) || !aligned16(d_a, d_b)) return MOE_EINVAL;
+    if (out_type != MOE_OUT_BF16 && out_type != MOE_OUT_F32) return MOE_EINVAL;
+    (void)d_ws, (void)ws_bytes;
+    clear_stale_error();
+    return hip_status(moe::launch_gemm_i8(d_a, d_sa, d_b, d_sb, d_bias, d_add, M, N, K, out_type == MOE_OUT_F32, d_out,
+                                          aligned16(d_out, d_add), (hipStream_t)stream));
+}
+
+size_t moe_glu_i8_workspace_bytes(int M, int I, int K) {
+    (void)M, (void)I, (void)K;
+    return 0;
+}
+
+int moe_glu_i8(const int8_t* d_a, const float* d_sa, const int8_t* d_w13, const float* d_s13, int M, int I, int K,
+               uint16_t* d_h, void* d_ws, size_t ws_bytes, void* stream) {
+    if (!d_a || !d_sa || !d_w13 || !d_s13 || !d_h || !valid_product(M, I, K) || !aligned16(d_a, d_w13))
+        return MOE_EINVAL;
+    (void)d_ws, (void)ws_bytes;
+    clear_stale_error();
+    return hip_status(moe::launch_glu_i8(d_a, d_sa, d_w13, d_s13, M, I, K, d_h, aligned16(d_h), (hipStream_t)stream));
 }
 
 int moe_pool_check(const moe_slot_pool* pool, int32_t* d_err, uint8_t* d_status, void* stream) {
