@@ -351,17 +351,13 @@ int moe_quant_rows(const uint16_t* d_x, int rows, int cols, int8_t* d_codes, flo
  * Codes are any int8 (-128 included). The results do not depend on how the
  * work is split and repeat bit for bit.
  * Limits: 1 <= M, N, I <= 2^30; K a multiple of 16, 16 <= K <= 131056; fewer than
- * 2^31 tiles of 16 x 8 outputs; d_a, d_b and d_w13 16-byte aligned.
- * The workspace holds the call's workspace_bytes bytes (it may be NULL where
- * that is 0; the query gives 0 for invalid sizes too). */
+ * 2^31 tiles of 16 x 8 outputs; d_a, d_b and d_w13 16-byte aligned. No
+ * workspace is needed. */
 enum { MOE_OUT_BF16 = 0, MOE_OUT_F32 = 1 };
-size_t moe_gemm_i8_workspace_bytes(int M, int N, int K);
 int moe_gemm_i8(const int8_t* d_a, const float* d_sa, const int8_t* d_b, const float* d_sb, const float* d_bias,
-                const void* d_add, int M, int N, int K, int out_type, void* d_out, void* d_ws, size_t ws_bytes,
-                void* stream);
-size_t moe_glu_i8_workspace_bytes(int M, int I, int K);
+                const void* d_add, int M, int N, int K, int out_type, void* d_out, void* stream);
 int moe_glu_i8(const int8_t* d_a, const float* d_sa, const int8_t* d_w13, const float* d_s13, int M, int I, int K,
-               uint16_t* d_h, void* d_ws, size_t ws_bytes, void* stream);
+               uint16_t* d_h, void* stream);
 
 /* ---------------------------------------------------------------- pool check
  * [VEP] "hierarchical paging of expert weights": slots are refilled while

@@ -73,10 +73,8 @@ def _declare(lib):
         "moe_quant_act": (c_int, [P, c_int, c_int, P, P, P]),
         "moe_norm": (c_int, [P, P, P, ctypes.c_float, c_int, c_int, c_int, P, P, P, P, P]),
         "moe_quant_rows": (c_int, [P, c_int, c_int, P, P, P]),
-        "moe_gemm_i8_workspace_bytes": (c_size_t, [c_int, c_int, c_int]),
-        "moe_gemm_i8": (c_int, [P, P, P, P, P, P, c_int, c_int, c_int, c_int, P, P, c_size_t, P]),
-        "moe_glu_i8_workspace_bytes": (c_size_t, [c_int, c_int, c_int]),
-        "moe_glu_i8": (c_int, [P, P, P, P, c_int, c_int, c_int, P, P, c_size_t, P]),
+        "moe_gemm_i8": (c_int, [P, P, P, P, P, P, c_int, c_int, c_int, c_int, P, P]),
+        "moe_glu_i8": (c_int, [P, P, P, P, c_int, c_int, c_int, P, P]),
         "moe_pool_check": (c_int, [ctypes.POINTER(moe_slot_pool), P, P, P]),
         "moe_debug_poison": (c_int, [c_int]),
         "moe_bitwidth_plan": (c_int, [P, c_int, c_int, P]),
@@ -539,12 +537,8 @@ def quant_rows(x, codes=None, scales=None):
     return codes, scales
 
 
-def gemm_i8_workspace_bytes(M, N, K):
-    return int(lib().moe_gemm_i8_workspace_bytes(M, N, K))
-
-
 @_on_stream
-def gemm_i8(a, sa, b, sb, bias=None, add=None, out=None, out_dtype=None, ws=None):
+def gemm_i8(a, sa, b, sb, bias=None, add=None, out=None, out_dtype=None):
     """moe_gemm_i8: (a @ b.T) * sa[:, None] * sb (+ bias) (+ add) of int8 a
     [M, K] and b [N, K]; out bf16 (default) or fp32 [M, N]; add has out's type
     and may be out itself."""
@@ -552,30 +546,22 @@ def gemm_i8(a, sa, b, sb, bias=None, add=None, out=None, out_dtype=None, ws=None
     M, K = _rows2d(a, "a")
     N = _rows2d(b, "b")[0]
     dev = a.device
-    st = _one_device(dev, sa, b, sb, bias, add, out, ws)
+    st = _one_device(dev, sa, b, sb, bias, add, out)
     if out is None:
         out = torch.empty((M, N), dtype=torch.bfloat16 if out_dtype is None else out_dtype, device=dev)
     ot = out.dtype
     if ot not in (torch.bfloat16, torch.float32) or (out_dtype is not None and ot != out_dtype):
         raise MoeError(f"out must be bfloat16 or float32 (and out_dtype, if given), got {ot}")
-    L = lib()
-    need = L.moe_gemm_i8_workspace_bytes(M, N, K)
-    if need and ws is None:
-        ws = torch.empty(need, dtype=torch.uint8, device=dev)
     f32 = torch.float32
-    _launch(dev, L.moe_gemm_i8, _shape(a, (M, K), torch.int8, "a"), _shape(sa, (M,), f32, "sa"),
+    _launch(dev, lib().moe_gemm_i8, _shape(a, (M, K), torch.int8, "a"), _shape(sa, (M,), f32, "sa"),
             _shape(b, (N, K), torch.int8, "b"), _shape(sb, (N,), f32, "sb"), _shape(bias, (N,), f32, "bias"),
             _shape(add, (M, N), ot, "add"), M, N, K, OUT_F32 if ot == f32 else OUT_BF16,
-            _shape(out, (M, N), ot, "out"), _ptr(ws, torch.uint8, need, "ws"), 0 if ws is None else ws.numel(), st)
+            _shape(out, (M, N), ot, "out"), st)
     return out
 
 
-def glu_i8_workspace_bytes(M, I, K):
-    return int(lib().moe_glu_i8_workspace_bytes(M, I, K))
-
-
 @_on_stream
-def glu_i8(a, sa, w13, s13, out=None, ws=None):
+def glu_i8(a, sa, w13, s13, out=None):
     """moe_glu_i8: silu(g) * u in bf16 [M, I], with g and u the int8 products
     of a [M, K] with rows [0, I) and [I, 2I) of w13 [2I, K], scaled."""
     import torch
@@ -585,16 +571,11 @@ def glu_i8(a, sa, w13, s13, out=None, ws=None):
         raise MoeError(f"w13 holds gate and up rows, as many of each: got {N} rows")
     I = N // 2
     dev = a.device
-    st = _one_device(dev, sa, w13, s13, out, ws)
+    st = _one_device(dev, sa, w13, s13, out)
     out = torch.empty((M, I), dtype=torch.bfloat16, device=dev) if out is None else out
-    L = lib()
-    need = L.moe_glu_i8_workspace_bytes(M, I, K)
-    if need and ws is None:
-        ws = torch.empty(need, dtype=torch.uint8, device=dev)
-    _launch(dev, L.moe_glu_i8, _shape(a, (M, K), torch.int8, "a"), _shape(sa, (M,), torch.float32, "sa"),
+    _launch(dev, lib().moe_glu_i8, _shape(a, (M, K), torch.int8, "a"), _shape(sa, (M,), torch.float32, "sa"),
             _shape(w13, (N, K), torch.int8, "w13"), _shape(s13, (N,), torch.float32, "s13"), M, I, K,
-            _shape(out, (M, I), torch.bfloat16, "out"), _ptr(ws, torch.uint8, need, "ws"),
-            0 if ws is None else ws.numel(), st)
+            _shape(out, (M, I), torch.bfloat16, "out"), st)
     return out
 
 

@@ -343,32 +343,19 @@ int moe_quant_rows(const uint16_t* d_x, int rows, int cols, int8_t* d_codes, flo
     return hip_status(moe::launch_quant_rows(d_x, rows, cols, d_codes, d_scales, vec, (hipStream_t)stream));
 }
 
-size_t moe_gemm_i8_workspace_bytes(int M, int N, int K) {
-    (void)M, (void)N, (void)K;
-    return 0;
-}
-
 int moe_gemm_i8(const int8_t* d_a, const float* d_sa, const int8_t* d_b, const float* d_sb, const float* d_bias,
-                const void* d_add, int M, int N, int K, int out_type, void* d_out, void* d_ws, size_t ws_bytes,
-                void* stream) {
+                const void* d_add, int M, int N, int K, int out_type, void* d_out, void* stream) {
     if (!d_a || !d_sa || !d_b || !d_sb || !d_out || !valid_product(M, N, K) || !aligned16(d_a, d_b)) return MOE_EINVAL;
     if (out_type != MOE_OUT_BF16 && out_type != MOE_OUT_F32) return MOE_EINVAL;
-    (void)d_ws, (void)ws_bytes;
     clear_stale_error();
     return hip_status(moe::launch_gemm_i8(d_a, d_sa, d_b, d_sb, d_bias, d_add, M, N, K, out_type == MOE_OUT_F32, d_out,
                                           aligned16(d_out, d_add), (hipStream_t)stream));
 }
 
-size_t moe_glu_i8_workspace_bytes(int M, int I, int K) {
-    (void)M, (void)I, (void)K;
-    return 0;
-}
-
 int moe_glu_i8(const int8_t* d_a, const float* d_sa, const int8_t* d_w13, const float* d_s13, int M, int I, int K,
-               uint16_t* d_h, void* d_ws, size_t ws_bytes, void* stream) {
+               uint16_t* d_h, void* stream) {
     if (!d_a || !d_sa || !d_w13 || !d_s13 || !d_h || !valid_product(M, I, K) || !aligned16(d_a, d_w13))
         return MOE_EINVAL;
-    (void)d_ws, (void)ws_bytes;
     clear_stale_error();
     return hip_status(moe::launch_glu_i8(d_a, d_sa, d_w13, d_s13, M, I, K, d_h, aligned16(d_h), (hipStream_t)stream));
 }

@@ -46,25 +46,28 @@ static __device__ __forceinline__ void barrier_lds() {
     asm volatile("" ::: "memory");
 }
 
-// NC adjacent output columns of one row
-template <int NC, bool F32>
-__device__ __forceinline__ void store_cols(const GemmArgs& p, int row, int col, float (&v)[NC]) {
-    const size_t o = (size_t)row * p.N + col;
-    if (p.vec) {                                        // N % NC == 0: all NC columns or none
-        if (col >= p.N) return;
-        if (F32) {
-            if (p.add) {
+// NC adjacent output columns of one row from column col on. VEC: all of them
+// exist or none (N % NC == 0) and their address is a multiple of their size
+// (up to 16 bytes); otherwise one by one. The aligned accesses are 16 bytes
+// where NC allows.
+template <int NC, bool F32, bool ADD>
+__device__ __forceinline__ void store_vec(const GemmArgs& p, size_t o, float (&v)[NC]) {
+    if constexpr (F32) {
+        constexpr int W = NC < 4 ? NC : 4;
+        typedef float fW __attribute__((ext_vector_type(W)));
 #pragma unroll
-                for (int n = 0; n < NC; ++n) v[n] += ((const float*)p.add + o)[n];
-            }
+        for (int h = 0; h < NC / W; ++h) {
+            fW x;
 #pragma unroll
-            for (int n = 0; n < NC; ++n) ((float*)p.out + o)[n] = v[n];
-            return;
+            for (int n = 0; n < W; ++n) x[n] = v[W * h + n];
+            if (ADD) x += *(const fW*)((const float*)p.add + o + W * h);
+            *(fW*)((float*)p.out + o + W * h) = x;
         }
-        uint32_t w[NC / 2];
-        if (p.add) {
-#pragma unroll
-            for (int h = 0; h < NC / 2; ++h) w[h] = *(const uint32_t*)((const uint16_t*)p.add + o + 2 * h);
+    } else {
+        typedef uint32_t uW __attribute__((ext_vector_type(NC / 2)));
+        uW w;
+        if (ADD) {
+            w = *(const uW*)((const uint16_t*)p.add + o);
 #pragma unroll
             for (int h = 0; h < NC / 2; ++h) {
                 v[2 * h] += __uint_as_float(w[h] << 16);
@@ -73,12 +76,12 @@ __device__ __forceinline__ void store_cols(const GemmArgs& p, int row, int col, 
         }
 #pragma unroll
         for (int h = 0; h < NC / 2; ++h) w[h] = pack_bf16(v[2 * h], v[2 * h + 1]);
-        uint16_t* d = (uint16_t*)p.out + o;
-        if constexpr (NC == 2) *(uint32_t*)d = w[0];
-        else if constexpr (NC == 4) *(uint2*)d = make_uint2(w[0], w[1]);
-        else *(uint4*)d = make_uint4(w[0], w[1], w[2], w[3]);
-        return;
+        *(uW*)((uint16_t*)p.out + o) = w;
     }
+}
+template <int NC, bool F32>
+__device__ __forceinline__ void store_each(const GemmArgs& p, int row, int col, float (&v)[NC]) {
+    const size_t o = (size_t)row * p.N + col;
 #pragma unroll
     for (int n = 0; n < NC; ++n) {
         if (col + n >= p.N) continue;
@@ -94,108 +97,306 @@ __device__ __forceinline__ void store_cols(const GemmArgs& p, int row, int col, 
 
 // ------------------------------------------------------------------ tiles
 // TM x TN outputs (glu: TN rows of B = TN / 2 columns of h) by WM x WN waves,
-// K in steps of 128 bytes through a ring of R LDS stages of TM + TN rows.
+// K in steps of 128 bytes through two LDS stages of TM + TN rows.
 // A stage row's 16-byte chunk c sits at c ^ ((row / 2) & 7): 16-byte fragment
-// reads of 32 (or 16) consecutive rows then meet every bank once.
-// B fragment f = nw NF + n, row m holds output column nw 32 NF + NF m + n, so
-// the columns a lane accumulates are adjacent (glu: the first half of a wave's
-// fragments are gate rows, the second the matching up rows).
+// reads of 16 consecutive rows then meet every bank once.
+// B fragment f = nw NF + n, row m holds output column nw 16 NC + NC m + n (NC
+// = NF), so the columns a lane accumulates are adjacent (glu: NC = NF / 2; the
+// first half of a wave's fragments are gate rows, the second the matching up
+// rows).
+// Persistent: a workgroup's tiles form one stream of K steps. In the second
+// half of a step's matrix instructions every fragment of the step is in
+// registers; past a barrier its stage is refilled with the step two ahead (the
+// next tile's first ones at a tile's end, so they land during the epilogue)
+// and the next step's first fragments are read.
+template <int V>
+struct IC {
+    static constexpr int value = V;
+};
+
 template <int TM, int TN, int WM, int WN, int R, bool GLU, bool F32>
-__global__ void __launch_bounds__(64 * WM * WN) gemm_tile_kernel(GemmArgs p, int tiles_m, int tiles_n) {
+__global__ void __launch_bounds__(64 * WM * WN, 2) gemm_tile_kernel(GemmArgs p, int tiles_m, int tiles_n) {
     constexpr int WAVES = WM * WN;
-    constexpr int MF = TM / WM / 32, NF = TN / WN / 32;
+    constexpr int MF = TM / WM / 16, NF = TN / WN / 16;
     constexpr int STAGE = (TM + TN) * 128;
     constexpr int LA = TM / 8 / WAVES, LB = TN / 8 / WAVES;      // 8-row loads per wave and step
     constexpr int OUTN = GLU ? TN / 2 : TN;                      // output columns of a tile
     constexpr int NC = GLU ? NF / 2 : NF;                        // adjacent output columns of a lane
-    static_assert(MF >= 1 && NC >= 1 && LA >= 1 && LB >= 1 && TM % (8 * WAVES) == 0 && TN % (8 * WAVES) == 0, "tile");
+    constexpr int META = TM + 2 * TN;                            // floats: row scales, column scales, bias
+    static_assert(LA >= 1 && LB >= 1 && TM % (8 * WAVES) == 0 && TN % (8 * WAVES) == 0 && TM % 64 == 0 && TN % 64 == 0, "tile");
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-    float* s_sa = (float*)(smem + R * STAGE);
-    float* s_sb = s_sa + TM;                                     // TN scales (glu: gate, then up)
-    float* s_bias = s_sb + TN;
+    float* s_meta = (float*)(smem + R * STAGE);                  // two tiles' worth
     const int lane = lane_id();
     const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int mw = wv / WN, nw = wv % WN;
+    const int K = p.K, S = max(R, (K + 127) / 128);
 
-    // tile of this workgroup: each XCD takes a run of consecutive tiles
-    // (blocks are dealt to the 8 XCDs in turn), and runs go down groups of 8
-    // row panels, so an XCD's L2 serves a few panels of A and B at a time
+    // this workgroup's tiles: start + idx + per_x j, j < nj. Each XCD takes a
+    // run of consecutive tiles (blocks are dealt to the 8 XCDs in turn), and
+    // runs go down groups of 8 row panels, so an XCD's L2 serves a few panels
+    // of A and B at a time
     const int total = tiles_m * tiles_n;
-    int L;
-    {
-        const int x = blockIdx.x & 7, i = blockIdx.x >> 3, per = total >> 3, rem = total & 7;
-        L = x * per + min(x, rem) + i;
-    }
-    const int GM = 8;
-    const int grp = L / (GM * tiles_n), first = grp * GM, gsz = min(GM, tiles_m - first);
-    const int tm = first + (L - grp * GM * tiles_n) % gsz, tn = (L - grp * GM * tiles_n) / gsz;
-    const int row0 = tm * TM, col0 = tn * OUTN;
+    const int xcd = blockIdx.x & 7, idx = blockIdx.x >> 3, per_x = gridDim.x >> 3;
+    const int per = total >> 3, rem = total & 7;
+    const int start = xcd * per + min(xcd, rem), cnt = per + (xcd < rem ? 1 : 0);
+    const int nj = cnt > idx ? (cnt - idx + per_x - 1) / per_x : 0;
+    if (nj == 0) return;
+    auto place = [&](int j, int& row0, int& col0) __attribute__((always_inline)) {
+        const int L = start + idx + per_x * j;
+        const int grp = L / (8 * tiles_n), first = grp * 8, gsz = min(8, tiles_m - first), r = L - first * tiles_n;
+        row0 = (first + r % gsz) * TM;
+        col0 = r / gsz * OUTN;
+    };
 
     // ---- load side: load j of this wave fills stage rows 8 (wv LA + j) ..
     // (A; B after TM rows likewise); lane i: row i / 8 of them, chunk
-    // (i % 8) ^ ((row / 2) & 7) of its source row
-    const int K = p.K, S = (K + 127) / 128;
-    const int sub = lane >> 3;
-    auto chunk = [&](int r8) { return 16 * ((lane & 7) ^ ((4 * r8 + (lane >> 4)) & 7)); };   // r8: row / 8
+    // (i % 8) ^ ((row / 2) & 7) of its source row. 32-bit offsets from
+    // wave-uniform bases; per-lane constants are formed where they are used
+    // from an opaque copy of the lane id, so that none is held in registers
+    // (or turned into 64-bit pointers) across the step loop.
+    auto opaque_lane = [&]() __attribute__((always_inline)) {
+        int l = lane_id();
+        asm volatile("" : "+v"(l));
+        return l;
+    };
+    const int ch0 = 16 * ((lane & 7) ^ (lane >> 4));             // chunk of even 8-row groups; odd ones: ^ 64
     uint32_t oA[LA], oB[LB];
+    const uint8_t* bA;
     const uint8_t* bB[LB];
-    const uint8_t* bA = (const uint8_t*)p.a + (size_t)row0 * K;
+    int row0 = 0, col0 = 0, row1, col1;                          // the tile being multiplied; the one being loaded
+    auto setup = [&](int j) __attribute__((always_inline)) {
+        place(j, row1, col1);
+        const int sub = opaque_lane() >> 3;
+        bA = (const uint8_t*)p.a + (size_t)row1 * K;
 #pragma unroll
-    for (int j = 0; j < LA; ++j) {
-        const int r8 = wv * LA + j;
-        oA[j] = (uint32_t)min(8 * r8 + sub, p.M - 1 - row0) * K + chunk(r8);
-    }
+        for (int i = 0; i < LA; ++i) {
+            const int r8 = wv * LA + i;
+            oA[i] = (uint32_t)min(8 * r8 + sub, p.M - 1 - row1) * K + (ch0 ^ (64 * (r8 & 1)));
+        }
 #pragma unroll
-    for (int j = 0; j < LB; ++j) {
-        const int r8 = wv * LB + j, f = r8 / 4, m = 8 * (r8 & 3) + sub;
-        const int w = f / NF, n = f % NF;
-        const int c = w * 32 * NC + NC * m + n % NC;             // output column in the tile
-        bB[j] = (const uint8_t*)p.b + ((size_t)col0 + (GLU && n >= NC ? p.N : 0)) * K;
-        oB[j] = (uint32_t)min(c, p.N - 1 - col0) * K + chunk(r8);
-    }
-    auto issue = [&](int s) __attribute__((always_inline)) {
-        uint8_t* st = smem + (s % R) * STAGE;
-        const int k0 = s * 128;
-        if (k0 + 128 <= K) {
-#pragma unroll
-            for (int j = 0; j < LA; ++j) lds_dma16(bA + k0 + oA[j], st + 1024 * (wv * LA + j));
-#pragma unroll
-            for (int j = 0; j < LB; ++j) lds_dma16(bB[j] + k0 + oB[j], st + TM * 128 + 1024 * (wv * LB + j));
-        } else {                                                 // K ends inside this step
-#pragma unroll
-            for (int j = 0; j < LA; ++j)
-                lds_dma16(k0 + chunk(wv * LA + j) < K ? bA + k0 + oA[j] : g_zero16, st + 1024 * (wv * LA + j));
-#pragma unroll
-            for (int j = 0; j < LB; ++j)
-                lds_dma16(k0 + chunk(wv * LB + j) < K ? bB[j] + k0 + oB[j] : g_zero16,
-                          st + TM * 128 + 1024 * (wv * LB + j));
+        for (int i = 0; i < LB; ++i) {
+            const int r8 = wv * LB + i, f = r8 / 2, m = 8 * (r8 & 1) + sub;
+            const int w = f / NF, n = f % NF;
+            const int c = w * 16 * NC + NC * m + n % NC;         // output column in the tile
+            bB[i] = (const uint8_t*)p.b + ((size_t)col1 + (GLU && n >= NC ? p.N : 0)) * K;
+            oB[i] = (uint32_t)min(c, p.N - 1 - col1) * K + (ch0 ^ (64 * (r8 & 1)));
         }
     };
+    // the loaded tile's scales into metadata slot `slot`
+    auto meta = [&](int slot) __attribute__((always_inline)) {
+        const int ln = opaque_lane();
+        float* md = s_meta + slot * META;
+        for (int i = wv; i < TM / 64; i += WAVES)
+            lds_dma4(p.sa + min(row1 + 64 * i + ln, p.M - 1), (uint8_t*)(md + 64 * i));
+        for (int i = wv; i < TN / 64; i += WAVES) {
+            const int c = 64 * i + ln;
+            const int n = GLU ? min(col1 + c % OUTN, p.N - 1) + (c >= OUTN ? p.N : 0) : min(col1 + c, p.N - 1);
+            lds_dma4(p.sb + n, (uint8_t*)(md + TM + 64 * i));
+            if (!GLU) lds_dma4(p.bias ? p.bias + n : (const float*)g_zero16, (uint8_t*)(md + TM + TN + 64 * i));
+        }
+    };
+    // load l of the K bytes from k0 on into stage st; chunks at or past kend are zeros
+    auto dma = [&](int k0, int kend, int st, int l) __attribute__((always_inline)) {
+        const int j = l < LA ? l : 0, i = l < LA ? 0 : l - LA;
+        const int r8 = l < LA ? wv * LA + j : wv * LB + i;
+        uint32_t o = l < LA ? oA[j] : oB[i];
+        asm volatile("" : "+v"(o));
+        const uint8_t* src = (l < LA ? bA : bB[i]) + k0 + o;
+        src = k0 + (ch0 ^ (64 * (r8 & 1))) < kend ? src : g_zero16;
+        lds_dma16(src, smem + st * STAGE + (l < LA ? 0 : TM * 128) + 1024 * r8);
+    };
 
-    // ---- scales into LDS (no wait of their own: they precede the first stage)
-    for (int i = wv; i < TM / 64; i += WAVES)
+    // ---- multiply side: lane (m, q) holds 16 K bytes of fragment row m, chunk 4 u + q in sub-step u
+    i32x4 acc[MF][NF];
+    auto zero_acc = [&]() __attribute__((always_inline)) {
+#pragma unroll
+        for (int a = 0; a < MF; ++a)
+#pragma unroll
+            for (int n = 0; n < NF; ++n) acc[a][n] = i32x4{0, 0, 0, 0};
+    };
+    // (sub-step 1's chunk is sub-step 0's ^ 4: byte offset ^ 64)
+    const int lo = (lane & 15) * 128 + (((lane >> 4) ^ ((lane >> 1) & 7)) << 4);
+    i32x4 fa[2][MF], fb[2][NF];
+    constexpr int NK = MF * NF, NR = MF + NF, NL = LA + LB;
+    // fragment i of sub-step u, in the order the instructions take them
+    auto read = [&](int st, int u, int i) __attribute__((always_inline)) {
+        int off = st * STAGE;
+        asm volatile("" : "+s"(off));
+        const uint8_t* b = smem + off + (lo ^ (64 * u));
+        if (i == 0) fa[u][0] = *(const i32x4*)(b + mw * MF * 2048);
+        else if (i <= NF) fb[u][i - 1] = *(const i32x4*)(b + TM * 128 + (nw * NF + i - 1) * 2048);
+        else fa[u][i - NF] = *(const i32x4*)(b + (mw * MF + i - NF) * 2048);
+    };
+    // sub-step 0 of a step: multiply, and read sub-step 1 behind the first instructions
+    auto half0 = [&](int st) __attribute__((always_inline)) {
+#pragma unroll
+        for (int k = 0; k < NK; ++k) {
+            acc[k / NF][k % NF] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fa[0][k / NF], fb[0][k % NF], acc[k / NF][k % NF], 0, 0, 0);
+            if (k < NR) read(st, 1, k);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    // sub-step 1: after BAR instructions every wave's reads of the stage are
+    // done and the other stage has landed; then that stage's first fragments
+    // are read and this one is refilled (the loads spread over the rest)
+    constexpr int BAR = 2;
+    constexpr int LS = (NK - BAR) / NL > 0 ? (NK - BAR) / NL : 1;
+    auto half1 = [&](int st, int nx, int k0, int kend) __attribute__((always_inline)) {
+#pragma unroll
+        for (int k = 0; k < NK; ++k) {
+            acc[k / NF][k % NF] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fa[1][k / NF], fb[1][k % NF], acc[k / NF][k % NF], 0, 0, 0);
+            if (k == BAR - 1) {
+                wait_vmcnt<(R - 2) * NL>();                       // (more in flight than that: waits for more)
+                barrier_lds();
+            }
+            if (k >= BAR - 1 && k - BAR + 1 < NR) read(nx, 0, k - BAR + 1);
+            if (k >= BAR && (k - BAR) % LS == 0 && (k - BAR) / LS < NL) dma(k0, kend, st, (k - BAR) / LS);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        static_assert((NK - 1 - BAR) / LS >= NL - 1 && NK - BAR + 1 > NR, "every load and read has its instruction");
+    };
+    // KIND 0: aligned rows, 1: aligned rows with the addend, 2: any
+    auto rows_out = [&](const float* md, auto kind) __attribute__((always_inline)) {
+        constexpr int KIND = decltype(kind)::value;
+        const int ln = opaque_lane();
+        const int m = ln & 15, q = ln >> 4;
+        const int cw = nw * 16 * NC + NC * m, col = col0 + cw;
+        float sb[NF], bias[NC];
+#pragma unroll
+        for (int n = 0; n < NF; ++n) sb[n] = md[TM + (GLU && n >= NC ? OUTN : 0) + cw + n % NC];
+#pragma unroll
+        for (int n = 0; n < NC; ++n) bias[n] = GLU ? 0.f : md[TM + TN + cw + n];
+        // lane (m, q), register i of fragment (a, n): row 16 (mw MF + a) + 4 q + i
+#pragma unroll
+        for (int a = 0; a < MF; ++a) {
+            const f32x4 sa = *(const f32x4*)(md + 16 * (mw * MF + a) + 4 * q);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int row = row0 + 16 * (mw * MF + a) + 4 * q + i;
+                float v[NC];
+#pragma unroll
+                for (int n = 0; n < NC; ++n) {
+                    if constexpr (GLU) v[n] = glu_h((float)acc[a][n][i] * sa[i] * sb[n], (float)acc[a][n + NC][i] * sa[i] * sb[n + NC]);
+                    else v[n] = (float)acc[a][n][i] * sa[i] * sb[n] + bias[n];
+                }
+                if constexpr (KIND == 2) {
+                    if (row < p.M) store_each<NC, F32>(p, row, col, v);
+                } else {
+                    if (row < p.M && col < p.N) store_vec<NC, F32, KIND == 1>(p, (size_t)row * p.N + col, v);
+                }
+            }
+        }
+    };
+    auto epilogue = [&](int slot) __attribute__((always_inline)) {
+        const float* md = s_meta + slot * META;
+        if (!p.vec) rows_out(md, IC<2>{});
+        else if (!GLU && p.add) rows_out(md, IC<GLU ? 0 : 1>{});
+        else rows_out(md, IC<0>{});
+    };
+
+    setup(0);
+    meta(0);
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int l = 0; l < NL; ++l) dma(128 * r, K, r, l);
+    zero_acc();
+    wait_vmcnt<(R - 1) * NL>();
+    barrier_lds();
+#pragma unroll
+    for (int i = 0; i < NR; ++i) read(0, 0, i);
+    int st = 0, nx = 1;
+    for (int j = 0; j < nj; ++j) {
+        row0 = row1;
+        col0 = col1;
+        const int kn = j + 1 < nj ? K : 0;                       // K of the loads past this tile's last step
+        for (int s = 0; s < S; ++s) {
+            half0(st);
+            const bool next = s == S - R && kn;
+            if (next) setup(j + 1);                              // every load of tile j is out
+            half1(st, nx, (s + R < S ? s + R : s + R - S) * 128, s + R < S ? K : kn);
+            if (next) meta((j + 1) & 1);                         // (after half1's wait)
+            st = nx;
+            nx = nx + 1 == R ? 0 : nx + 1;
+        }
+        epilogue(j & 1);
+        zero_acc();
+    }
+}
+
+// ------------------------------------------------------------------ few tiles
+// Smaller tiles, for outputs that large tiles would spread over too few CUs.
+// The waves of a workgroup share one TM x TN tile and split each step's K
+// instead: wave k multiplies the 32-byte sub-steps k, k + WK .. of the whole
+// tile, which reads half as much LDS per matrix instruction as splitting the
+// tile (a 64 x 64 tile in four 32 x 32 quarters), and their int32 sums meet in
+// LDS (the ring's memory, free by then), where the epilogue takes them in row
+// order.
+template <int TM, int TN, int WK, int BK, int R, bool GLU, bool F32>
+__global__ void __launch_bounds__(64 * WK) gemm_split_kernel(GemmArgs p, int tiles_m, int tiles_n) {
+    constexpr int MF = TM / 32, NF = TN / 32;
+    constexpr int SEG = BK / 128;                                // 128-byte segments of a step, each a block of rows
+    constexpr int STAGE = (TM + TN) * BK;
+    constexpr int LD = (TM + TN) * SEG / 8 / WK;                 // 8-row loads per wave and step
+    constexpr int OUTN = GLU ? TN / 2 : TN;
+    static_assert((TM + TN) * SEG % (8 * WK) == 0 && (BK / 32) % WK == 0 && WK * TM * TN * 4 <= R * STAGE, "tile");
+    extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+    float* s_sa = (float*)(smem + R * STAGE);
+    float* s_sb = s_sa + 64 * ((TM + 63) / 64);
+    float* s_bias = s_sb + 64 * ((TN + 63) / 64);
+    const int lane = lane_id();
+    const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    // consecutive tiles share their B rows (the tall operand: the weights) on one XCD
+    int L;
+    {
+        const int total = tiles_m * tiles_n;
+        const int x = blockIdx.x & 7, i = blockIdx.x >> 3, per = total >> 3, rem = total & 7;
+        L = x * per + min(x, rem) + i;
+    }
+    const int row0 = (L % tiles_m) * TM, col0 = (L / tiles_m) * OUTN;
+    const int K = p.K, S = (K + BK - 1) / BK;
+
+    // load j of this wave: 8 stage rows; lane i row i / 8 of them, chunk (i % 8) ^ ((row / 2) & 7)
+    uint32_t off[LD];
+    const uint8_t* base[LD];
+    auto chunk = [&](int r8) { return 16 * ((lane & 7) ^ ((4 * r8 + (lane >> 4)) & 7)); };
+    auto kpos = [&](int j) { return (wv * LD + j) / ((TM + TN) / 8) * 128 + chunk(wv * LD + j); };   // K byte inside the step
+#pragma unroll
+    for (int j = 0; j < LD; ++j) {
+        const int r = (wv * LD + j) % ((TM + TN) / 8) * 8;       // first stage row of the load
+        const int sub = r + (lane >> 3);
+        if (r < TM) {
+            base[j] = (const uint8_t*)p.a + (size_t)row0 * K;
+            off[j] = (uint32_t)min(sub, p.M - 1 - row0) * K + kpos(j);
+        } else {
+            const int up = GLU && r - TM >= OUTN;
+            base[j] = (const uint8_t*)p.b + ((size_t)col0 + (up ? p.N : 0)) * K;
+            off[j] = (uint32_t)min(sub - TM - (up ? OUTN : 0), p.N - 1 - col0) * K + kpos(j);
+        }
+    }
+    auto fill = [&](int s) __attribute__((always_inline)) {
+        uint8_t* st = smem + (s % R) * STAGE;
+        const int k0 = s * BK;
+        if (k0 + BK <= K) {
+#pragma unroll
+            for (int j = 0; j < LD; ++j) lds_dma16(base[j] + k0 + off[j], st + 1024 * (wv * LD + j));
+        } else {                                                 // K ends in this step, or before it: zeros
+#pragma unroll
+            for (int j = 0; j < LD; ++j)
+                lds_dma16(k0 + kpos(j) < K ? base[j] + k0 + off[j] : g_zero16, st + 1024 * (wv * LD + j));
+        }
+    };
+    for (int i = wv; i < (TM + 63) / 64; i += WK)
         lds_dma4(p.sa + min(row0 + 64 * i + lane, p.M - 1), (uint8_t*)(s_sa + 64 * i));
-    for (int i = wv; i < TN / 64; i += WAVES) {
+    for (int i = wv; i < (TN + 63) / 64; i += WK) {
         const int c = 64 * i + lane;
-        const int n = GLU ? min(col0 + c % OUTN, p.N - 1) + (c >= OUTN ? p.N : 0) : min(col0 + c, p.N - 1);
+        const int n = GLU ? min(col0 + c % OUTN, p.N - 1) + (c >= OUTN && c < TN ? p.N : 0) : min(col0 + c, p.N - 1);
         lds_dma4(p.sb + n, (uint8_t*)(s_sb + 64 * i));
         if (!GLU && p.bias) lds_dma4(p.bias + n, (uint8_t*)(s_bias + 64 * i));
     }
-    // a step past the end fills its ring slot with zeros, so every step has
-    // the same number of loads to count (and the slot is not read)
-    auto fill = [&](int s) __attribute__((always_inline)) {
-        if (s < S) {
-            issue(s);
-            return;
-        }
-        uint8_t* st = smem + (s % R) * STAGE;
-#pragma unroll
-        for (int j = 0; j < LA + LB; ++j) lds_dma16(g_zero16, st + 1024 * (wv * (LA + LB) + j));
-    };
 #pragma unroll
     for (int s = 0; s < R - 1; ++s) fill(s);
 
-    // ---- multiply
     i32x16 acc[MF][NF];
 #pragma unroll
     for (int a = 0; a < MF; ++a)
@@ -205,18 +406,19 @@ __global__ void __launch_bounds__(64 * WM * WN) gemm_tile_kernel(GemmArgs p, int
             for (int i = 0; i < 16; ++i) acc[a][n][i] = 0;
     const int m = lane & 31, hi = lane >> 5, sw = (m >> 1) & 7;
     for (int s = 0; s < S; ++s) {
-        wait_vmcnt<(R - 2) * (LA + LB)>();                       // stage s landed (this wave's part)
-        barrier_lds();                                           // ... everyone's; and everyone has read stage s - 1
-        if (R > 2 || s + 1 < S) fill(s + R - 1);
+        wait_vmcnt<(R - 2) * LD>();
+        barrier_lds();
+        fill(s + R - 1);
         const uint8_t* st = smem + (s % R) * STAGE;
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks) {
-            const int off = m * 128 + (((2 * ks + hi) ^ sw) << 4);
+        for (int i = 0; i < BK / 32 / WK; ++i) {
+            const int ks = wv + i * WK;
+            const uint8_t* sg = st + (ks / 4) * (TM + TN) * 128 + m * 128 + (((2 * (ks & 3) + hi) ^ sw) << 4);
             i32x4 fa[MF], fb[NF];
 #pragma unroll
-            for (int a = 0; a < MF; ++a) fa[a] = *(const i32x4*)(st + (mw * MF + a) * 4096 + off);
+            for (int a = 0; a < MF; ++a) fa[a] = *(const i32x4*)(sg + a * 4096);
 #pragma unroll
-            for (int n = 0; n < NF; ++n) fb[n] = *(const i32x4*)(st + TM * 128 + (nw * NF + n) * 4096 + off);
+            for (int n = 0; n < NF; ++n) fb[n] = *(const i32x4*)(sg + TM * 128 + n * 4096);
 #pragma unroll
             for (int a = 0; a < MF; ++a)
 #pragma unroll
@@ -224,87 +426,41 @@ __global__ void __launch_bounds__(64 * WM * WN) gemm_tile_kernel(GemmArgs p, int
                     acc[a][n] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fa[a], fb[n], acc[a][n], 0, 0, 0);
         }
     }
-    wait_vmcnt<0>();
-
-    // ---- epilogue: lane (m, hi), register i of fragment (a, n): row
-    // 32 (mw MF + a) + 8 (i / 4) + 4 hi + i % 4, column NC m + n of the wave's
-    const int cw = nw * 32 * NC + NC * m, col = col0 + cw;
-    float sb[NF], bias[NC];
-#pragma unroll
-    for (int n = 0; n < NF; ++n) sb[n] = s_sb[(GLU && n >= NC ? OUTN : 0) + cw + n % NC];
-#pragma unroll
-    for (int n = 0; n < NC; ++n) bias[n] = !GLU && p.bias ? s_bias[cw + n] : 0.f;
+    wait_vmcnt<0>();                                             // the last fills land before their memory is reused
+    barrier_lds();
+    int* s_acc = (int*)smem;
 #pragma unroll
     for (int a = 0; a < MF; ++a)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int r = 32 * (mw * MF + a) + 8 * (i / 4) + 4 * hi + i % 4;
-            const float sa = s_sa[r];
-            float v[NC];
+        for (int n = 0; n < NF; ++n)
 #pragma unroll
-            for (int n = 0; n < NC; ++n) {
-                if constexpr (GLU) v[n] = glu_h((float)acc[a][n][i] * sa * sb[n], (float)acc[a][n + NC][i] * sa * sb[n + NC]);
-                else v[n] = (float)acc[a][n][i] * sa * sb[n] + bias[n];
-            }
-            if (row0 + r < p.M) store_cols<NC, F32>(p, row0 + r, col, v);
+            for (int i = 0; i < 16; ++i)
+                s_acc[wv * TM * TN + (32 * a + 8 * (i / 4) + 4 * hi + i % 4) * TN + 32 * n + m] = acc[a][n][i];
+    barrier_lds();
+    constexpr int QN = OUTN / 4;                                 // groups of 4 output columns of a row
+#pragma unroll 2
+    for (int t = threadIdx.x; t < TM * QN; t += 64 * WK) {
+        const int r = t / QN, c = t % QN * 4;
+        if (row0 + r >= p.M) continue;
+        i32x4 g = {0, 0, 0, 0}, u = {0, 0, 0, 0};
+#pragma unroll
+        for (int w = 0; w < WK; ++w) {
+            g += *(const i32x4*)(s_acc + w * TM * TN + r * TN + c);
+            if (GLU) u += *(const i32x4*)(s_acc + w * TM * TN + r * TN + c + OUTN);
         }
-}
-
-// ------------------------------------------------------------------ few rows
-// Up to 16 MF rows: the weights are streamed once, straight into registers.
-// A workgroup owns 16 rows of B (glu: 8 gate and the matching 8 up rows); its
-// waves split K in runs of 64 bytes and add their int32 sums in LDS.
-template <int MF, int WAVES, bool GLU, bool F32>
-__global__ void __launch_bounds__(64 * WAVES) gemm_rows_kernel(GemmArgs p) {
-    __shared__ int s_acc[WAVES][MF][256];
-    const int lane = lane_id(), wv = threadIdx.x / 64;
-    const int m = lane & 15, q = lane >> 4;
-    constexpr int OUTN = GLU ? 8 : 16;
-    const int col0 = blockIdx.x * OUTN;
-    const int c = min(col0 + (GLU ? m & 7 : m), p.N - 1);
-    const uint8_t* rb = (const uint8_t*)p.b + ((size_t)c + (GLU && m >= 8 ? p.N : 0)) * p.K;
-    const uint8_t* ra[MF];
+        const float sa = s_sa[r];
+        float v[4];
 #pragma unroll
-    for (int a = 0; a < MF; ++a) ra[a] = (const uint8_t*)p.a + (size_t)min(16 * a + m, p.M - 1) * p.K;
-    i32x4 acc[MF];
-#pragma unroll
-    for (int a = 0; a < MF; ++a) acc[a] = i32x4{0, 0, 0, 0};
-    const int U = (p.K + 63) / 64;
-#pragma unroll 4
-    for (int u = wv; u < U; u += WAVES) {
-        const int k = 64 * u + 16 * q;
-        const bool in = k < p.K;
-        const i32x4 fb = *(const i32x4*)(in ? rb + k : g_zero16);
-#pragma unroll
-        for (int a = 0; a < MF; ++a) {
-            const i32x4 fa = *(const i32x4*)(in ? ra[a] + k : g_zero16);
-            acc[a] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fa, fb, acc[a], 0, 0, 0);
+        for (int n = 0; n < 4; ++n) {
+            v[n] = (float)g[n] * sa * s_sb[c + n];
+            if constexpr (GLU) v[n] = glu_h(v[n], (float)u[n] * sa * s_sb[OUTN + c + n]);
+            else if (p.bias) v[n] += s_bias[c + n];
         }
-    }
-#pragma unroll
-    for (int a = 0; a < MF; ++a)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s_acc[wv][a][16 * (4 * q + i) + m] = acc[a][i];
-    __syncthreads();
-    for (int t = threadIdx.x; t < 16 * MF * OUTN; t += 64 * WAVES) {
-        const int row = t / OUTN, n = t % OUTN, e = 16 * (row & 15) + n;
-        if (row >= p.M || col0 + n >= p.N) continue;
-        int g = 0, u = 0;
-        for (int w = 0; w < WAVES; ++w) {
-            g += s_acc[w][row >> 4][e];
-            if (GLU) u += s_acc[w][row >> 4][e + 8];
-        }
-        const float sa = p.sa[row];
-        float v = (float)g * sa * p.sb[col0 + n];
-        if constexpr (GLU) v = glu_h(v, (float)u * sa * p.sb[p.N + col0 + n]);
-        else if (p.bias) v += p.bias[col0 + n];
-        const size_t o = (size_t)row * p.N + col0 + n;
-        if (F32) {
-            if (p.add) v += ((const float*)p.add)[o];
-            ((float*)p.out)[o] = v;
-        } else {
-            if (p.add) v += bf16_to_f32(((const uint16_t*)p.add)[o]);
-            ((uint16_t*)p.out)[o] = (uint16_t)pack_bf16(v, 0.f);
+        if (!p.vec) store_each<4, F32>(p, row0 + r, col0 + c, v);
+        else if (col0 + c < p.N) {
+            const size_t o = (size_t)(row0 + r) * p.N + col0 + c;
+            if (!GLU && p.add) store_vec<4, F32, true>(p, o, v);
+            else store_vec<4, F32, false>(p, o, v);
         }
     }
 }
@@ -312,30 +468,78 @@ __global__ void __launch_bounds__(64 * WAVES) gemm_rows_kernel(GemmArgs p) {
 // ------------------------------------------------------------------ launch
 template <int TM, int TN, int WM, int WN, int R, bool GLU, bool F32>
 static hipError_t launch_tile(GemmArgs p, int kid, hipStream_t stream) {
-    constexpr int OUTN = GLU ? TN / 2 : TN, NC = (GLU ? TN / 2 : TN) / WN / 32;
-    constexpr int SMEM = R * (TM + TN) * 128 + 4 * (TM + 2 * TN);
+    constexpr int OUTN = GLU ? TN / 2 : TN, NC = OUTN / WN / 16;
+    constexpr int SMEM = R * (TM + TN) * 128 + 8 * (TM + 2 * TN);
+    constexpr int PER_CU = 163840 / SMEM < 8 / (WM * WN) ? 163840 / SMEM : 8 / (WM * WN);
     hipError_t e = hipFuncSetAttribute((const void*)gemm_tile_kernel<TM, TN, WM, WN, R, GLU, F32>,
                                        hipFuncAttributeMaxDynamicSharedMemorySize, SMEM);
     if (e != hipSuccess) return e;
     p.vec = p.vec && p.N % NC == 0;
     const int tm = (p.M + TM - 1) / TM, tn = (p.N + OUTN - 1) / OUTN;
-    MOE_LAUNCH(kid, stream, (gemm_tile_kernel<TM, TN, WM, WN, R, GLU, F32>), dim3((unsigned)(tm * tn)),
-               dim3(64 * WM * WN), SMEM, stream, p, tm, tn);
+    const int slots = (device_cus() * PER_CU + 7) / 8 * 8, grid = min(slots, (tm * tn + 7) / 8 * 8);
+    MOE_LAUNCH(kid, stream, (gemm_tile_kernel<TM, TN, WM, WN, R, GLU, F32>), dim3((unsigned)grid), dim3(64 * WM * WN),
+               SMEM, stream, p, tm, tn);
     return hipGetLastError();
 }
 
-template <int MF, int WAVES, bool GLU, bool F32>
-static hipError_t launch_few(const GemmArgs& p, int kid, hipStream_t stream) {
-    MOE_LAUNCH(kid, stream, (gemm_rows_kernel<MF, WAVES, GLU, F32>), dim3((unsigned)((p.N + (GLU ? 7 : 15)) / (GLU ? 8 : 16))),
-               dim3(64 * WAVES), 0, stream, p);
+template <int TM, int TN, int WK, int BK, int R, bool GLU, bool F32>
+static hipError_t launch_split(GemmArgs p, int kid, hipStream_t stream) {
+    constexpr int OUTN = GLU ? TN / 2 : TN;
+    constexpr int SMEM = R * (TM + TN) * BK + 256 * ((TM + 63) / 64 + 2 * ((TN + 63) / 64));
+    hipError_t e = hipFuncSetAttribute((const void*)gemm_split_kernel<TM, TN, WK, BK, R, GLU, F32>,
+                                       hipFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    if (e != hipSuccess) return e;
+    p.vec = p.vec && p.N % 4 == 0;
+    const int tm = (p.M + TM - 1) / TM, tn = (p.N + OUTN - 1) / OUTN;
+    MOE_LAUNCH(kid, stream, (gemm_split_kernel<TM, TN, WK, BK, R, GLU, F32>), dim3((unsigned)(tm * tn)), dim3(64 * WK),
+               SMEM, stream, p, tm, tn);
     return hipGetLastError();
+}
+
+// The tile shapes, and what a K step of 128 costs them (us, measured on
+// products whose operands come from L2): `one` with at most one workgroup on
+// each CU, `full` with all `per_cu` of them; `round` is a round's prologue and
+// epilogue. Large tiles move fewer bytes per output, small ones reach more CUs.
+struct Shape {
+    int tm, tn, per_cu;
+    float one, full, round;
+};
+enum { S_256x256, S_256x128, S_128x128, S_64x64, S_64x32, S_32x32, S_COUNT };
+static const Shape kShapes[S_COUNT] = {{256, 256, 1, 1.45f, 1.45f, 3.0f}, {256, 128, 1, 0.80f, 0.80f, 1.8f},
+                                       {128, 128, 2, 0.70f, 0.99f, 1.2f}, {64, 64, 2, 0.23f, 0.46f, 0.6f},
+                                       {64, 32, 1, 0.13f, 0.13f, 0.6f},   {32, 32, 2, 0.07f, 0.23f, 0.4f}};
+
+// The shape that the costs above make the fastest for this many output rows
+// and B rows.
+static int pick_shape(int M, long long rows_b, int K) {
+    const long long cus = device_cus();
+    const float steps = (float)((K + 127) / 128);
+    int best = 0;
+    float least = 3.4e38f;
+    for (int i = 0; i < S_COUNT; ++i) {
+        const Shape& c = kShapes[i];
+        const long long tiles = ((M + c.tm - 1) / c.tm) * ((rows_b + c.tn - 1) / c.tn), slots = cus * c.per_cu;
+        const long long rounds = tiles / slots, rest = tiles % slots;
+        const float t = (float)rounds * (c.full * steps + c.round) +
+                        (rest ? (rest <= cus ? c.one : c.full) * steps + c.round : 0.f);
+        if (t < least) {
+            least = t;
+            best = i;
+        }
+    }
+    return best;
 }
 
 template <bool GLU, bool F32>
 static hipError_t launch_any(const GemmArgs& p, int kid, hipStream_t stream) {
-    if (p.M <= 16) return launch_few<1, 16, GLU, F32>(p, kid, stream);
-    if (p.M <= 32) return launch_few<2, 16, GLU, F32>(p, kid, stream);
-    return launch_tile<256, 256, 4, 2, 2, GLU, F32>(p, kid, stream);
+    switch (pick_shape(p.M, (long long)p.N * (GLU ? 2 : 1), p.K)) {
+        case S_256x256: return launch_tile<256, 256, 4, 2, 2, GLU, F32>(p, kid, stream);
+        case S_256x128: return launch_tile<256, 128, 4, 2, 3, GLU, F32>(p, kid, stream);
+        case S_128x128: return launch_tile<128, 128, 2, 2, 2, GLU, F32>(p, kid, stream);
+        case S_64x64: return launch_split<64, 64, 4, 128, 4, GLU, F32>(p, kid, stream);
+        case S_64x32: return launch_split<64, 32, 8, 256, 4, GLU, F32>(p, kid, stream);
+        default: return launch_split<32, 32, 8, 256, 4, GLU, F32>(p, kid, stream);
+    }
 }
 
 hipError_t launch_gemm_i8(const int8_t* a, const float* sa, const int8_t* b, const float* sb, const float* bias,

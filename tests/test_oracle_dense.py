@@ -88,11 +88,11 @@ def test_product_host_checks(L):
 
     def gemm(**k):
         v = {**ok, **k}
-        return L.moe_gemm_i8(v["a"], v["sa"], v["b"], v["sb"], n, n, v["M"], v["N"], v["K"], v["t"], v["out"], n, 0, n)
+        return L.moe_gemm_i8(v["a"], v["sa"], v["b"], v["sb"], n, n, v["M"], v["N"], v["K"], v["t"], v["out"], n)
 
     def glu(**k):
         v = {**ok, **k}
-        return L.moe_glu_i8(v["a"], v["sa"], v["b"], v["sb"], v["M"], v["N"], v["K"], v["out"], n, 0, n)
+        return L.moe_glu_i8(v["a"], v["sa"], v["b"], v["sb"], v["M"], v["N"], v["K"], v["out"], n)
 
     for bad in (dict(a=n), dict(sa=n), dict(b=n), dict(sb=n), dict(out=n), dict(a=odd), dict(b=odd), dict(M=0), dict(N=0),
                 dict(K=0), dict(K=8), dict(K=72), dict(K=131072), dict(M=1 << 30, N=1 << 30), dict(M=(1 << 30) + 1, N=1)):
