@@ -309,15 +309,14 @@ int moe_quant_act(const uint16_t* d_x, int rows, int cols, uint8_t* d_codes, uin
 
 /* ---------------------------------------------------------------- norm
  * The rows the layer reads: x of moe_layer / moe_expert_ffn / moe_route_gemm
- * and the 8-bit rows of the dense products below. Per row of cols values, in
- * fp32:
- *    v = x (+ res),  r = 1 / sqrt(mean(v^2) + eps),  y = v * r (* weight).
- * Written as asked for, each rounded once from the fp32 values:
+ * and the 8-bit rows of the dense products below. Per row of cols values:
+ *    v = x (+ res) in fp32,  r = 1 / sqrt(mean(v^2) + eps),  y = v * r (* weight),
+ * sums and y in fp64. Written as asked for, each from the unrounded values:
  *  d_sum bf16 [rows, cols]: v, the residual stream going on; d_y bf16
  *  [rows, cols]: y; and with qmode
  *   MOE_Q_I8_ROW: d_codes i8 [rows, cols] and d_scales f32 [rows]; with
- *     m = max(max|y|, 2^-100): scale = m / 127, code = rint(y * (127 / m))
- *     (ties to even), all in fp32; code * scale stands for y;
+ *     m = max(max|y|, 2^-100): scale = m / 127, code = rint(127 * y / m)
+ *     (ties to even); code * scale stands for y;
  *   MOE_Q_FP8_G128_POW2: d_codes u8 [rows, cols] and d_scales u8
  *     [rows, cols / 128]: the e4m3 codes and E8M0 bytes of moe_quant_act, of
  *     the unrounded y (cols % 128 == 0, every pointer 16-byte aligned);
@@ -325,15 +324,21 @@ int moe_quant_act(const uint16_t* d_x, int rows, int cols, uint8_t* d_codes, uin
  *  d_x bf16 [rows, cols]; d_res the same or NULL; d_weight f32 [cols] or NULL
  *  (ones); d_sum and d_y may be NULL, but something has to be written.
  * d_sum and d_y may each be d_x or d_res itself (not the same one); no other
- * overlap is allowed. A row (FP8: a group) of y that holds infinity or NaN
- * gets codes 0 and a NaN scale (FP8: the E8M0 NaN byte 255); a row whose sum
- * of squares overflows fp32 gives y = 0, as the formula does in fp32.
+ * overlap is allowed. A row (FP8: a group) of y that holds NaN or a value past
+ * the largest fp32 gets codes 0 and a NaN scale (FP8: the E8M0 NaN byte 255).
  * Limits: 1 <= rows, 1 <= cols <= 16384, eps > 0 and finite.
- * moe_quant_rows: MOE_Q_I8_ROW of the rows of d_x themselves. */
+ * moe_quant_rows: MOE_Q_I8_ROW of the rows of d_x themselves (the codes are
+ * exactly the definition's, ties included).
+ * moe_dequant_rows: the way back, d_out bf16 [rows, cols] = code * scale
+ * rounded once, for either kind of rows (MOE_Q_FP8_G128_POW2: those of
+ * moe_quant_act too; cols % 128 == 0, d_codes and d_out 16-byte aligned);
+ * rows * cols < 2^35 (2^32 where cols % 8 or an address is not 16-byte aligned). */
 enum { MOE_Q_NONE = 0, MOE_Q_I8_ROW = 1, MOE_Q_FP8_G128_POW2 = 2 };
 int moe_norm(const uint16_t* d_x, const uint16_t* d_res, const float* d_weight, float eps, int rows, int cols,
              int qmode, uint16_t* d_sum, uint16_t* d_y, uint8_t* d_codes, void* d_scales, void* stream);
 int moe_quant_rows(const uint16_t* d_x, int rows, int cols, int8_t* d_codes, float* d_scales, void* stream);
+int moe_dequant_rows(const uint8_t* d_codes, const void* d_scales, int rows, int cols, int qmode, uint16_t* d_out,
+                     void* stream);
 
 /* ---------------------------------------------------------------- int8 products
  * The dense products that run for every token beside the routed experts (a

@@ -6,7 +6,6 @@ allocated with torch before the call. If the library is missing the first
 call raises: there is no other implementation to fall back to.
 """
 import ctypes
-import functools
 import os
 import re
 from ctypes import c_int, c_size_t, c_void_p
@@ -73,6 +72,7 @@ def _declare(lib):
         "moe_quant_act": (c_int, [P, c_int, c_int, P, P, P]),
         "moe_norm": (c_int, [P, P, P, ctypes.c_float, c_int, c_int, c_int, P, P, P, P, P]),
         "moe_quant_rows": (c_int, [P, c_int, c_int, P, P, P]),
+        "moe_dequant_rows": (c_int, [P, P, c_int, c_int, c_int, P, P]),
         "moe_gemm_i8": (c_int, [P, P, P, P, P, P, c_int, c_int, c_int, c_int, P, P]),
         "moe_glu_i8": (c_int, [P, P, P, P, c_int, c_int, c_int, P, P]),
         "moe_pool_check": (c_int, [ctypes.POINTER(moe_slot_pool), P, P, P]),
@@ -436,157 +436,161 @@ def quant_act(x, codes=None, exps=None, stream=None):
 
 
 # ---------------------------------------------------------------- norm, int8 products
-def _on_stream(f):
-    """Runs f with its `stream` argument as the current stream, so that what f
-    allocates (outputs, workspaces, intermediates freed when it returns) belongs
-    to that stream too and is not handed out again while it is in use there."""
-    @functools.wraps(f)
-    def call(*args, stream=None, **kwargs):
-        if stream is None:
-            return f(*args, **kwargs)
-        import torch
-        for t in (*args, *kwargs.values()):
-            if isinstance(t, torch.Tensor) and t.device != stream.device:
-                raise MoeError(f"the stream is on {stream.device}, a tensor on {t.device}")
-        with torch.cuda.stream(stream):
-            return f(*args, **kwargs)
-    return call
-
-
-def _one_device(dev, *tensors):
-    """The current stream of the device that all tensors of a call have to be on."""
+# Small calls of these are bound by the host, so each argument is looked at
+# once and the addresses go to the library as plain integers.
+def _on(stream, f, *args):
+    """f(*args) with `stream` as the current stream, so that what f allocates
+    (outputs, intermediates freed when it returns) belongs to that stream too
+    and is not handed out again while it is in use there."""
     import torch
-    for t in tensors:
-        if t is not None and t.device != dev:
-            raise MoeError(f"tensors of one call are on {dev} and {t.device}")
-    if dev.type != "cuda":
-        raise MoeError("tensors must be device tensors")
-    return torch.cuda.current_stream(dev).cuda_stream
+    for t in args:
+        if isinstance(t, torch.Tensor) and t.device != stream.device:
+            raise MoeError(f"the stream is on {stream.device}, a tensor on {t.device}")
+    with torch.cuda.stream(stream):
+        return f(*args)
 
 
-def _shape(t, shape, dtype, name):
-    """Address of a contiguous tensor of exactly this shape and type (None passes)."""
+def _arg(t, shape, dtype, dev, name):
+    """Address of a contiguous tensor of exactly this shape and type on device `dev` (None passes)."""
     if t is None:
         return None
-    if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
-        raise MoeError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}, "
-                       f"got {t.dtype} {tuple(t.shape)}")
+    if t.shape != shape or t.dtype != dtype or not t.is_contiguous() or t.get_device() != dev:
+        raise MoeError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on device {dev}, "
+                       f"got {t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
-def _rows2d(t, name):
-    if t.dim() != 2 or t.shape[0] < 1 or t.shape[1] < 1:
-        raise MoeError(f"{name} must be a non-empty matrix, got shape {tuple(t.shape)}")
-    return t.shape
+def _matrix(t, name):
+    """(rows, cols, device index) of a non-empty matrix in device memory."""
+    dev = t.get_device()
+    if t.dim() != 2 or not t.numel() or dev < 0:
+        raise MoeError(f"{name} must be a non-empty matrix on the device, got shape {tuple(t.shape)} on {t.device}")
+    rows, cols = t.shape
+    return rows, cols, dev
 
 
 def _launch(dev, fn, *args):
-    """The call with `dev` as the current device (streams and kernels belong to one)."""
+    """fn(*args, stream) on the current stream of device `dev`, with `dev` as the current device."""
     import torch
-    if torch.cuda.current_device() == dev.index:
-        status = fn(*args)
+    stream = torch._C._cuda_getCurrentRawStream(dev)
+    if torch.cuda.current_device() == dev:
+        status = fn(*args, stream)
     else:
         with torch.cuda.device(dev):
-            status = fn(*args)
+            status = fn(*args, stream)
     if status != MOE_OK:
         _check(status)
 
 
-@_on_stream
-def norm(x, weight=None, eps=1e-6, res=None, q_mode=Q_NONE, with_y=True, sum=None, y=None, codes=None, scales=None):
+def norm(x, weight=None, eps=1e-6, res=None, q_mode=Q_NONE, with_y=True, sum=None, y=None, codes=None, scales=None,
+         stream=None):
     """moe_norm: RMS norm of the rows of x (+ res) with optional 8-bit rows.
 
     Returns (y, sum, codes, scales): y bf16 (None with with_y=False), sum the
-    bf16 residual stream x + res (None without res), codes and scales as q_mode
-    says (Q_I8_ROW: int8 codes, fp32 scale per row; Q_FP8_G128_POW2: e4m3
-    bytes, E8M0 byte per 128 columns; Q_NONE: None). Outputs not passed are
-    allocated; sum and y may be x or res themselves."""
+    bf16 residual stream x + res (None without res, unless passed), codes and
+    scales as q_mode says (Q_I8_ROW: int8 codes, fp32 scale per row;
+    Q_FP8_G128_POW2: e4m3 bytes, E8M0 byte per 128 columns; Q_NONE: None).
+    Outputs not passed are allocated; sum and y may be x or res themselves."""
+    if stream is not None:
+        return _on(stream, norm, x, weight, eps, res, q_mode, with_y, sum, y, codes, scales)
     import torch
-    T, H = shape = _rows2d(x, "x")
-    dev = x.device
-    st = _one_device(dev, weight, res, sum, y, codes, scales)
-    if with_y and y is None:
+    T, H, dev = _matrix(x, "x")
+    shape, bf = (T, H), torch.bfloat16
+    if not with_y:
+        y = None
+    elif y is None:
         y = torch.empty_like(x)
     if res is not None and sum is None:
         sum = torch.empty_like(x)
     ct, ss, sd = torch.int8, (T,), torch.float32
-    if q_mode == Q_FP8_G128_POW2:
-        ct, ss, sd = torch.uint8, (T, H // 128), torch.uint8
     if q_mode != Q_NONE:
-        codes = torch.empty(shape, dtype=ct, device=dev) if codes is None else codes
-        scales = torch.empty(ss, dtype=sd, device=dev) if scales is None else scales
-    bf = torch.bfloat16
-    _launch(dev, lib().moe_norm, _shape(x, shape, bf, "x"), _shape(res, shape, bf, "res"),
-            _shape(weight, (H,), torch.float32, "weight"), eps, T, H, q_mode, _shape(sum, shape, bf, "sum"),
-            _shape(y, shape, bf, "y") if with_y else None, _shape(codes, shape, ct, "codes"),
-            _shape(scales, ss, sd, "scales"), st)
-    return (y if with_y else None), sum, codes, scales
+        if q_mode == Q_FP8_G128_POW2:
+            ct, ss, sd = torch.uint8, (T, H // 128), torch.uint8
+        codes = x.new_empty(shape, dtype=ct) if codes is None else codes
+        scales = x.new_empty(ss, dtype=sd) if scales is None else scales
+    _launch(dev, lib().moe_norm, _arg(x, shape, bf, dev, "x"), _arg(res, shape, bf, dev, "res"),
+            _arg(weight, (H,), torch.float32, dev, "weight"), eps, T, H, q_mode, _arg(sum, shape, bf, dev, "sum"),
+            _arg(y, shape, bf, dev, "y"), _arg(codes, shape, ct, dev, "codes"), _arg(scales, ss, sd, dev, "scales"))
+    return y, sum, codes, scales
 
 
-@_on_stream
-def quant_rows(x, codes=None, scales=None):
+def quant_rows(x, codes=None, scales=None, stream=None):
     """moe_quant_rows: (int8 codes [rows, cols], fp32 scales [rows]) of the bf16 rows of x."""
+    if stream is not None:
+        return _on(stream, quant_rows, x, codes, scales)
     import torch
-    T, H = shape = _rows2d(x, "x")
-    dev = x.device
-    st = _one_device(dev, codes, scales)
-    codes = torch.empty(shape, dtype=torch.int8, device=dev) if codes is None else codes
-    scales = torch.empty(T, dtype=torch.float32, device=dev) if scales is None else scales
-    _launch(dev, lib().moe_quant_rows, _shape(x, shape, torch.bfloat16, "x"), T, H,
-            _shape(codes, shape, torch.int8, "codes"), _shape(scales, (T,), torch.float32, "scales"), st)
+    T, H, dev = _matrix(x, "x")
+    codes = x.new_empty((T, H), dtype=torch.int8) if codes is None else codes
+    scales = x.new_empty((T,), dtype=torch.float32) if scales is None else scales
+    _launch(dev, lib().moe_quant_rows, _arg(x, (T, H), torch.bfloat16, dev, "x"), T, H,
+            _arg(codes, (T, H), torch.int8, dev, "codes"), _arg(scales, (T,), torch.float32, dev, "scales"))
     return codes, scales
 
 
-@_on_stream
-def gemm_i8(a, sa, b, sb, bias=None, add=None, out=None, out_dtype=None):
+def dequant_rows(codes, scales, out=None, stream=None):
+    """moe_dequant_rows: code * scale in bf16 [rows, cols], of int8 codes with an
+    fp32 scale per row or of e4m3 bytes (uint8) with an E8M0 byte per 128 columns."""
+    if stream is not None:
+        return _on(stream, dequant_rows, codes, scales, out)
+    import torch
+    T, H, dev = _matrix(codes, "codes")
+    out = codes.new_empty((T, H), dtype=torch.bfloat16) if out is None else out
+    if codes.dtype == torch.int8:
+        mode, ss, sd = Q_I8_ROW, (T,), torch.float32
+    else:
+        mode, ss, sd = Q_FP8_G128_POW2, (T, H // 128), torch.uint8
+    _launch(dev, lib().moe_dequant_rows, _arg(codes, (T, H), torch.int8 if mode == Q_I8_ROW else torch.uint8, dev, "codes"),
+            _arg(scales, ss, sd, dev, "scales"), T, H, mode, _arg(out, (T, H), torch.bfloat16, dev, "out"))
+    return out
+
+
+def gemm_i8(a, sa, b, sb, bias=None, add=None, out=None, out_dtype=None, stream=None):
     """moe_gemm_i8: (a @ b.T) * sa[:, None] * sb (+ bias) (+ add) of int8 a
     [M, K] and b [N, K]; out bf16 (default) or fp32 [M, N]; add has out's type
     and may be out itself."""
+    if stream is not None:
+        return _on(stream, gemm_i8, a, sa, b, sb, bias, add, out, out_dtype)
     import torch
-    M, K = _rows2d(a, "a")
-    N = _rows2d(b, "b")[0]
-    dev = a.device
-    st = _one_device(dev, sa, b, sb, bias, add, out)
+    M, K, dev = _matrix(a, "a")
+    N, i8, f32 = _matrix(b, "b")[0], torch.int8, torch.float32
+    ot = out_dtype if out_dtype is not None else torch.bfloat16 if out is None else out.dtype
+    if ot != torch.bfloat16 and ot != f32:
+        raise MoeError(f"out must be bfloat16 or float32, got {ot}")
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16 if out_dtype is None else out_dtype, device=dev)
-    ot = out.dtype
-    if ot not in (torch.bfloat16, torch.float32) or (out_dtype is not None and ot != out_dtype):
-        raise MoeError(f"out must be bfloat16 or float32 (and out_dtype, if given), got {ot}")
-    f32 = torch.float32
-    _launch(dev, lib().moe_gemm_i8, _shape(a, (M, K), torch.int8, "a"), _shape(sa, (M,), f32, "sa"),
-            _shape(b, (N, K), torch.int8, "b"), _shape(sb, (N,), f32, "sb"), _shape(bias, (N,), f32, "bias"),
-            _shape(add, (M, N), ot, "add"), M, N, K, OUT_F32 if ot == f32 else OUT_BF16,
-            _shape(out, (M, N), ot, "out"), st)
+        out = a.new_empty((M, N), dtype=ot)
+    _launch(dev, lib().moe_gemm_i8, _arg(a, (M, K), i8, dev, "a"), _arg(sa, (M,), f32, dev, "sa"),
+            _arg(b, (N, K), i8, dev, "b"), _arg(sb, (N,), f32, dev, "sb"), _arg(bias, (N,), f32, dev, "bias"),
+            _arg(add, (M, N), ot, dev, "add"), M, N, K, OUT_F32 if ot == f32 else OUT_BF16,
+            _arg(out, (M, N), ot, dev, "out"))
     return out
 
 
-@_on_stream
-def glu_i8(a, sa, w13, s13, out=None):
+def glu_i8(a, sa, w13, s13, out=None, stream=None):
     """moe_glu_i8: silu(g) * u in bf16 [M, I], with g and u the int8 products
     of a [M, K] with rows [0, I) and [I, 2I) of w13 [2I, K], scaled."""
+    if stream is not None:
+        return _on(stream, glu_i8, a, sa, w13, s13, out)
     import torch
-    M, K = _rows2d(a, "a")
-    N = _rows2d(w13, "w13")[0]
+    M, K, dev = _matrix(a, "a")
+    N, i8, f32 = _matrix(w13, "w13")[0], torch.int8, torch.float32
     if N % 2:
         raise MoeError(f"w13 holds gate and up rows, as many of each: got {N} rows")
     I = N // 2
-    dev = a.device
-    st = _one_device(dev, sa, w13, s13, out)
-    out = torch.empty((M, I), dtype=torch.bfloat16, device=dev) if out is None else out
-    _launch(dev, lib().moe_glu_i8, _shape(a, (M, K), torch.int8, "a"), _shape(sa, (M,), torch.float32, "sa"),
-            _shape(w13, (N, K), torch.int8, "w13"), _shape(s13, (N,), torch.float32, "s13"), M, I, K,
-            _shape(out, (M, I), torch.bfloat16, "out"), st)
+    out = a.new_empty((M, I), dtype=torch.bfloat16) if out is None else out
+    _launch(dev, lib().moe_glu_i8, _arg(a, (M, K), i8, dev, "a"), _arg(sa, (M,), f32, dev, "sa"),
+            _arg(w13, (N, K), i8, dev, "w13"), _arg(s13, (N,), f32, dev, "s13"), M, I, K,
+            _arg(out, (M, I), torch.bfloat16, dev, "out"))
     return out
 
 
-@_on_stream
-def shared_expert_i8(a, sa, w13, s13, w2, s2, add=None, out=None):
+def shared_expert_i8(a, sa, w13, s13, w2, s2, add=None, out=None, stream=None):
     """A shared expert that runs for every token beside the routed ones: gated
     product, row quantizer, down product (+ add, the routed experts' output; out
     may be add itself). a int8 [T, H] and sa as norm or quant_rows give them;
     w13 int8 [2I, H], w2 int8 [H, I] with I a multiple of 16. Returns bf16 [T, H]."""
-    h = glu_i8(a, sa, w13, s13)
-    hq, hs = quant_rows(h)
+    if stream is not None:
+        return _on(stream, shared_expert_i8, a, sa, w13, s13, w2, s2, add, out)
+    hq, hs = quant_rows(glu_i8(a, sa, w13, s13))
     return gemm_i8(hq, hs, w2, s2, add=add, out=out)
 
 

@@ -329,18 +329,29 @@ int moe_norm(const uint16_t* d_x, const uint16_t* d_res, const float* d_weight, 
     if (qmode < MOE_Q_NONE || qmode > MOE_Q_FP8_G128_POW2) return MOE_EINVAL;
     if (qmode == MOE_Q_NONE ? (d_codes || d_scales || (!d_sum && !d_y)) : (!d_codes || !d_scales)) return MOE_EINVAL;
     if (d_sum && d_sum == d_y) return MOE_EINVAL;
-    const bool vec = cols % 8 == 0 && aligned16(d_x, d_res, d_weight, d_sum, d_y, d_codes);
-    if (qmode == MOE_Q_FP8_G128_POW2 && (cols % MOE_ACT_G || !vec)) return MOE_EINVAL;
+    const bool aligned = aligned16(d_x, d_res, d_weight, d_sum, d_y, d_codes);
+    if (qmode == MOE_Q_FP8_G128_POW2 && (cols % MOE_ACT_G || !aligned)) return MOE_EINVAL;
     clear_stale_error();
     return hip_status(moe::launch_norm(d_x, d_res, d_weight, eps, rows, cols, qmode, d_sum, d_y, d_codes, d_scales,
-                                       vec, (hipStream_t)stream));
+                                       aligned, (hipStream_t)stream));
 }
 
 int moe_quant_rows(const uint16_t* d_x, int rows, int cols, int8_t* d_codes, float* d_scales, void* stream) {
     if (!d_x || !d_codes || !d_scales || rows < 1 || cols < 1 || cols > moe::norm_max_cols()) return MOE_EINVAL;
-    const bool vec = cols % 8 == 0 && aligned16(d_x, d_codes);
     clear_stale_error();
-    return hip_status(moe::launch_quant_rows(d_x, rows, cols, d_codes, d_scales, vec, (hipStream_t)stream));
+    return hip_status(moe::launch_quant_rows(d_x, rows, cols, d_codes, d_scales, aligned16(d_x, d_codes),
+                                             (hipStream_t)stream));
+}
+
+int moe_dequant_rows(const uint8_t* d_codes, const void* d_scales, int rows, int cols, int qmode, uint16_t* d_out,
+                     void* stream) {
+    if (!d_codes || !d_scales || !d_out || rows < 1 || cols < 1 || cols > moe::norm_max_cols()) return MOE_EINVAL;
+    if (qmode != MOE_Q_I8_ROW && qmode != MOE_Q_FP8_G128_POW2) return MOE_EINVAL;
+    const bool vec = cols % 8 == 0 && aligned16(d_codes, d_out);
+    if (qmode == MOE_Q_FP8_G128_POW2 && (cols % MOE_ACT_G || !vec)) return MOE_EINVAL;
+    if ((long long)rows * cols >= (vec ? 1LL << 35 : 1LL << 32)) return MOE_EINVAL;   // 32-bit vector (value) indices
+    clear_stale_error();
+    return hip_status(moe::launch_dequant_rows(d_codes, d_scales, rows, cols, qmode, d_out, vec, (hipStream_t)stream));
 }
 
 int moe_gemm_i8(const int8_t* d_a, const float* d_sa, const int8_t* d_b, const float* d_sb, const float* d_bias,

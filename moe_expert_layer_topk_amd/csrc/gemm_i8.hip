@@ -12,6 +12,8 @@
 #include "moe_common.h"
 #include "moe_kernels.h"
 
+#include <atomic>
+
 namespace moe {
 
 typedef int i32x16 __attribute__((ext_vector_type(16)));
@@ -466,13 +468,25 @@ __global__ void __launch_bounds__(64 * WK) gemm_split_kernel(GemmArgs p, int til
 }
 
 // ------------------------------------------------------------------ launch
+// Raises a kernel's dynamic LDS limit, once for each device (the call costs
+// more than the launch's other checks together; racing callers repeat it).
+static hipError_t allow_lds(const void* kernel, int bytes, std::atomic<uint64_t>& done) {
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
+    const uint64_t bit = 1ull << (dev & 63);
+    if (e != hipSuccess || (dev < 64 && (done.load(std::memory_order_relaxed) & bit))) return e;
+    e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == hipSuccess && dev < 64) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
+
 template <int TM, int TN, int WM, int WN, int R, bool GLU, bool F32>
 static hipError_t launch_tile(GemmArgs p, int kid, hipStream_t stream) {
     constexpr int OUTN = GLU ? TN / 2 : TN, NC = OUTN / WN / 16;
     constexpr int SMEM = R * (TM + TN) * 128 + 8 * (TM + 2 * TN);
     constexpr int PER_CU = 163840 / SMEM < 8 / (WM * WN) ? 163840 / SMEM : 8 / (WM * WN);
-    hipError_t e = hipFuncSetAttribute((const void*)gemm_tile_kernel<TM, TN, WM, WN, R, GLU, F32>,
-                                       hipFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    static std::atomic<uint64_t> done{0};
+    const hipError_t e = allow_lds((const void*)gemm_tile_kernel<TM, TN, WM, WN, R, GLU, F32>, SMEM, done);
     if (e != hipSuccess) return e;
     p.vec = p.vec && p.N % NC == 0;
     const int tm = (p.M + TM - 1) / TM, tn = (p.N + OUTN - 1) / OUTN;
@@ -486,8 +500,8 @@ template <int TM, int TN, int WK, int BK, int R, bool GLU, bool F32>
 static hipError_t launch_split(GemmArgs p, int kid, hipStream_t stream) {
     constexpr int OUTN = GLU ? TN / 2 : TN;
     constexpr int SMEM = R * (TM + TN) * BK + 256 * ((TM + 63) / 64 + 2 * ((TN + 63) / 64));
-    hipError_t e = hipFuncSetAttribute((const void*)gemm_split_kernel<TM, TN, WK, BK, R, GLU, F32>,
-                                       hipFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    static std::atomic<uint64_t> done{0};
+    const hipError_t e = allow_lds((const void*)gemm_split_kernel<TM, TN, WK, BK, R, GLU, F32>, SMEM, done);
     if (e != hipSuccess) return e;
     p.vec = p.vec && p.N % 4 == 0;
     const int tm = (p.M + TM - 1) / TM, tn = (p.N + OUTN - 1) / OUTN;

@@ -13,7 +13,7 @@ int record_hip_error(int hip_error);
 // kernel ids for launch tracing (names in profile.hip)
 enum KernelId { K_ROUTE, K_ROUTE_ALIGN, K_ALIGN_SINGLE, K_ALIGN_HIST, K_ALIGN_SCAN, K_ALIGN_SCATTER, K_GEMM1_STREAM,
                 K_GEMM2_STREAM, K_QUANT_ACT, K_GEMM1_FP8, K_GEMM2_FP8, K_GEMM1_TILE, K_GEMM2_TILE, K_MFMA_PREP, K_COMBINE, K_DEQUANT, K_POOL_CHECK, K_POISON, K_ROUTER_GEMM, K_REQUANT, K_UNPACK,
-                K_NORM, K_QUANT_ROWS, K_GEMM_I8, K_GLU_I8, K_COUNT };
+                K_NORM, K_QUANT_ROWS, K_DEQUANT_ROWS, K_GEMM_I8, K_GLU_I8, K_COUNT };
 // events the next launch of kernel `kid` on `s` should stamp (false: not tracing)
 bool prof_events(int kid, hipStream_t s, hipEvent_t* start, hipEvent_t* stop);
 
@@ -111,13 +111,15 @@ hipError_t launch_dequant(const PoolArgs& pa, int slot, float* w13, float* w2, h
 // activation quantization alone: e4m3 codes [rows][cols], E8M0 bytes [rows][cols / 128]
 hipError_t launch_quant_act(const uint16_t* x, int rows, int cols, uint8_t* codes, uint8_t* exps, hipStream_t stream);
 
-// residual addition + RMS norm with optional 8-bit rows, and the int8 row quantizer (norm.hip); vec: every
-// pointer is 16-byte aligned and cols is a multiple of 8
+// residual addition + RMS norm with optional 8-bit rows, the int8 row quantizer, and 8-bit rows back to bf16 (norm.hip);
+// aligned: every pointer of the rows is 16-byte aligned; vec: and cols is a multiple of 8
 int norm_max_cols();
 hipError_t launch_norm(const uint16_t* x, const uint16_t* res, const float* w, float eps, int rows, int cols, int qmode,
-                       uint16_t* sum, uint16_t* y, uint8_t* codes, void* scales, bool vec, hipStream_t stream);
-hipError_t launch_quant_rows(const uint16_t* x, int rows, int cols, int8_t* codes, float* scales, bool vec,
+                       uint16_t* sum, uint16_t* y, uint8_t* codes, void* scales, bool aligned, hipStream_t stream);
+hipError_t launch_quant_rows(const uint16_t* x, int rows, int cols, int8_t* codes, float* scales, bool aligned,
                              hipStream_t stream);
+hipError_t launch_dequant_rows(const uint8_t* codes, const void* scales, int rows, int cols, int qmode, uint16_t* out,
+                               bool vec, hipStream_t stream);
 
 // int8 products (gemm_i8.hip); vec: out (and add) are 16-byte aligned
 hipError_t launch_gemm_i8(const int8_t* a, const float* sa, const int8_t* b, const float* sb, const float* bias,

@@ -1,21 +1,31 @@
 // Row operators ahead of the 8-bit products: residual addition + RMS norm with
-// optional 8-bit rows, and the int8 row quantizer on its own.
+// optional 8-bit rows, the int8 row quantizer on its own, and the way back from
+// 8-bit rows to bf16.
 //
-// norm:  v = x + res, r = 1 / sqrt(mean(v^2) + eps), y = v r w, all in fp32;
-//        sum = bf16(v), y = bf16(y), codes from the fp32 y: every output is
-//        rounded once.
-// int8:  m = max(max|y|, 2^-100), scale = m / 127, code = rint(y (127 / m)).
+// norm:  v = x + res (fp32), r = 1 / sqrt(mean(v^2) + eps), y = v r w;
+//        sum = bf16(v), y = bf16(y), codes from the unrounded y.
+// int8:  m = max(max|y|, 2^-100), scale = m / 127, code = rint(127 y / m).
 //        The floor keeps 127 / m finite and needs no special case for a row of
-//        zeros. Maxima are taken over the bit patterns of |y| as integers:
-//        they order like the values, with infinity and NaN above all of them,
-//        so a row holding either is found by the same reduction (scale NaN,
-//        codes 0: an int8 code cannot carry it).
-// e4m3:  per 128 columns, the power-of-two scale of moe_quant_act; a group
-//        holding infinity or NaN gets the E8M0 NaN byte and codes 0.
+//        zeros.
+// e4m3:  per 128 columns, the power-of-two scale of moe_quant_act.
+//
+// The squares' sum, r, y and the code's argument are fp64: a code changes where
+// its argument passes a border, so an error of 2^-24 would change some ten
+// codes in a million, and double-precision vector arithmetic is fast enough
+// here to hide behind memory (measured below). e4m3 codes come from y rounded
+// to odd, which a second rounding to fewer bits leaves correctly rounded.
+// Rows of int8 read from bf16 (quant_rows): 127 x / m is a border exactly, or
+// at least 1 / 512 away from it, so rounding the fp64 product to fp32 first
+// puts the exact ties back on the border.
+// A row (e4m3: a group) that holds NaN or infinity gets codes 0 and a NaN scale
+// (e4m3: the E8M0 NaN byte): an 8-bit code cannot carry them.
 //
 // Bound by HBM: each input is read once and each output written once. A row
 // stays in registers between the reductions and the stores (so the outputs
-// may be the inputs' own memory): one pass, up to 16384 columns.
+// may be the inputs' own memory): one pass, up to 16384 columns. 16384 x 2048
+// with the residual, both bf16 outputs and int8 rows: 57 us, 5.3 TB/s (a 1 GiB
+// copy on the same card: 5.1; with fp32 arithmetic 51 us); without 8-bit rows
+// 45 us. Reading a row twice would have added a third to its bytes.
 #include "moe_common.h"
 #include "moe_kernels.h"
 
@@ -31,9 +41,10 @@ struct NormArgs {
     uint16_t* y;              // may be null
     uint8_t* codes;
     void* scales;
+    double inv_cols;
 };
 
-constexpr float NORM_FLOOR = 0x1p-100f;
+constexpr double NORM_FLOOR = 0x1p-100;
 
 // two fp32 -> packed bf16, round to nearest even, NaN kept
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
@@ -41,72 +52,130 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     typedef __bf16 b2 __attribute__((ext_vector_type(2)));
     return __builtin_bit_cast(uint32_t, __builtin_convertvector((f2){a, b}, b2));
 }
-__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
-__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, o, 64));
-    return v;
-}
 
-// Reductions over the TPR threads of a row (64: one wave; 256: the workgroup,
-// through four LDS words that no other reduction of the kernel uses).
+// The largest |value| seen, and the largest upper word of an |value| as an
+// integer: at or above 0x7FF00000 where one was NaN or infinite (the maximum
+// of two floating-point values leaves a NaN out).
+struct Peak {
+    double m = 0.0;
+    uint32_t hi = 0;
+    __device__ __forceinline__ void add(double u) {
+        m = fmax(m, fabs(u));
+        hi = max(hi, (uint32_t)(__builtin_bit_cast(uint64_t, u) >> 32) & 0x7FFFFFFFu);
+    }
+};
+
+// Sum over the TPR threads of a row (64: one wave; 256: the workgroup, through
+// four LDS words that no other reduction of the kernel uses).
 template <int TPR>
-__device__ __forceinline__ float row_sum(float v, float* s) {
-    v = wave_sum(v);
+__device__ __forceinline__ double row_sum(double v, double* s) {
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
     if (TPR == 64) return v;
     if (lane_id() == 0) s[threadIdx.x / 64] = v;
     __syncthreads();
     return (s[0] + s[1]) + (s[2] + s[3]);
 }
-template <int TPR>
-__device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* s) {
-    v = wave_max_u32(v);
-    if (TPR == 64) return v;
-    if (lane_id() == 0) s[threadIdx.x / 64] = v;
-    __syncthreads();
-    return max(max(s[0], s[1]), max(s[2], s[3]));
+
+// 1 / sqrt(a) and 1 / a to a few 2^-52: the hardware's estimates (2^-24 and
+// better) and two Newton steps
+__device__ __forceinline__ double rsqrt_f64(double a) {
+    double r = __builtin_amdgcn_rsq(a);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) r = fma(0.5 * r, fma(-a * r, r, 1.0), r);
+    return a == __builtin_inf() ? 0.0 : r;
+}
+__device__ __forceinline__ double rcp_f64(double a) {
+    double r = __builtin_amdgcn_rcp(a);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) r = fma(r, fma(-a, r, 1.0), r);
+    return r;
 }
 
-// int8 scale and multiplier of a row from the bits of its largest |value|
-__device__ __forceinline__ void i8_scale(uint32_t amax_bits, float* scale, float* inv) {
-    if (amax_bits >= 0x7F800000u) {
+// int8 scale of a row and the multiplier of its v w values, from the threads'
+// peaks of |v w| and the row's r (both positive: rounding keeps their order).
+// mul 0: the row holds NaN or infinity, or a value past fp32.
+template <int TPR>
+__device__ __forceinline__ void i8_scale(Peak p, double r, double* s_max, uint32_t* s_bad, float* scale, double* mul) {
+    uint32_t bad = __ballot(p.hi >= 0x7FF00000u) != 0;
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) p.m = fmax(p.m, __shfl_xor(p.m, o, 64));
+    if (TPR != 64) {
+        if (lane_id() == 0) {
+            s_max[threadIdx.x / 64] = p.m;
+            s_bad[threadIdx.x / 64] = bad;
+        }
+        __syncthreads();
+        p.m = fmax(fmax(s_max[0], s_max[1]), fmax(s_max[2], s_max[3]));
+        bad = s_bad[0] | s_bad[1] | s_bad[2] | s_bad[3];
+    }
+    const double m = fmax(p.m * r, NORM_FLOOR);
+    // (r is 0 or NaN only where a value of the row, or the sum of its squares, was not finite)
+    if (bad || !(r > 0.0) || m > 3.4028234663852886e38) {
         *scale = __uint_as_float(0x7FC00000u);
-        *inv = 0.f;
+        *mul = 0.0;
         return;
     }
-    const float m = fmaxf(__uint_as_float(amax_bits), NORM_FLOOR);
-    *scale = m / 127.0f;
-    *inv = 127.0f / m;
+    *scale = (float)(m * (1.0 / 127.0));
+    *mul = r * (127.0 * rcp_f64(m));
 }
-// the low byte of the result is the code (inv = 0: a row that holds NaN or
-// infinity, whose products here may be NaN)
-__device__ __forceinline__ int i8_code(float v, float inv) {
-    const float c = fminf(fmaxf(rintf(v * inv), -127.f), 127.f);
-    return inv == 0.f ? 0 : (int)c;
+// the low byte of the result is the code
+template <bool NORM>
+__device__ __forceinline__ int i8_code(double u, double mul) {
+    if (mul == 0.0) return 0;
+    return NORM ? (int)rint(u * mul) : (int)rintf((float)(u * mul));
+}
+// y rounded to odd at 20 mantissa bits: the upper word, its last bit set where the lower is not zero
+__device__ __forceinline__ float to_odd(double y) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, y);
+    const uint32_t hi = (uint32_t)(b >> 32) | ((uint32_t)b != 0 ? 1u : 0u);
+    return (float)__builtin_bit_cast(double, (uint64_t)hi << 32);
 }
 
 // Rows of 16-byte vectors: TPR threads per row, NV vectors of 8 per thread.
-template <int TPR, int NV, bool NORM>
+// SHIFT: the rows' length is no multiple of 8. Vectors then lie on the
+// tensors' own 16-byte grid (all tensors start on it, so a row is shifted
+// alike in each of them); the first and the last of a row may hold elements of
+// the rows beside it, which count as zeros and are not written, and the last
+// of the whole tensor may end past it, where it is read one by one.
+template <int TPR, int NV, bool NORM, bool SHIFT>
 __global__ void __launch_bounds__(256) norm_vec_kernel(NormArgs p) {
-    __shared__ float s_sum[4];
-    __shared__ uint32_t s_max[4];
+    __shared__ double s_sum[4], s_max[4];
+    __shared__ uint32_t s_bad[4];
     const int t = threadIdx.x % TPR;
     const long row = (long)blockIdx.x * (256 / TPR) + threadIdx.x / TPR;
     if (TPR == 64 && row >= p.rows) return;             // whole waves; no barrier follows
-    const size_t base = (size_t)row * p.cols;
-    const int nvec = p.cols / 8;
+    const int off = SHIFT ? (int)(((size_t)row * p.cols) & 7) : 0;
+    const size_t base = (size_t)row * p.cols - off;     // of the row's first vector
+    const int end = off + p.cols;                       // the row's elements: [off, end) from there
+    const int nvec = SHIFT ? (end + 7) / 8 : p.cols / 8;
+    // vector i holds elements of this row only
+    auto whole = [&](int i) { return !SHIFT || (8 * i >= off && 8 * i + 8 <= end); };
+    auto load = [&](const uint16_t* src, int i) __attribute__((always_inline)) {
+        if (SHIFT && base + 8 * i + 8 > (size_t)p.rows * p.cols) {
+            i32x4 x = {0, 0, 0, 0};
+            for (int d = 0; 8 * i + d < end; ++d) x[d / 2] |= (int)((uint32_t)src[base + 8 * i + d] << (16 * (d & 1)));
+            return x;
+        }
+        return __builtin_nontemporal_load((const i32x4*)(src + base) + i);
+    };
+    auto store8 = [&](uint16_t* dst, int i, const i32x4& o) __attribute__((always_inline)) {
+        if (whole(i)) *((i32x4*)(dst + base) + i) = o;
+        else
+            for (int d = 0; d < 8; ++d)
+                if (8 * i + d >= off && 8 * i + d < end) dst[base + 8 * i + d] = (uint16_t)((uint32_t)o[d / 2] >> (16 * (d & 1)));
+    };
     i32x4 xr[NV], rr[NV];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         const int i = t + j * TPR;
         xr[j] = rr[j] = i32x4{0, 0, 0, 0};
         if (i < nvec) {
-            xr[j] = __builtin_nontemporal_load((const i32x4*)(p.x + base) + i);
-            if (NORM && p.res) rr[j] = __builtin_nontemporal_load((const i32x4*)(p.res + base) + i);
+            xr[j] = load(p.x, i);
+            if (NORM && p.res) rr[j] = load(p.res, i);
         }
     }
-    float v[NV][8];
-    float ss = 0.f;
+    float v[NV][8];                                     // (absent vectors hold zeros)
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
@@ -116,94 +185,132 @@ __global__ void __launch_bounds__(256) norm_vec_kernel(NormArgs p) {
             if (NORM) {
                 v[j][2 * d] += __uint_as_float((uint32_t)rr[j][d] << 16);
                 v[j][2 * d + 1] += __uint_as_float((uint32_t)rr[j][d] & 0xFFFF0000u);
-                ss = fmaf(v[j][2 * d], v[j][2 * d], ss);
-                ss = fmaf(v[j][2 * d + 1], v[j][2 * d + 1], ss);
             }
         }
-    if (NORM) {
-        const float r = rsqrtf(row_sum<TPR>(ss, s_sum) / (float)p.cols + p.eps);
+    if (SHIFT) {
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int i = t + j * TPR;
-            if (i >= nvec) continue;
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int d = 0; d < 8; ++d) {
+                const int e = 8 * (t + j * TPR) + d;
+                if (e < off || e >= end) v[j][d] = 0.f;
+            }
+    }
+    double r = 1.0;
+    if (NORM) {
+        double ss = 0.0;
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int d = 0; d < 8; ++d) ss = fma((double)v[j][d], (double)v[j][d], ss);
+        r = rsqrt_f64(fma(row_sum<TPR>(ss, s_sum), p.inv_cols, (double)p.eps));
+    }
+    // v w of vector j (exact: two 24-bit factors), formed again where it is
+    // needed; y is that times r
+    auto vw_of = [&](int j, double (&u)[8]) __attribute__((always_inline)) {
+#pragma unroll
+        for (int d = 0; d < 8; ++d) {
+            asm volatile("" : "+v"(v[j][d]));           // (converted again, not kept as a double)
+            u[d] = (double)v[j][d];
+        }
+        if (NORM && p.w) {
+            int i = min(t + j * TPR, nvec - 1);
+            asm volatile("" : "+v"(i));                 // (and the weights loaded again)
+            if (!whole(i)) {
+                for (int d = 0; d < 8; ++d) u[d] *= (double)p.w[min(max(8 * i + d - off, 0), p.cols - 1)];
+                return;
+            }
+            typedef f32x4 f32x4_dword __attribute__((aligned(4)));   // (vector loads need whole dwords only)
+            const f32x4 w0 = *(const f32x4_dword*)(p.w + 8 * i - off), w1 = *(const f32x4_dword*)(p.w + 8 * i - off + 4);
+#pragma unroll
+            for (int d = 0; d < 4; ++d) {
+                u[d] *= (double)w0[d];
+                u[4 + d] *= (double)w1[d];
+            }
+        }
+    };
+    Peak peak;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        if (j * TPR >= nvec) break;
+        const int i = t + j * TPR;
+        double u[8];
+        vw_of(j, u);
+        if (NORM && i < nvec) {
             if (p.sum) {
                 i32x4 o;
 #pragma unroll
                 for (int d = 0; d < 4; ++d) o[d] = (int)pack_bf16(v[j][2 * d], v[j][2 * d + 1]);
-                *((i32x4*)(p.sum + base) + i) = o;
-            }
-            f32x4 w0 = {1, 1, 1, 1}, w1 = {1, 1, 1, 1};
-            if (p.w) {
-                w0 = *((const f32x4*)p.w + 2 * i);
-                w1 = *((const f32x4*)p.w + 2 * i + 1);
-            }
-#pragma unroll
-            for (int d = 0; d < 4; ++d) {
-                v[j][d] = v[j][d] * r * w0[d];
-                v[j][4 + d] = v[j][4 + d] * r * w1[d];
+                store8(p.sum, i, o);
             }
             if (p.y) {
                 i32x4 o;
 #pragma unroll
-                for (int d = 0; d < 4; ++d) o[d] = (int)pack_bf16(v[j][2 * d], v[j][2 * d + 1]);
-                *((i32x4*)(p.y + base) + i) = o;
+                for (int d = 0; d < 4; ++d) o[d] = (int)pack_bf16((float)(u[2 * d] * r), (float)(u[2 * d + 1] * r));
+                store8(p.y, i, o);
             }
         }
-    }
-    if (p.qmode == MOE_Q_I8_ROW) {
-        uint32_t am = 0;
+        if (p.qmode == MOE_Q_I8_ROW) {
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
+            for (int d = 0; d < 8; ++d) peak.add(u[d]);
+        } else if (NORM && !SHIFT && p.qmode == MOE_Q_FP8_G128_POW2) {
+            // 16 consecutive lanes hold a group of 128 columns (cols % 128 ==
+            // 0: a group's vectors are all present or all absent)
+            float z[8];
+            uint32_t gm = 0;
 #pragma unroll
-            for (int d = 0; d < 8; ++d) am = max(am, abs_bits(v[j][d]));   // (absent vectors hold zeros)
-        float scale, inv;
-        i8_scale(row_max<TPR>(am, s_max), &scale, &inv);
-        if (t == 0) ((float*)p.scales)[row] = scale;
+            for (int d = 0; d < 8; ++d) {
+                z[d] = to_odd(u[d] * r);
+                gm = max(gm, __float_as_uint(z[d]) & 0x7FFFFFFFu);
+            }
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int i = t + j * TPR;
+            for (int o = 1; o < 16; o <<= 1) gm = max(gm, (uint32_t)__shfl_xor((int)gm, o, 64));
             if (i >= nvec) continue;
-            uint32_t o[2] = {0, 0};
-#pragma unroll
-            for (int d = 0; d < 8; ++d) o[d / 4] |= (uint32_t)(i8_code(v[j][d], inv) & 0xFF) << (8 * (d % 4));
-            *((uint2*)(p.codes + base) + i) = make_uint2(o[0], o[1]);
-        }
-    } else if (p.qmode == MOE_Q_FP8_G128_POW2) {
-        // 16 consecutive lanes hold a group of 128 columns (cols % 128 == 0:
-        // a group's vectors are all present or all absent)
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int i = t + j * TPR;
-            uint32_t am = 0;
-#pragma unroll
-            for (int d = 0; d < 8; ++d) am = max(am, abs_bits(v[j][d]));
-#pragma unroll
-            for (int o = 1; o < 16; o <<= 1) am = max(am, (uint32_t)__shfl_xor((int)am, o, 64));
-            if (i >= nvec) continue;
-            const bool bad = am >= 0x7F800000u;
-            int s = bad ? 0 : pow2_exponent_448(__uint_as_float(am));
+            const bool bad = gm >= 0x7F800000u;
+            int s = bad ? 0 : pow2_exponent_448(__uint_as_float(gm));
             s = s < -127 ? -127 : (s > 127 ? 127 : s);
             uint32_t o[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-                o[h] = f32x2_to_e4m3(ldexpf(v[j][4 * h], -s), ldexpf(v[j][4 * h + 1], -s)) |
-                       (f32x2_to_e4m3(ldexpf(v[j][4 * h + 2], -s), ldexpf(v[j][4 * h + 3], -s)) << 16);
+                o[h] = f32x2_to_e4m3(ldexpf(z[4 * h], -s), ldexpf(z[4 * h + 1], -s)) |
+                       (f32x2_to_e4m3(ldexpf(z[4 * h + 2], -s), ldexpf(z[4 * h + 3], -s)) << 16);
             *((uint2*)(p.codes + base) + i) = bad ? make_uint2(0, 0) : make_uint2(o[0], o[1]);
             if ((i & 15) == 0) ((uint8_t*)p.scales)[(size_t)row * (p.cols / 128) + i / 16] = (uint8_t)(bad ? 255 : s + 127);
         }
     }
+    if (p.qmode == MOE_Q_I8_ROW) {
+        float scale;
+        double mul;                                     // 127 r / m: what v w is multiplied by
+        i8_scale<TPR>(peak, r, s_max, s_bad, &scale, &mul);
+        if (t == 0) ((float*)p.scales)[row] = scale;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            if (j * TPR >= nvec) break;
+            const int i = t + j * TPR;
+            double u[8];
+            vw_of(j, u);
+            uint32_t o[2] = {0, 0};
+#pragma unroll
+            for (int d = 0; d < 8; ++d) o[d / 4] |= (uint32_t)(i8_code<NORM>(u[d], mul) & 0xFF) << (8 * (d % 4));
+            if (i >= nvec) continue;
+            if (whole(i)) *((uint2*)(p.codes + base) + i) = make_uint2(o[0], o[1]);
+            else
+                for (int d = 0; d < 8; ++d)
+                    if (8 * i + d >= off && 8 * i + d < end) p.codes[base + 8 * i + d] = (uint8_t)(o[d / 4] >> (8 * (d % 4)));
+        }
+    }
 }
 
-// Rows whose length or address is no multiple of 16 bytes: one element per
-// thread and step, a workgroup per row.
+// Rows whose address is no multiple of 16 bytes (or that the vector kernel has
+// no room for): one element per thread and step, a workgroup per row.
 template <int NE, bool NORM>
 __global__ void __launch_bounds__(256) norm_elem_kernel(NormArgs p) {
-    __shared__ float s_sum[4];
-    __shared__ uint32_t s_max[4];
+    __shared__ double s_sum[4], s_max[4];
+    __shared__ uint32_t s_bad[4];
     const int t = threadIdx.x;
     const size_t row = blockIdx.x, base = row * p.cols;
     float v[NE];
-    float ss = 0.f;
+    double r = 1.0, ss = 0.0;
 #pragma unroll
     for (int j = 0; j < NE; ++j) {
         const int i = t + j * 256;
@@ -212,67 +319,125 @@ __global__ void __launch_bounds__(256) norm_elem_kernel(NormArgs p) {
             v[j] = bf16_to_f32(p.x[base + i]);
             if (NORM && p.res) v[j] += bf16_to_f32(p.res[base + i]);
         }
-        ss = fmaf(v[j], v[j], ss);
     }
     if (NORM) {
-        const float r = rsqrtf(row_sum<256>(ss, s_sum) / (float)p.cols + p.eps);
 #pragma unroll
-        for (int j = 0; j < NE; ++j) {
-            const int i = t + j * 256;
-            if (i >= p.cols) continue;
-            if (p.sum) p.sum[base + i] = (uint16_t)pack_bf16(v[j], 0.f);
-            v[j] = v[j] * r * (p.w ? p.w[i] : 1.f);
-            if (p.y) p.y[base + i] = (uint16_t)pack_bf16(v[j], 0.f);
-        }
+        for (int j = 0; j < NE; ++j) ss = fma((double)v[j], (double)v[j], ss);
+        r = rsqrt_f64(fma(row_sum<256>(ss, s_sum), p.inv_cols, (double)p.eps));
+    }
+    auto vw_of = [&](int j) __attribute__((always_inline)) {
+        asm volatile("" : "+v"(v[j]));                  // (converted again, not kept as a double)
+        return (double)v[j] * (NORM && p.w ? (double)p.w[min(t + j * 256, p.cols - 1)] : 1.0);
+    };
+    Peak peak;
+#pragma unroll
+    for (int j = 0; j < NE; ++j) {
+        if (j * 256 >= p.cols) break;
+        const int i = t + j * 256;
+        const double u = vw_of(j);
+        peak.add(u);
+        if (!NORM || i >= p.cols) continue;
+        if (p.sum) p.sum[base + i] = (uint16_t)pack_bf16(v[j], 0.f);
+        if (p.y) p.y[base + i] = (uint16_t)pack_bf16((float)(u * r), 0.f);
     }
     if (p.qmode == MOE_Q_I8_ROW) {
-        uint32_t am = 0;
-#pragma unroll
-        for (int j = 0; j < NE; ++j) am = max(am, abs_bits(v[j]));
-        float scale, inv;
-        i8_scale(row_max<256>(am, s_max), &scale, &inv);
+        float scale;
+        double mul;
+        i8_scale<256>(peak, r, s_max, s_bad, &scale, &mul);
         if (t == 0) ((float*)p.scales)[row] = scale;
 #pragma unroll
         for (int j = 0; j < NE; ++j) {
             const int i = t + j * 256;
-            if (i < p.cols) p.codes[base + i] = (uint8_t)i8_code(v[j], inv);
+            if (i < p.cols) p.codes[base + i] = (uint8_t)i8_code<NORM>(vw_of(j), mul);
         }
     }
 }
 
+// ------------------------------------------------------------------ 8-bit rows -> bf16
+// 8 values per thread and step (ELEM: one); code * scale in fp32, rounded once.
+template <int QMODE, bool ELEM>
+__global__ void __launch_bounds__(256) dequant_rows_kernel(const uint8_t* codes, const void* scales, int cols, size_t n,
+                                                           uint16_t* out) {
+    // (the caller keeps the number of vectors below 2^32)
+    const uint32_t iv = blockIdx.x * 256u + threadIdx.x;
+    const size_t i = (size_t)iv * (ELEM ? 1 : 8);
+    if (i >= n) return;
+    const uint32_t row = iv / (uint32_t)(ELEM ? cols : cols / 8);
+    float sc;
+    if (QMODE == MOE_Q_I8_ROW) sc = ((const float*)scales)[row];
+    else {
+        const uint8_t e = ((const uint8_t*)scales)[i / 128];             // (rows are whole groups)
+        sc = e == 255 ? __uint_as_float(0x7FC00000u) : ldexpf(1.0f, (int)e - 127);
+    }
+    if (ELEM) {
+        out[i] = (uint16_t)pack_bf16((float)(int8_t)codes[i] * sc, 0.f);
+        return;
+    }
+    const uint2 c = *(const uint2*)(codes + i);
+    i32x4 o;
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+        const uint32_t w = (d < 2 ? c.x : c.y) >> (16 * (d & 1));
+        const float a = QMODE == MOE_Q_I8_ROW ? (float)(int8_t)w : e4m3_to_f32(w & 0xFF);
+        const float b = QMODE == MOE_Q_I8_ROW ? (float)(int8_t)(w >> 8) : e4m3_to_f32((w >> 8) & 0xFF);
+        o[d] = (int)pack_bf16(a * sc, b * sc);
+    }
+    *(i32x4*)(out + i) = o;
+}
+
 int norm_max_cols() { return 16384; }
 
-template <bool NORM>
-static hipError_t launch_rows(const NormArgs& p, bool vec, int kid, hipStream_t stream) {
-    const dim3 b(256);
-    const unsigned R = (unsigned)p.rows;
-    if (!vec) {
-        if (p.cols <= 2048) MOE_LAUNCH(kid, stream, (norm_elem_kernel<8, NORM>), dim3(R), b, 0, stream, p);
-        else MOE_LAUNCH(kid, stream, (norm_elem_kernel<64, NORM>), dim3(R), b, 0, stream, p);
-        return hipGetLastError();
-    }
-    const int nvec = p.cols / 8;
+// A wave per row needs no exchange through LDS; a workgroup per row reads a row
+// sooner. Measured (norm with int8 rows, us): 16384 x 512 int8 rows alone 10.8
+// a wave, 19.4 a workgroup; 16384 x 1112 42 and 47; 16384 x 2048 57 and 59; 1 x
+// 2048 6.6 and 5.0; 512 x 2048 8.6 and 6.8; 1000 x 2048 11.3 and 9.1.
+template <bool NORM, bool SHIFT>
+static hipError_t launch_vec(const NormArgs& p, int nvec, int kid, hipStream_t stream) {
+    const dim3 b(256), R((unsigned)p.rows), R4(((unsigned)p.rows + 3) / 4);
     if (nvec <= 256 && p.rows >= 1024) {
-        const dim3 g((R + 3) / 4);
-        if (nvec <= 64) MOE_LAUNCH(kid, stream, (norm_vec_kernel<64, 1, NORM>), g, b, 0, stream, p);
-        else if (nvec <= 128) MOE_LAUNCH(kid, stream, (norm_vec_kernel<64, 2, NORM>), g, b, 0, stream, p);
-        else MOE_LAUNCH(kid, stream, (norm_vec_kernel<64, 4, NORM>), g, b, 0, stream, p);
-    } else if (nvec <= 256) MOE_LAUNCH(kid, stream, (norm_vec_kernel<256, 1, NORM>), dim3(R), b, 0, stream, p);
-    else if (nvec <= 512) MOE_LAUNCH(kid, stream, (norm_vec_kernel<256, 2, NORM>), dim3(R), b, 0, stream, p);
-    else if (nvec <= 1024) MOE_LAUNCH(kid, stream, (norm_vec_kernel<256, 4, NORM>), dim3(R), b, 0, stream, p);
-    else MOE_LAUNCH(kid, stream, (norm_vec_kernel<256, 8, NORM>), dim3(R), b, 0, stream, p);
+        if (nvec <= 64) MOE_LAUNCH(kid, stream, (norm_vec_kernel<64, 1, NORM, SHIFT>), R4, b, 0, stream, p);
+        else if (nvec <= 128) MOE_LAUNCH(kid, stream, (norm_vec_kernel<64, 2, NORM, SHIFT>), R4, b, 0, stream, p);
+        else MOE_LAUNCH(kid, stream, (norm_vec_kernel<64, 4, NORM, SHIFT>), R4, b, 0, stream, p);
+    } else if (nvec <= 256) MOE_LAUNCH(kid, stream, (norm_vec_kernel<256, 1, NORM, SHIFT>), R, b, 0, stream, p);
+    else if (nvec <= 512) MOE_LAUNCH(kid, stream, (norm_vec_kernel<256, 2, NORM, SHIFT>), R, b, 0, stream, p);
+    else if (nvec <= 1024) MOE_LAUNCH(kid, stream, (norm_vec_kernel<256, 4, NORM, SHIFT>), R, b, 0, stream, p);
+    else MOE_LAUNCH(kid, stream, (norm_vec_kernel<256, 8, NORM, SHIFT>), R, b, 0, stream, p);
+    return hipGetLastError();
+}
+
+template <bool NORM>
+static hipError_t launch_rows(const NormArgs& p, bool aligned, int kid, hipStream_t stream) {
+    const int nvec = (p.cols + 14) / 8;                          // vectors of a shifted row at most
+    if (aligned && p.cols % 8 == 0) return launch_vec<NORM, false>(p, p.cols / 8, kid, stream);
+    if (aligned && nvec <= 2048) return launch_vec<NORM, true>(p, nvec, kid, stream);
+    const dim3 b(256), R((unsigned)p.rows);
+    if (p.cols <= 2048) MOE_LAUNCH(kid, stream, (norm_elem_kernel<8, NORM>), R, b, 0, stream, p);
+    else MOE_LAUNCH(kid, stream, (norm_elem_kernel<64, NORM>), R, b, 0, stream, p);
     return hipGetLastError();
 }
 
 hipError_t launch_norm(const uint16_t* x, const uint16_t* res, const float* w, float eps, int rows, int cols, int qmode,
-                       uint16_t* sum, uint16_t* y, uint8_t* codes, void* scales, bool vec, hipStream_t stream) {
-    return launch_rows<true>(NormArgs{x, res, w, eps, rows, cols, qmode, sum, y, codes, scales}, vec, K_NORM, stream);
+                       uint16_t* sum, uint16_t* y, uint8_t* codes, void* scales, bool aligned, hipStream_t stream) {
+    return launch_rows<true>(NormArgs{x, res, w, eps, rows, cols, qmode, sum, y, codes, scales, 1.0 / cols}, aligned, K_NORM, stream);
 }
 
-hipError_t launch_quant_rows(const uint16_t* x, int rows, int cols, int8_t* codes, float* scales, bool vec,
+hipError_t launch_quant_rows(const uint16_t* x, int rows, int cols, int8_t* codes, float* scales, bool aligned,
                              hipStream_t stream) {
     return launch_rows<false>(NormArgs{x, nullptr, nullptr, 0.f, rows, cols, MOE_Q_I8_ROW, nullptr, nullptr,
-                                       (uint8_t*)codes, scales}, vec, K_QUANT_ROWS, stream);
+                                       (uint8_t*)codes, scales, 1.0 / cols}, aligned, K_QUANT_ROWS, stream);
+}
+
+hipError_t launch_dequant_rows(const uint8_t* codes, const void* scales, int rows, int cols, int qmode, uint16_t* out,
+                               bool vec, hipStream_t stream) {
+    const size_t n = (size_t)rows * cols;
+    const dim3 g((unsigned)((n + (vec ? 2047 : 255)) / (vec ? 2048 : 256))), b(256);
+    if (qmode == MOE_Q_FP8_G128_POW2)
+        MOE_LAUNCH(K_DEQUANT_ROWS, stream, (dequant_rows_kernel<MOE_Q_FP8_G128_POW2, false>), g, b, 0, stream, codes, scales, cols, n, out);
+    else if (vec)
+        MOE_LAUNCH(K_DEQUANT_ROWS, stream, (dequant_rows_kernel<MOE_Q_I8_ROW, false>), g, b, 0, stream, codes, scales, cols, n, out);
+    else
+        MOE_LAUNCH(K_DEQUANT_ROWS, stream, (dequant_rows_kernel<MOE_Q_I8_ROW, true>), g, b, 0, stream, codes, scales, cols, n, out);
+    return hipGetLastError();
 }
 
 }  // namespace moe

@@ -82,6 +82,14 @@ def test_norm_host_checks(L):
         assert L.moe_quant_rows(*bad, n) == -1, bad
 
 
+def test_dequant_rows_host_checks(L):
+    f, n, odd = ctypes.c_void_p(0x1000), None, ctypes.c_void_p(0x1008)
+    for bad in ((n, f, 4, 64, 1, f), (f, n, 4, 64, 1, f), (f, f, 4, 64, 1, n), (f, f, 0, 64, 1, f), (f, f, 4, 0, 1, f),
+                (f, f, 4, 16385, 1, f), (f, f, 4, 64, 0, f), (f, f, 4, 64, 3, f), (f, f, 4, 64, 2, f), (odd, f, 4, 128, 2, f),
+                (f, f, 4, 128, 2, odd), (f, f, 1 << 21, 16384, 1, f), (odd, f, 1 << 18, 16384, 1, f)):
+        assert L.moe_dequant_rows(*bad, n) == -1, bad
+
+
 def test_product_host_checks(L):
     f, n, odd = ctypes.c_void_p(0x1000), None, ctypes.c_void_p(0x1008)
     ok = dict(a=f, sa=f, b=f, sb=f, M=4, N=32, K=64, t=0, out=f)
