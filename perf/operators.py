@@ -139,11 +139,6 @@ def _plain_fp8(v):
     return codes, (s + 127).to(torch.uint8)[:, :, 0].contiguous().view(torch.float8_e8m0fnu)
 
 
-def _values(codes, scale):
-    """int8 codes and their row scales -> the values they stand for, in bf16."""
-    return torch.mul(codes, scale[:, None], out=torch.empty(codes.shape, dtype=torch.bfloat16, device=codes.device))
-
-
 def _run_plain(s):
     c = s["case"]
     if c["op"] == "quant":
@@ -181,7 +176,7 @@ def _run_own(s):
     c = s["case"]
     if c["op"] == "quant":
         codes, scale = moe.quant_rows(s["x"])
-        return _values(codes, scale), scale
+        return moe.dequant_rows(codes, scale), scale
     if c["op"] == "norm":
         mode = {"none": moe.Q_NONE, "i8": moe.Q_I8_ROW, "fp8": moe.Q_FP8_G128_POW2}[c["q"]]
         y, total, codes, scale = moe.norm(s["x"], s["w"], EPS, res=s["res"], q_mode=mode, with_y=c["y"])
@@ -191,7 +186,7 @@ def _run_own(s):
         if c["res"]:
             out["sum"] = total
         if c["q"] == "i8":
-            out["q"], out["scale"] = _values(codes, scale), scale
+            out["q"], out["scale"] = moe.dequant_rows(codes, scale), scale
         elif c["q"] == "fp8":
             out["q"], out["scale"] = codes.view(torch.float8_e4m3fn), scale.view(torch.float8_e8m0fnu)
         return out
