@@ -460,13 +460,14 @@ def _arg(t, shape, dtype, dev, name):
     return t.data_ptr()
 
 
-def _matrix(t, name):
-    """(rows, cols, device index) of a non-empty matrix in device memory."""
+def _matrix(t, dtype, name):
+    """(rows, cols, device index, address) of a non-empty contiguous matrix in device memory."""
     dev = t.get_device()
-    if t.dim() != 2 or not t.numel() or dev < 0:
-        raise MoeError(f"{name} must be a non-empty matrix on the device, got shape {tuple(t.shape)} on {t.device}")
+    if dev < 0 or t.dtype != dtype or t.dim() != 2 or not t.is_contiguous() or not t.numel():
+        raise MoeError(f"{name} must be a non-empty contiguous {dtype} matrix on the device, "
+                       f"got {t.dtype} {tuple(t.shape)} on {t.device}")
     rows, cols = t.shape
-    return rows, cols, dev
+    return rows, cols, dev, t.data_ptr()
 
 
 def _launch(dev, fn, *args):
@@ -494,23 +495,30 @@ def norm(x, weight=None, eps=1e-6, res=None, q_mode=Q_NONE, with_y=True, sum=Non
     if stream is not None:
         return _on(stream, norm, x, weight, eps, res, q_mode, with_y, sum, y, codes, scales)
     import torch
-    T, H, dev = _matrix(x, "x")
-    shape, bf = (T, H), torch.bfloat16
+    bf = torch.bfloat16
+    T, H, dev, px = _matrix(x, bf, "x")
+    shape = (T, H)
     if not with_y:
-        y = None
+        y = py = None
     elif y is None:
         y = torch.empty_like(x)
+        py = y.data_ptr()
+    else:
+        py = _arg(y, shape, bf, dev, "y")
     if res is not None and sum is None:
         sum = torch.empty_like(x)
-    ct, ss, sd = torch.int8, (T,), torch.float32
+    pc = ps = None
     if q_mode != Q_NONE:
+        ct, ss, sd = torch.int8, (T,), torch.float32
         if q_mode == Q_FP8_G128_POW2:
             ct, ss, sd = torch.uint8, (T, H // 128), torch.uint8
         codes = x.new_empty(shape, dtype=ct) if codes is None else codes
         scales = x.new_empty(ss, dtype=sd) if scales is None else scales
-    _launch(dev, lib().moe_norm, _arg(x, shape, bf, dev, "x"), _arg(res, shape, bf, dev, "res"),
-            _arg(weight, (H,), torch.float32, dev, "weight"), eps, T, H, q_mode, _arg(sum, shape, bf, dev, "sum"),
-            _arg(y, shape, bf, dev, "y"), _arg(codes, shape, ct, dev, "codes"), _arg(scales, ss, sd, dev, "scales"))
+        pc, ps = _arg(codes, shape, ct, dev, "codes"), _arg(scales, ss, sd, dev, "scales")
+    elif codes is not None or scales is not None:
+        raise MoeError("codes and scales are written only with a q_mode")
+    _launch(dev, lib().moe_norm, px, _arg(res, shape, bf, dev, "res"), _arg(weight, (H,), torch.float32, dev, "weight"),
+            eps, T, H, q_mode, _arg(sum, shape, bf, dev, "sum"), py, pc, ps)
     return y, sum, codes, scales
 
 
@@ -519,11 +527,11 @@ def quant_rows(x, codes=None, scales=None, stream=None):
     if stream is not None:
         return _on(stream, quant_rows, x, codes, scales)
     import torch
-    T, H, dev = _matrix(x, "x")
+    T, H, dev, px = _matrix(x, torch.bfloat16, "x")
     codes = x.new_empty((T, H), dtype=torch.int8) if codes is None else codes
     scales = x.new_empty((T,), dtype=torch.float32) if scales is None else scales
-    _launch(dev, lib().moe_quant_rows, _arg(x, (T, H), torch.bfloat16, dev, "x"), T, H,
-            _arg(codes, (T, H), torch.int8, dev, "codes"), _arg(scales, (T,), torch.float32, dev, "scales"))
+    _launch(dev, lib().moe_quant_rows, px, T, H, _arg(codes, (T, H), torch.int8, dev, "codes"),
+            _arg(scales, (T,), torch.float32, dev, "scales"))
     return codes, scales
 
 
@@ -533,14 +541,18 @@ def dequant_rows(codes, scales, out=None, stream=None):
     if stream is not None:
         return _on(stream, dequant_rows, codes, scales, out)
     import torch
-    T, H, dev = _matrix(codes, "codes")
-    out = codes.new_empty((T, H), dtype=torch.bfloat16) if out is None else out
     if codes.dtype == torch.int8:
+        T, H, dev, pc = _matrix(codes, torch.int8, "codes")
         mode, ss, sd = Q_I8_ROW, (T,), torch.float32
     else:
+        T, H, dev, pc = _matrix(codes, torch.uint8, "codes")
         mode, ss, sd = Q_FP8_G128_POW2, (T, H // 128), torch.uint8
-    _launch(dev, lib().moe_dequant_rows, _arg(codes, (T, H), torch.int8 if mode == Q_I8_ROW else torch.uint8, dev, "codes"),
-            _arg(scales, ss, sd, dev, "scales"), T, H, mode, _arg(out, (T, H), torch.bfloat16, dev, "out"))
+    if out is None:
+        out = codes.new_empty((T, H), dtype=torch.bfloat16)
+        po = out.data_ptr()
+    else:
+        po = _arg(out, (T, H), torch.bfloat16, dev, "out")
+    _launch(dev, lib().moe_dequant_rows, pc, _arg(scales, ss, sd, dev, "scales"), T, H, mode, po)
     return out
 
 
@@ -551,17 +563,22 @@ def gemm_i8(a, sa, b, sb, bias=None, add=None, out=None, out_dtype=None, stream=
     if stream is not None:
         return _on(stream, gemm_i8, a, sa, b, sb, bias, add, out, out_dtype)
     import torch
-    M, K, dev = _matrix(a, "a")
-    N, i8, f32 = _matrix(b, "b")[0], torch.int8, torch.float32
+    i8, f32 = torch.int8, torch.float32
+    M, K, dev, pa = _matrix(a, i8, "a")
+    N, Kb, devb, pb = _matrix(b, i8, "b")
+    if Kb != K or devb != dev:
+        raise MoeError(f"a {tuple(a.shape)} on {a.device} and b {tuple(b.shape)} on {b.device} do not fit")
     ot = out_dtype if out_dtype is not None else torch.bfloat16 if out is None else out.dtype
     if ot != torch.bfloat16 and ot != f32:
         raise MoeError(f"out must be bfloat16 or float32, got {ot}")
     if out is None:
         out = a.new_empty((M, N), dtype=ot)
-    _launch(dev, lib().moe_gemm_i8, _arg(a, (M, K), i8, dev, "a"), _arg(sa, (M,), f32, dev, "sa"),
-            _arg(b, (N, K), i8, dev, "b"), _arg(sb, (N,), f32, dev, "sb"), _arg(bias, (N,), f32, dev, "bias"),
-            _arg(add, (M, N), ot, dev, "add"), M, N, K, OUT_F32 if ot == f32 else OUT_BF16,
-            _arg(out, (M, N), ot, dev, "out"))
+        po = out.data_ptr()
+    else:
+        po = _arg(out, (M, N), ot, dev, "out")
+    _launch(dev, lib().moe_gemm_i8, pa, _arg(sa, (M,), f32, dev, "sa"), pb, _arg(sb, (N,), f32, dev, "sb"),
+            _arg(bias, (N,), f32, dev, "bias"), _arg(add, (M, N), ot, dev, "add"), M, N, K,
+            OUT_F32 if ot == f32 else OUT_BF16, po)
     return out
 
 
@@ -571,15 +588,19 @@ def glu_i8(a, sa, w13, s13, out=None, stream=None):
     if stream is not None:
         return _on(stream, glu_i8, a, sa, w13, s13, out)
     import torch
-    M, K, dev = _matrix(a, "a")
-    N, i8, f32 = _matrix(w13, "w13")[0], torch.int8, torch.float32
-    if N % 2:
-        raise MoeError(f"w13 holds gate and up rows, as many of each: got {N} rows")
+    i8, f32 = torch.int8, torch.float32
+    M, K, dev, pa = _matrix(a, i8, "a")
+    N, Kw, devw, pw = _matrix(w13, i8, "w13")
+    if N % 2 or Kw != K or devw != dev:
+        raise MoeError(f"w13 holds as many gate as up rows, as long as a's and beside them: "
+                       f"a {tuple(a.shape)} on {a.device}, w13 {tuple(w13.shape)} on {w13.device}")
     I = N // 2
-    out = a.new_empty((M, I), dtype=torch.bfloat16) if out is None else out
-    _launch(dev, lib().moe_glu_i8, _arg(a, (M, K), i8, dev, "a"), _arg(sa, (M,), f32, dev, "sa"),
-            _arg(w13, (N, K), i8, dev, "w13"), _arg(s13, (N,), f32, dev, "s13"), M, I, K,
-            _arg(out, (M, I), torch.bfloat16, dev, "out"))
+    if out is None:
+        out = a.new_empty((M, I), dtype=torch.bfloat16)
+        po = out.data_ptr()
+    else:
+        po = _arg(out, (M, I), torch.bfloat16, dev, "out")
+    _launch(dev, lib().moe_glu_i8, pa, _arg(sa, (M,), f32, dev, "sa"), pw, _arg(s13, (N,), f32, dev, "s13"), M, I, K, po)
     return out
 
 

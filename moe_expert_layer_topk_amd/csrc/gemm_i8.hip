@@ -37,7 +37,13 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     typedef __bf16 b2 __attribute__((ext_vector_type(2)));
     return __builtin_bit_cast(uint32_t, __builtin_convertvector((f2){a, b}, b2));
 }
-__device__ __forceinline__ float glu_h(float g, float u) { return g / (1.0f + __expf(-g)) * u; }
+// silu(g) u; the hardware's base-2 exponential and reciprocal are within one
+// step of fp32 each (the correctly rounded division costs ten instructions more
+// in an epilogue that no matrix instruction hides: gated 16384 x 512 x 2048
+// 37.2 us with it)
+__device__ __forceinline__ float glu_h(float g, float u) {
+    return g * u * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269504088896341f));
+}
 
 // Workgroup barrier that waits for the wave's LDS traffic only (the fence of
 // __syncthreads() would drain the direct-to-LDS loads in flight).
@@ -48,39 +54,45 @@ static __device__ __forceinline__ void barrier_lds() {
     asm volatile("" ::: "memory");
 }
 
-// NC adjacent output columns of one row from column col on. VEC: all of them
-// exist or none (N % NC == 0) and their address is a multiple of their size
-// (up to 16 bytes); otherwise one by one. The aligned accesses are 16 bytes
-// where NC allows.
-template <int NC, bool F32, bool ADD>
-__device__ __forceinline__ void store_vec(const GemmArgs& p, size_t o, float (&v)[NC]) {
-    if constexpr (F32) {
-        constexpr int W = NC < 4 ? NC : 4;
-        typedef float fW __attribute__((ext_vector_type(W)));
+// NC adjacent output columns of one row. VEC: all of them exist or none (N %
+// NC == 0) and their address is a multiple of their size (up to 16 bytes);
+// otherwise one by one. Outputs are written once and not read here: stored
+// past the caches' order of use, so that a launch does not end by writing back
+// what its last tiles left in L2 (16384 x 2048 x 512 with the addend 45 -> 35
+// us, gated 16384 x 512 x 2048 35.0 -> 33.5, others the same).
+template <int NC, bool F32>
+struct Cols {
+    typedef uint32_t word __attribute__((ext_vector_type(NC == 2 && !F32 ? 1 : NC * (F32 ? 4 : 2) / 4 < 4 ? NC * (F32 ? 4 : 2) / 4 : 4)));
+    static constexpr int W = sizeof(word) / 4;                   // dwords of an access
+    static constexpr int NW = NC * (F32 ? 4 : 2) / (4 * W);      // accesses
+    word w[NW];
+    __device__ __forceinline__ void load(const void* p, size_t o) {
+        const word* q = (const word*)((const uint8_t*)p + o * (F32 ? 4 : 2));
 #pragma unroll
-        for (int h = 0; h < NC / W; ++h) {
-            fW x;
+        for (int h = 0; h < NW; ++h) w[h] = q[h];
+    }
+    __device__ __forceinline__ void add_to(float (&v)[NC]) const {
 #pragma unroll
-            for (int n = 0; n < W; ++n) x[n] = v[W * h + n];
-            if (ADD) x += *(const fW*)((const float*)p.add + o + W * h);
-            *(fW*)((float*)p.out + o + W * h) = x;
-        }
-    } else {
-        typedef uint32_t uW __attribute__((ext_vector_type(NC / 2)));
-        uW w;
-        if (ADD) {
-            w = *(const uW*)((const uint16_t*)p.add + o);
-#pragma unroll
-            for (int h = 0; h < NC / 2; ++h) {
-                v[2 * h] += __uint_as_float(w[h] << 16);
-                v[2 * h + 1] += __uint_as_float(w[h] & 0xFFFF0000u);
+        for (int n = 0; n < NC; ++n) {
+            if (F32) v[n] += __uint_as_float(w[n / W][n % W]);
+            else {
+                const uint32_t d = w[n / 2 / W][n / 2 % W];
+                v[n] += __uint_as_float(n & 1 ? d & 0xFFFF0000u : d << 16);
             }
         }
-#pragma unroll
-        for (int h = 0; h < NC / 2; ++h) w[h] = pack_bf16(v[2 * h], v[2 * h + 1]);
-        *(uW*)((uint16_t*)p.out + o) = w;
     }
-}
+    __device__ __forceinline__ static void store(void* p, size_t o, const float (&v)[NC]) {
+        Cols c;
+#pragma unroll
+        for (int d = 0; d < NW * W; ++d) {
+            if (F32) c.w[d / W][d % W] = __float_as_uint(v[d]);
+            else c.w[d / W][d % W] = pack_bf16(v[2 * d], v[2 * d + 1]);
+        }
+        word* q = (word*)((uint8_t*)p + o * (F32 ? 4 : 2));
+#pragma unroll
+        for (int h = 0; h < NW; ++h) __builtin_nontemporal_store(c.w[h], q + h);
+    }
+};
 template <int NC, bool F32>
 __device__ __forceinline__ void store_each(const GemmArgs& p, int row, int col, float (&v)[NC]) {
     const size_t o = (size_t)row * p.N + col;
@@ -272,8 +284,21 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gemm_tile_kernel(GemmArgs p, 
 #pragma unroll
         for (int a = 0; a < MF; ++a) {
             const f32x4 sa = *(const f32x4*)(md + 16 * (mw * MF + a) + 4 * q);
+            // the addends of NB rows are loaded together (rows and columns past
+            // the output: from inside it, and dropped)
+            constexpr int NB = F32 ? 2 : 4;
+            Cols<NC, F32> plus[KIND == 1 ? NB : 1];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
+                if constexpr (KIND == 1) {
+                    if (i % NB == 0) {
+#pragma unroll
+                        for (int b = 0; b < NB; ++b) {
+                            const int row = min(row0 + 16 * (mw * MF + a) + 4 * q + i + b, p.M - 1);
+                            plus[b].load(p.add, (size_t)row * p.N + (col < p.N ? col : 0));
+                        }
+                    }
+                }
                 const int row = row0 + 16 * (mw * MF + a) + 4 * q + i;
                 float v[NC];
 #pragma unroll
@@ -284,7 +309,17 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gemm_tile_kernel(GemmArgs p, 
                 if constexpr (KIND == 2) {
                     if (row < p.M) store_each<NC, F32>(p, row, col, v);
                 } else {
-                    if (row < p.M && col < p.N) store_vec<NC, F32, KIND == 1>(p, (size_t)row * p.N + col, v);
+                    if constexpr (KIND == 1) {
+                        plus[i % NB].add_to(v);
+                        // used outside the masked store: otherwise the wait for
+                        // the addends sinks into it, and where no lane stores
+                        // they stay in flight and the step loop waits, every
+                        // step, before it reuses their registers (226 -> 242 us
+                        // at 4096 x 8192 x 8192, which has no addend)
+#pragma unroll
+                        for (int n = 0; n < NC; ++n) asm volatile("" : "+v"(v[n]));
+                    }
+                    if (row < p.M && col < p.N) Cols<NC, F32>::store(p.out, (size_t)row * p.N + col, v);
                 }
             }
         }
@@ -461,8 +496,12 @@ __global__ void __launch_bounds__(64 * WK) gemm_split_kernel(GemmArgs p, int til
         if (!p.vec) store_each<4, F32>(p, row0 + r, col0 + c, v);
         else if (col0 + c < p.N) {
             const size_t o = (size_t)(row0 + r) * p.N + col0 + c;
-            if (!GLU && p.add) store_vec<4, F32, true>(p, o, v);
-            else store_vec<4, F32, false>(p, o, v);
+            if (!GLU && p.add) {
+                Cols<4, F32> plus;
+                plus.load(p.add, o);
+                plus.add_to(v);
+            }
+            Cols<4, F32>::store(p.out, o, v);
         }
     }
 }
