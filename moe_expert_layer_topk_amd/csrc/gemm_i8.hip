@@ -369,14 +369,15 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gemm_tile_kernel(GemmArgs p, 
 // tile (a 64 x 64 tile in four 32 x 32 quarters), and their int32 sums meet in
 // LDS (the ring's memory, free by then), where the epilogue takes them in row
 // order.
-template <int TM, int TN, int WK, int BK, int R, bool GLU, bool F32>
+template <int TM, int TN, int WK, int R, bool GLU, bool F32>
 __global__ void __launch_bounds__(64 * WK) gemm_split_kernel(GemmArgs p, int tiles_m, int tiles_n) {
     constexpr int MF = TM / 32, NF = TN / 32;
+    constexpr int BK = 32 * WK;                                  // a step: one sub-step for each wave
     constexpr int SEG = BK / 128;                                // 128-byte segments of a step, each a block of rows
     constexpr int STAGE = (TM + TN) * BK;
     constexpr int LD = (TM + TN) * SEG / 8 / WK;                 // 8-row loads per wave and step
     constexpr int OUTN = GLU ? TN / 2 : TN;
-    static_assert((TM + TN) * SEG % (8 * WK) == 0 && (BK / 32) % WK == 0 && WK * TM * TN * 4 <= R * STAGE, "tile");
+    static_assert(BK % 128 == 0 && (TM + TN) * SEG % (8 * WK) == 0 && WK * TM * TN * 4 <= R * STAGE, "tile");
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
     float* s_sa = (float*)(smem + R * STAGE);
     float* s_sb = s_sa + 64 * ((TM + 63) / 64);
@@ -432,7 +433,7 @@ __global__ void __launch_bounds__(64 * WK) gemm_split_kernel(GemmArgs p, int til
         if (!GLU && p.bias) lds_dma4(p.bias + n, (uint8_t*)(s_bias + 64 * i));
     }
 #pragma unroll
-    for (int s = 0; s < R - 1; ++s) fill(s);
+    for (int s = 0; s < R; ++s) fill(s);
 
     i32x16 acc[MF][NF];
 #pragma unroll
@@ -441,27 +442,38 @@ __global__ void __launch_bounds__(64 * WK) gemm_split_kernel(GemmArgs p, int til
         for (int n = 0; n < NF; ++n)
 #pragma unroll
             for (int i = 0; i < 16; ++i) acc[a][n][i] = 0;
-    const int m = lane & 31, hi = lane >> 5, sw = (m >> 1) & 7;
-    for (int s = 0; s < S; ++s) {
+    const int m = lane & 31, hi = lane >> 5;
+    const int lo = (wv / 4) * (TM + TN) * 128 + m * 128 + (((2 * (wv & 3) + hi) ^ ((m >> 1) & 7)) << 4);
+    i32x4 fa[2][MF], fb[2][NF];
+    auto read = [&](int s, int u) __attribute__((always_inline)) {
+        const uint8_t* sg = smem + (s % R) * STAGE + lo;
+#pragma unroll
+        for (int a = 0; a < MF; ++a) fa[u][a] = *(const i32x4*)(sg + a * 4096);
+#pragma unroll
+        for (int n = 0; n < NF; ++n) fb[u][n] = *(const i32x4*)(sg + TM * 128 + n * 4096);
+    };
+    // step s is in register set u: past the barrier its stage is free for step
+    // s + R, and step s + 1, which has landed, goes to the other set while s is
+    // multiplied
+    auto step = [&](int s, int u) __attribute__((always_inline)) {
         wait_vmcnt<(R - 2) * LD>();
         barrier_lds();
-        fill(s + R - 1);
-        const uint8_t* st = smem + (s % R) * STAGE;
+        read(s + 1, u ^ 1);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int i = 0; i < BK / 32 / WK; ++i) {
-            const int ks = wv + i * WK;
-            const uint8_t* sg = st + (ks / 4) * (TM + TN) * 128 + m * 128 + (((2 * (ks & 3) + hi) ^ sw) << 4);
-            i32x4 fa[MF], fb[NF];
+        for (int a = 0; a < MF; ++a)
 #pragma unroll
-            for (int a = 0; a < MF; ++a) fa[a] = *(const i32x4*)(sg + a * 4096);
-#pragma unroll
-            for (int n = 0; n < NF; ++n) fb[n] = *(const i32x4*)(sg + TM * 128 + n * 4096);
-#pragma unroll
-            for (int a = 0; a < MF; ++a)
-#pragma unroll
-                for (int n = 0; n < NF; ++n)
-                    acc[a][n] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fa[a], fb[n], acc[a][n], 0, 0, 0);
-        }
+            for (int n = 0; n < NF; ++n)
+                acc[a][n] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fa[u][a], fb[u][n], acc[a][n], 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+        fill(s + R);
+    };
+    wait_vmcnt<(R - 1) * LD>();
+    barrier_lds();
+    read(0, 0);
+    for (int s = 0; s < S; s += 2) {                             // (a step past the end multiplies zeros)
+        step(s, 0);
+        step(s + 1, 1);
     }
     wait_vmcnt<0>();                                             // the last fills land before their memory is reused
     barrier_lds();
@@ -535,32 +547,40 @@ static hipError_t launch_tile(GemmArgs p, int kid, hipStream_t stream) {
     return hipGetLastError();
 }
 
-template <int TM, int TN, int WK, int BK, int R, bool GLU, bool F32>
+template <int TM, int TN, int WK, int R, bool GLU, bool F32>
 static hipError_t launch_split(GemmArgs p, int kid, hipStream_t stream) {
     constexpr int OUTN = GLU ? TN / 2 : TN;
-    constexpr int SMEM = R * (TM + TN) * BK + 256 * ((TM + 63) / 64 + 2 * ((TN + 63) / 64));
+    constexpr int SMEM = R * (TM + TN) * 32 * WK + 256 * ((TM + 63) / 64 + 2 * ((TN + 63) / 64));
     static std::atomic<uint64_t> done{0};
-    const hipError_t e = allow_lds((const void*)gemm_split_kernel<TM, TN, WK, BK, R, GLU, F32>, SMEM, done);
+    const hipError_t e = allow_lds((const void*)gemm_split_kernel<TM, TN, WK, R, GLU, F32>, SMEM, done);
     if (e != hipSuccess) return e;
     p.vec = p.vec && p.N % 4 == 0;
     const int tm = (p.M + TM - 1) / TM, tn = (p.N + OUTN - 1) / OUTN;
-    MOE_LAUNCH(kid, stream, (gemm_split_kernel<TM, TN, WK, BK, R, GLU, F32>), dim3((unsigned)(tm * tn)), dim3(64 * WK),
+    MOE_LAUNCH(kid, stream, (gemm_split_kernel<TM, TN, WK, R, GLU, F32>), dim3((unsigned)(tm * tn)), dim3(64 * WK),
                SMEM, stream, p, tm, tn);
     return hipGetLastError();
 }
 
-// The tile shapes, and what a K step of 128 costs them (us, measured on
-// products whose operands come from L2): `one` with at most one workgroup on
-// each CU, `full` with all `per_cu` of them; `round` is a round's prologue and
-// epilogue. Large tiles move fewer bytes per output, small ones reach more CUs.
+// The tile shapes, and what they cost (us): a K step of 128 with at most one
+// workgroup on each CU (`one`) and with all `per_cu` of them (`full`), and a
+// round's prologue and epilogue (`round`). Large tiles move fewer bytes per
+// output, small ones reach more CUs. The figures are a fit to 400 products
+// with random sizes (1..16384 rows, 64..8192 columns, K 128..8192), each timed
+// with every shape: the shape picked by them is 1.8% slower than the best of
+// the five on average. E.g. 333 x 1000 x 4112: 32x64 9.6 us, 128x128 26;
+// 2048^3: 128x128 16 us, 256x256 26, 64x64 23; 16384 x 2048 x 2048: 256x256 64
+// us, 128x128 73. 256x128, 128x64 and 64x32 tiles were measured beside these
+// and gain less than 1% together.
 struct Shape {
     int tm, tn, per_cu;
     float one, full, round;
 };
-enum { S_256x256, S_256x128, S_128x128, S_64x64, S_64x32, S_32x32, S_COUNT };
-static const Shape kShapes[S_COUNT] = {{256, 256, 1, 1.45f, 1.45f, 3.0f}, {256, 128, 1, 0.80f, 0.80f, 1.8f},
-                                       {128, 128, 2, 0.70f, 0.99f, 1.2f}, {64, 64, 2, 0.23f, 0.46f, 0.6f},
-                                       {64, 32, 1, 0.13f, 0.13f, 0.6f},   {32, 32, 2, 0.07f, 0.23f, 0.4f}};
+enum { S_256x256, S_128x128, S_64x64, S_32x64, S_32x32, S_COUNT };
+static const Shape kShapes[S_COUNT] = {{256, 256, 1, 1.17f, 1.17f, 2.6f},
+                                       {128, 128, 2, 0.43f, 0.79f, 0.7f},
+                                       {64, 64, 2, 0.16f, 0.38f, 0.9f},
+                                       {32, 64, 1, 0.16f, 0.16f, 0.8f},
+                                       {32, 32, 2, 0.03f, 0.23f, 1.0f}};
 
 // The shape that the costs above make the fastest for this many output rows
 // and B rows.
@@ -587,11 +607,10 @@ template <bool GLU, bool F32>
 static hipError_t launch_any(const GemmArgs& p, int kid, hipStream_t stream) {
     switch (pick_shape(p.M, (long long)p.N * (GLU ? 2 : 1), p.K)) {
         case S_256x256: return launch_tile<256, 256, 4, 2, 2, GLU, F32>(p, kid, stream);
-        case S_256x128: return launch_tile<256, 128, 4, 2, 3, GLU, F32>(p, kid, stream);
         case S_128x128: return launch_tile<128, 128, 2, 2, 2, GLU, F32>(p, kid, stream);
-        case S_64x64: return launch_split<64, 64, 4, 128, 4, GLU, F32>(p, kid, stream);
-        case S_64x32: return launch_split<64, 32, 8, 256, 4, GLU, F32>(p, kid, stream);
-        default: return launch_split<32, 32, 8, 256, 4, GLU, F32>(p, kid, stream);
+        case S_64x64: return launch_split<64, 64, 4, 4, GLU, F32>(p, kid, stream);
+        case S_32x64: return launch_split<32, 64, 8, 4, GLU, F32>(p, kid, stream);
+        default: return launch_split<32, 32, 8, 4, GLU, F32>(p, kid, stream);
     }
 }
 
