@@ -436,8 +436,27 @@ def quant_act(x, codes=None, exps=None, stream=None):
 
 
 # ---------------------------------------------------------------- norm, int8 products
-# Small calls of these are bound by the host, so each argument is looked at
-# once and the addresses go to the library as plain integers.
+# Small calls of these are bound by the host: their tensors are looked at,
+# their outputs allocated and the C ABI called in _marshal.so (csrc/marshal.cpp),
+# on the current stream of the tensors' device.
+_marshal = None
+
+
+def _load_marshal():
+    """The loaded marshalling module (raises if it has not been built)."""
+    global _marshal
+    if _marshal is None:
+        lib()                                  # torch and libmoe first: the module binds to both
+        try:
+            from . import _marshal as m
+        except ImportError as e:
+            raise MoeError(f"_marshal.so does not load ({e}): build it with __graft_entry__.build() "
+                           "(python -m moe_expert_layer_topk_amd.build)") from e
+        m.set_error(MoeError)
+        _marshal = m
+    return _marshal
+
+
 def _on(stream, f, *args):
     """f(*args) with `stream` as the current stream, so that what f allocates
     (outputs, intermediates freed when it returns) belongs to that stream too
@@ -448,39 +467,6 @@ def _on(stream, f, *args):
             raise MoeError(f"the stream is on {stream.device}, a tensor on {t.device}")
     with torch.cuda.stream(stream):
         return f(*args)
-
-
-def _arg(t, shape, dtype, dev, name):
-    """Address of a contiguous tensor of exactly this shape and type on device `dev` (None passes)."""
-    if t is None:
-        return None
-    if t.shape != shape or t.dtype != dtype or not t.is_contiguous() or t.get_device() != dev:
-        raise MoeError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on device {dev}, "
-                       f"got {t.dtype} {tuple(t.shape)} on {t.device}")
-    return t.data_ptr()
-
-
-def _matrix(t, dtype, name):
-    """(rows, cols, device index, address) of a non-empty contiguous matrix in device memory."""
-    dev = t.get_device()
-    if dev < 0 or t.dtype != dtype or t.dim() != 2 or not t.is_contiguous() or not t.numel():
-        raise MoeError(f"{name} must be a non-empty contiguous {dtype} matrix on the device, "
-                       f"got {t.dtype} {tuple(t.shape)} on {t.device}")
-    rows, cols = t.shape
-    return rows, cols, dev, t.data_ptr()
-
-
-def _launch(dev, fn, *args):
-    """fn(*args, stream) on the current stream of device `dev`, with `dev` as the current device."""
-    import torch
-    stream = torch._C._cuda_getCurrentRawStream(dev)
-    if torch.cuda.current_device() == dev:
-        status = fn(*args, stream)
-    else:
-        with torch.cuda.device(dev):
-            status = fn(*args, stream)
-    if status != MOE_OK:
-        _check(status)
 
 
 def norm(x, weight=None, eps=1e-6, res=None, q_mode=Q_NONE, with_y=True, sum=None, y=None, codes=None, scales=None,
@@ -494,45 +480,14 @@ def norm(x, weight=None, eps=1e-6, res=None, q_mode=Q_NONE, with_y=True, sum=Non
     Outputs not passed are allocated; sum and y may be x or res themselves."""
     if stream is not None:
         return _on(stream, norm, x, weight, eps, res, q_mode, with_y, sum, y, codes, scales)
-    import torch
-    bf = torch.bfloat16
-    T, H, dev, px = _matrix(x, bf, "x")
-    shape = (T, H)
-    if not with_y:
-        y = py = None
-    elif y is None:
-        y = torch.empty_like(x)
-        py = y.data_ptr()
-    else:
-        py = _arg(y, shape, bf, dev, "y")
-    if res is not None and sum is None:
-        sum = torch.empty_like(x)
-    pc = ps = None
-    if q_mode != Q_NONE:
-        ct, ss, sd = torch.int8, (T,), torch.float32
-        if q_mode == Q_FP8_G128_POW2:
-            ct, ss, sd = torch.uint8, (T, H // 128), torch.uint8
-        codes = x.new_empty(shape, dtype=ct) if codes is None else codes
-        scales = x.new_empty(ss, dtype=sd) if scales is None else scales
-        pc, ps = _arg(codes, shape, ct, dev, "codes"), _arg(scales, ss, sd, dev, "scales")
-    elif codes is not None or scales is not None:
-        raise MoeError("codes and scales are written only with a q_mode")
-    _launch(dev, lib().moe_norm, px, _arg(res, shape, bf, dev, "res"), _arg(weight, (H,), torch.float32, dev, "weight"),
-            eps, T, H, q_mode, _arg(sum, shape, bf, dev, "sum"), py, pc, ps)
-    return y, sum, codes, scales
+    return (_marshal or _load_marshal()).norm(x, weight, eps, res, q_mode, with_y, sum, y, codes, scales)
 
 
 def quant_rows(x, codes=None, scales=None, stream=None):
     """moe_quant_rows: (int8 codes [rows, cols], fp32 scales [rows]) of the bf16 rows of x."""
     if stream is not None:
         return _on(stream, quant_rows, x, codes, scales)
-    import torch
-    T, H, dev, px = _matrix(x, torch.bfloat16, "x")
-    codes = x.new_empty((T, H), dtype=torch.int8) if codes is None else codes
-    scales = x.new_empty((T,), dtype=torch.float32) if scales is None else scales
-    _launch(dev, lib().moe_quant_rows, px, T, H, _arg(codes, (T, H), torch.int8, dev, "codes"),
-            _arg(scales, (T,), torch.float32, dev, "scales"))
-    return codes, scales
+    return (_marshal or _load_marshal()).quant_rows(x, codes, scales)
 
 
 def dequant_rows(codes, scales, out=None, stream=None):
@@ -540,20 +495,7 @@ def dequant_rows(codes, scales, out=None, stream=None):
     fp32 scale per row or of e4m3 bytes (uint8) with an E8M0 byte per 128 columns."""
     if stream is not None:
         return _on(stream, dequant_rows, codes, scales, out)
-    import torch
-    if codes.dtype == torch.int8:
-        T, H, dev, pc = _matrix(codes, torch.int8, "codes")
-        mode, ss, sd = Q_I8_ROW, (T,), torch.float32
-    else:
-        T, H, dev, pc = _matrix(codes, torch.uint8, "codes")
-        mode, ss, sd = Q_FP8_G128_POW2, (T, H // 128), torch.uint8
-    if out is None:
-        out = codes.new_empty((T, H), dtype=torch.bfloat16)
-        po = out.data_ptr()
-    else:
-        po = _arg(out, (T, H), torch.bfloat16, dev, "out")
-    _launch(dev, lib().moe_dequant_rows, pc, _arg(scales, ss, sd, dev, "scales"), T, H, mode, po)
-    return out
+    return (_marshal or _load_marshal()).dequant_rows(codes, scales, out)
 
 
 def gemm_i8(a, sa, b, sb, bias=None, add=None, out=None, out_dtype=None, stream=None):
@@ -562,24 +504,7 @@ def gemm_i8(a, sa, b, sb, bias=None, add=None, out=None, out_dtype=None, stream=
     and may be out itself."""
     if stream is not None:
         return _on(stream, gemm_i8, a, sa, b, sb, bias, add, out, out_dtype)
-    import torch
-    i8, f32 = torch.int8, torch.float32
-    M, K, dev, pa = _matrix(a, i8, "a")
-    N, Kb, devb, pb = _matrix(b, i8, "b")
-    if Kb != K or devb != dev:
-        raise MoeError(f"a {tuple(a.shape)} on {a.device} and b {tuple(b.shape)} on {b.device} do not fit")
-    ot = out_dtype if out_dtype is not None else torch.bfloat16 if out is None else out.dtype
-    if ot != torch.bfloat16 and ot != f32:
-        raise MoeError(f"out must be bfloat16 or float32, got {ot}")
-    if out is None:
-        out = a.new_empty((M, N), dtype=ot)
-        po = out.data_ptr()
-    else:
-        po = _arg(out, (M, N), ot, dev, "out")
-    _launch(dev, lib().moe_gemm_i8, pa, _arg(sa, (M,), f32, dev, "sa"), pb, _arg(sb, (N,), f32, dev, "sb"),
-            _arg(bias, (N,), f32, dev, "bias"), _arg(add, (M, N), ot, dev, "add"), M, N, K,
-            OUT_F32 if ot == f32 else OUT_BF16, po)
-    return out
+    return (_marshal or _load_marshal()).gemm_i8(a, sa, b, sb, bias, add, out, out_dtype)
 
 
 def glu_i8(a, sa, w13, s13, out=None, stream=None):
@@ -587,21 +512,7 @@ def glu_i8(a, sa, w13, s13, out=None, stream=None):
     of a [M, K] with rows [0, I) and [I, 2I) of w13 [2I, K], scaled."""
     if stream is not None:
         return _on(stream, glu_i8, a, sa, w13, s13, out)
-    import torch
-    i8, f32 = torch.int8, torch.float32
-    M, K, dev, pa = _matrix(a, i8, "a")
-    N, Kw, devw, pw = _matrix(w13, i8, "w13")
-    if N % 2 or Kw != K or devw != dev:
-        raise MoeError(f"w13 holds as many gate as up rows, as long as a's and beside them: "
-                       f"a {tuple(a.shape)} on {a.device}, w13 {tuple(w13.shape)} on {w13.device}")
-    I = N // 2
-    if out is None:
-        out = a.new_empty((M, I), dtype=torch.bfloat16)
-        po = out.data_ptr()
-    else:
-        po = _arg(out, (M, I), torch.bfloat16, dev, "out")
-    _launch(dev, lib().moe_glu_i8, pa, _arg(sa, (M,), f32, dev, "sa"), pw, _arg(s13, (N,), f32, dev, "s13"), M, I, K, po)
-    return out
+    return (_marshal or _load_marshal()).glu_i8(a, sa, w13, s13, out)
 
 
 def shared_expert_i8(a, sa, w13, s13, w2, s2, add=None, out=None, stream=None):

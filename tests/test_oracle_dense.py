@@ -61,6 +61,16 @@ def L():
     return moe.lib()
 
 
+def test_missing_marshal_module_fails_loudly(L, monkeypatch):
+    import sys
+    from moe_expert_layer_topk_amd import binding
+    monkeypatch.setattr(binding, "_marshal", None)
+    monkeypatch.setitem(sys.modules, "moe_expert_layer_topk_amd._marshal", None)
+    monkeypatch.delattr(moe, "_marshal", raising=False)
+    with pytest.raises(moe.MoeError, match="_marshal"):
+        moe.quant_rows(None)
+
+
 def test_norm_host_checks(L):
     f, n, odd = ctypes.c_void_p(0x1000), None, ctypes.c_void_p(0x1002)     # never dereferenced
     ok = dict(x=f, res=n, w=n, eps=1e-6, rows=4, cols=256, q=0, sum=n, y=f, codes=n, scales=n)
@@ -114,7 +124,8 @@ def test_binding_refuses_before_a_launch():
     x = torch.zeros(4, 64, dtype=torch.bfloat16)
     a = torch.zeros(4, 64, dtype=torch.int8)
     s = torch.zeros(4)
-    for call in (lambda: moe.norm(x), lambda: moe.quant_rows(x), lambda: moe.gemm_i8(a, s, a, s),
+    for call in (lambda: moe.norm(None), lambda: moe.norm(3), lambda: moe.gemm_i8(a, s, None, s), lambda: moe.gemm_i8(a, None, a, s),
+                 lambda: moe.norm(x), lambda: moe.quant_rows(x), lambda: moe.dequant_rows(a, s), lambda: moe.dequant_rows(None, s), lambda: moe.gemm_i8(a, s, a, s),
                  lambda: moe.glu_i8(a, s, a, s), lambda: moe.norm(x[0]), lambda: moe.quant_rows(x[:0]),
                  lambda: moe.glu_i8(a, s, a[:3], s[:3])):
         with pytest.raises(moe.MoeError):
