@@ -209,16 +209,18 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gemm_tile_kernel(GemmArgs p, 
             if (!GLU) lds_dma4(p.bias ? p.bias + n : (const float*)g_zero16, (uint8_t*)(md + TM + TN + 64 * i));
         }
     };
-    // load l of the K bytes from k0 on into stage st; chunks at or past kend are zeros
-    auto dma = [&](int k0, int kend, int st, int l) __attribute__((always_inline)) {
+    // load l of the K bytes from k0 on into stage st; in0, in1: whether this
+    // lane's chunk of an even, odd 8-row group lies inside K (else zeros)
+    auto dma = [&](int k0, bool in0, bool in1, int st, int l) __attribute__((always_inline)) {
         const int j = l < LA ? l : 0, i = l < LA ? 0 : l - LA;
         const int r8 = l < LA ? wv * LA + j : wv * LB + i;
         uint32_t o = l < LA ? oA[j] : oB[i];
         asm volatile("" : "+v"(o));
         const uint8_t* src = (l < LA ? bA : bB[i]) + k0 + o;
-        src = k0 + (ch0 ^ (64 * (r8 & 1))) < kend ? src : g_zero16;
+        src = ((l < LA ? j : i) & 1 ? in1 : in0) ? src : g_zero16;
         lds_dma16(src, smem + st * STAGE + (l < LA ? 0 : TM * 128) + 1024 * r8);
     };
+    static_assert(LA % 2 == 0 && LB % 2 == 0, "load j of a wave fills an odd group where j is odd");
 
     // ---- multiply side: lane (m, q) holds 16 K bytes of fragment row m, chunk 4 u + q in sub-step u
     i32x4 acc[MF][NF];
@@ -232,21 +234,26 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gemm_tile_kernel(GemmArgs p, 
     const int lo = (lane & 15) * 128 + (((lane >> 4) ^ ((lane >> 1) & 7)) << 4);
     i32x4 fa[2][MF], fb[2][NF];
     constexpr int NK = MF * NF, NR = MF + NF, NL = LA + LB;
-    // fragment i of sub-step u, in the order the instructions take them
-    auto read = [&](int st, int u, int i) __attribute__((always_inline)) {
+    // this lane's bytes of its wave's first A and B fragment, sub-step u of stage st
+    const int loA = lo + mw * MF * 2048, loB = lo + TM * 128 + nw * NF * 2048;
+    auto frags = [&](int st, int u) __attribute__((always_inline)) {
         int off = st * STAGE;
         asm volatile("" : "+s"(off));
-        const uint8_t* b = smem + off + (lo ^ (64 * u));
-        if (i == 0) fa[u][0] = *(const i32x4*)(b + mw * MF * 2048);
-        else if (i <= NF) fb[u][i - 1] = *(const i32x4*)(b + TM * 128 + (nw * NF + i - 1) * 2048);
-        else fa[u][i - NF] = *(const i32x4*)(b + (mw * MF + i - NF) * 2048);
+        return make_int2((loA ^ (64 * u)) + off, (loB ^ (64 * u)) + off);
+    };
+    // fragment i of sub-step u, in the order the instructions take them
+    auto read = [&](int2 f, int u, int i) __attribute__((always_inline)) {
+        if (i == 0) fa[u][0] = *(const i32x4*)(smem + f.x);
+        else if (i <= NF) fb[u][i - 1] = *(const i32x4*)(smem + f.y + (i - 1) * 2048);
+        else fa[u][i - NF] = *(const i32x4*)(smem + f.x + (i - NF) * 2048);
     };
     // sub-step 0 of a step: multiply, and read sub-step 1 behind the first instructions
     auto half0 = [&](int st) __attribute__((always_inline)) {
+        const int2 f = frags(st, 1);
 #pragma unroll
         for (int k = 0; k < NK; ++k) {
             acc[k / NF][k % NF] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fa[0][k / NF], fb[0][k % NF], acc[k / NF][k % NF], 0, 0, 0);
-            if (k < NR) read(st, 1, k);
+            if (k < NR) read(f, 1, k);
             __builtin_amdgcn_sched_barrier(0);
         }
     };
@@ -256,6 +263,8 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gemm_tile_kernel(GemmArgs p, 
     constexpr int BAR = 2;
     constexpr int LS = (NK - BAR) / NL > 0 ? (NK - BAR) / NL : 1;
     auto half1 = [&](int st, int nx, int k0, int kend) __attribute__((always_inline)) {
+        const int2 f = frags(nx, 0);
+        const bool in0 = k0 + ch0 < kend, in1 = k0 + (ch0 ^ 64) < kend;
 #pragma unroll
         for (int k = 0; k < NK; ++k) {
             acc[k / NF][k % NF] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fa[1][k / NF], fb[1][k % NF], acc[k / NF][k % NF], 0, 0, 0);
@@ -263,8 +272,8 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gemm_tile_kernel(GemmArgs p, 
                 wait_vmcnt<(R - 2) * NL>();                       // (more in flight than that: waits for more)
                 barrier_lds();
             }
-            if (k >= BAR - 1 && k - BAR + 1 < NR) read(nx, 0, k - BAR + 1);
-            if (k >= BAR && (k - BAR) % LS == 0 && (k - BAR) / LS < NL) dma(k0, kend, st, (k - BAR) / LS);
+            if (k >= BAR - 1 && k - BAR + 1 < NR) read(f, 0, k - BAR + 1);
+            if (k >= BAR && (k - BAR) % LS == 0 && (k - BAR) / LS < NL) dma(k0, in0, in1, st, (k - BAR) / LS);
             __builtin_amdgcn_sched_barrier(0);
         }
         static_assert((NK - 1 - BAR) / LS >= NL - 1 && NK - BAR + 1 > NR, "every load and read has its instruction");
@@ -336,12 +345,12 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gemm_tile_kernel(GemmArgs p, 
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int l = 0; l < NL; ++l) dma(128 * r, K, r, l);
+        for (int l = 0; l < NL; ++l) dma(128 * r, 128 * r + ch0 < K, 128 * r + (ch0 ^ 64) < K, r, l);
     zero_acc();
     wait_vmcnt<(R - 1) * NL>();
     barrier_lds();
 #pragma unroll
-    for (int i = 0; i < NR; ++i) read(0, 0, i);
+    for (int i = 0; i < NR; ++i) read(frags(0, 0), 0, i);
     int st = 0, nx = 1;
     for (int j = 0; j < nj; ++j) {
         row0 = row1;
