@@ -128,6 +128,23 @@ struct IC {
     static constexpr int value = V;
 };
 
+// Rows of an operand from a tile's first one on, as a buffer: accesses past its
+// end return nothing.
+struct Operand {
+    const void* p;
+    uint32_t bytes;
+    __device__ __forceinline__ void set(const void* first, size_t n) {
+        p = first;
+        bytes = n > 0xFFFFFFF0ull ? 0xFFFFFFF0u : (uint32_t)n;
+    }
+    // 16 bytes a lane, from lane offset o + scalar offset k, to dst + 16 lane
+    __device__ __forceinline__ void load_lds(uint8_t* dst, uint32_t o, int k, int on) const {
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            __builtin_amdgcn_make_buffer_rsrc((void*)p, 0, on ? (int)bytes : 0, 0x00027000),
+            (__attribute__((address_space(3))) void*)dst, 16, (int)o, k, 0, 0);
+    }
+};
+
 template <int TM, int TN, int WM, int WN, int R, bool GLU, bool F32>
 __global__ void __launch_bounds__(64 * WM * WN, 2) gemm_tile_kernel(GemmArgs p, int tiles_m, int tiles_n) {
     constexpr int WAVES = WM * WN;
@@ -164,24 +181,27 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gemm_tile_kernel(GemmArgs p, 
 
     // ---- load side: load j of this wave fills stage rows 8 (wv LA + j) ..
     // (A; B after TM rows likewise); lane i: row i / 8 of them, chunk
-    // (i % 8) ^ ((row / 2) & 7) of its source row. 32-bit offsets from
-    // wave-uniform bases; per-lane constants are formed where they are used
-    // from an opaque copy of the lane id, so that none is held in registers
-    // (or turned into 64-bit pointers) across the step loop.
+    // (i % 8) ^ ((row / 2) & 7) of its source row. Buffer loads: 32-bit lane
+    // offsets from the tile's first row, the K position as a scalar, no
+    // address arithmetic in the step loop. A step that K ends in runs on into
+    // the next row, and past the operand's end the buffer's bounds check drops
+    // the access: the multiply side zeroes A there.
+    // (Per-lane constants used once a tile are formed there, from an opaque copy
+    // of the lane id: held across the step loop they would spill.)
     auto opaque_lane = [&]() __attribute__((always_inline)) {
         int l = lane_id();
         asm volatile("" : "+v"(l));
         return l;
     };
-    const int ch0 = 16 * ((lane & 7) ^ (lane >> 4));             // chunk of even 8-row groups; odd ones: ^ 64
     uint32_t oA[LA], oB[LB];
-    const uint8_t* bA;
-    const uint8_t* bB[LB];
+    Operand bA, bB, bU;                                          // A, B (glu: its gate rows), glu's up rows
     int row0 = 0, col0 = 0, row1, col1;                          // the tile being multiplied; the one being loaded
     auto setup = [&](int j) __attribute__((always_inline)) {
         place(j, row1, col1);
-        const int sub = opaque_lane() >> 3;
-        bA = (const uint8_t*)p.a + (size_t)row1 * K;
+        const int ln = opaque_lane(), sub = ln >> 3, ch0 = 16 * ((ln & 7) ^ (ln >> 4));   // (odd 8-row groups: chunk ^ 64)
+        bA.set(p.a + (size_t)row1 * K, (size_t)(p.M - row1) * K);
+        bB.set(p.b + (size_t)col1 * K, (size_t)(p.N - col1) * K);
+        if (GLU) bU.set(p.b + ((size_t)p.N + col1) * K, (size_t)(p.N - col1) * K);
 #pragma unroll
         for (int i = 0; i < LA; ++i) {
             const int r8 = wv * LA + i;
@@ -192,7 +212,6 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gemm_tile_kernel(GemmArgs p, 
             const int r8 = wv * LB + i, f = r8 / 2, m = 8 * (r8 & 1) + sub;
             const int w = f / NF, n = f % NF;
             const int c = w * 16 * NC + NC * m + n % NC;         // output column in the tile
-            bB[i] = (const uint8_t*)p.b + ((size_t)col1 + (GLU && n >= NC ? p.N : 0)) * K;
             oB[i] = (uint32_t)min(c, p.N - 1 - col1) * K + (ch0 ^ (64 * (r8 & 1)));
         }
     };
@@ -209,18 +228,14 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gemm_tile_kernel(GemmArgs p, 
             if (!GLU) lds_dma4(p.bias ? p.bias + n : (const float*)g_zero16, (uint8_t*)(md + TM + TN + 64 * i));
         }
     };
-    // load l of the K bytes from k0 on into stage st; in0, in1: whether this
-    // lane's chunk of an even, odd 8-row group lies inside K (else zeros)
-    auto dma = [&](int k0, bool in0, bool in1, int st, int l) __attribute__((always_inline)) {
+    // load l of the 128 K bytes from k0 on into stage st (on = 0: no access)
+    auto dma = [&](int k0, int on, int st, int l) __attribute__((always_inline)) {
         const int j = l < LA ? l : 0, i = l < LA ? 0 : l - LA;
-        const int r8 = l < LA ? wv * LA + j : wv * LB + i;
-        uint32_t o = l < LA ? oA[j] : oB[i];
-        asm volatile("" : "+v"(o));
-        const uint8_t* src = (l < LA ? bA : bB[i]) + k0 + o;
-        src = ((l < LA ? j : i) & 1 ? in1 : in0) ? src : g_zero16;
-        lds_dma16(src, smem + st * STAGE + (l < LA ? 0 : TM * 128) + 1024 * r8);
+        uint8_t* dst = smem + st * STAGE + (l < LA ? 1024 * (wv * LA + j) : TM * 128 + 1024 * (wv * LB + i));
+        if (l < LA) bA.load_lds(dst, oA[j], k0, on);
+        else if (GLU && (wv * LB + i) / 2 % NF >= NC) bU.load_lds(dst, oB[i], k0, on);
+        else bB.load_lds(dst, oB[i], k0, on);
     };
-    static_assert(LA % 2 == 0 && LB % 2 == 0, "load j of a wave fills an odd group where j is odd");
 
     // ---- multiply side: lane (m, q) holds 16 K bytes of fragment row m, chunk 4 u + q in sub-step u
     i32x4 acc[MF][NF];
@@ -247,9 +262,19 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gemm_tile_kernel(GemmArgs p, 
         else if (i <= NF) fb[u][i - 1] = *(const i32x4*)(smem + f.y + (i - 1) * 2048);
         else fa[u][i - NF] = *(const i32x4*)(smem + f.x + (i - NF) * 2048);
     };
-    // sub-step 0 of a step: multiply, and read sub-step 1 behind the first instructions
-    auto half0 = [&](int st) __attribute__((always_inline)) {
+    // A is zero past K (s: the step; 16-byte chunk 4 u + lane / 16 of it)
+    auto cut = [&](int s, int u) __attribute__((always_inline)) {
+        if (128 * (s + 1) <= K) return;
+        const bool out = 128 * s + 64 * u + 16 * (opaque_lane() >> 4) >= K;
+#pragma unroll
+        for (int a = 0; a < MF; ++a)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) fa[u][a][i] = out ? 0 : fa[u][a][i];
+    };
+    // sub-step 0 of step s: multiply, and read sub-step 1 behind the first instructions
+    auto half0 = [&](int s, int st) __attribute__((always_inline)) {
         const int2 f = frags(st, 1);
+        cut(s, 0);
 #pragma unroll
         for (int k = 0; k < NK; ++k) {
             acc[k / NF][k % NF] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fa[0][k / NF], fb[0][k % NF], acc[k / NF][k % NF], 0, 0, 0);
@@ -262,9 +287,9 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gemm_tile_kernel(GemmArgs p, 
     // are read and this one is refilled (the loads spread over the rest)
     constexpr int BAR = 2;
     constexpr int LS = (NK - BAR) / NL > 0 ? (NK - BAR) / NL : 1;
-    auto half1 = [&](int st, int nx, int k0, int kend) __attribute__((always_inline)) {
+    auto half1 = [&](int s, int st, int nx, int k0, int on) __attribute__((always_inline)) {
         const int2 f = frags(nx, 0);
-        const bool in0 = k0 + ch0 < kend, in1 = k0 + (ch0 ^ 64) < kend;
+        cut(s, 1);
 #pragma unroll
         for (int k = 0; k < NK; ++k) {
             acc[k / NF][k % NF] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fa[1][k / NF], fb[1][k % NF], acc[k / NF][k % NF], 0, 0, 0);
@@ -273,7 +298,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gemm_tile_kernel(GemmArgs p, 
                 barrier_lds();
             }
             if (k >= BAR - 1 && k - BAR + 1 < NR) read(f, 0, k - BAR + 1);
-            if (k >= BAR && (k - BAR) % LS == 0 && (k - BAR) / LS < NL) dma(k0, in0, in1, st, (k - BAR) / LS);
+            if (k >= BAR && (k - BAR) % LS == 0 && (k - BAR) / LS < NL) dma(k0, on, st, (k - BAR) / LS);
             __builtin_amdgcn_sched_barrier(0);
         }
         static_assert((NK - 1 - BAR) / LS >= NL - 1 && NK - BAR + 1 > NR, "every load and read has its instruction");
@@ -281,8 +306,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gemm_tile_kernel(GemmArgs p, 
     // KIND 0: aligned rows, 1: aligned rows with the addend, 2: any
     auto rows_out = [&](const float* md, auto kind) __attribute__((always_inline)) {
         constexpr int KIND = decltype(kind)::value;
-        const int ln = opaque_lane();
-        const int m = ln & 15, q = ln >> 4;
+        const int ln = opaque_lane(), m = ln & 15, q = ln >> 4;
         const int cw = nw * 16 * NC + NC * m, col = col0 + cw;
         float sb[NF], bias[NC];
 #pragma unroll
@@ -345,7 +369,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gemm_tile_kernel(GemmArgs p, 
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int l = 0; l < NL; ++l) dma(128 * r, 128 * r + ch0 < K, 128 * r + (ch0 ^ 64) < K, r, l);
+        for (int l = 0; l < NL; ++l) dma(128 * r, 1, r, l);
     zero_acc();
     wait_vmcnt<(R - 1) * NL>();
     barrier_lds();
@@ -355,12 +379,12 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gemm_tile_kernel(GemmArgs p, 
     for (int j = 0; j < nj; ++j) {
         row0 = row1;
         col0 = col1;
-        const int kn = j + 1 < nj ? K : 0;                       // K of the loads past this tile's last step
+        const int more = j + 1 < nj;
         for (int s = 0; s < S; ++s) {
-            half0(st);
-            const bool next = s == S - R && kn;
+            half0(s, st);
+            const bool next = s == S - R && more;
             if (next) setup(j + 1);                              // every load of tile j is out
-            half1(st, nx, (s + R < S ? s + R : s + R - S) * 128, s + R < S ? K : kn);
+            half1(s, st, nx, (s + R < S ? s + R : s + R - S) * 128, s + R < S || more);
             if (next) meta((j + 1) & 1);                         // (after half1's wait)
             st = nx;
             nx = nx + 1 == R ? 0 : nx + 1;
