@@ -275,6 +275,10 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gemm_tile_kernel(GemmArgs p, 
     auto half0 = [&](int s, int st) __attribute__((always_inline)) {
         const int2 f = frags(st, 1);
         cut(s, 0);
+        // two workgroups on a CU: the one in its first half, which waits for
+        // nothing, goes first (4096 x 2048 x 2048 19.6 -> 18.3 us; with one the
+        // order does not matter)
+        if (TM == 128) __builtin_amdgcn_s_setprio(1);
 #pragma unroll
         for (int k = 0; k < NK; ++k) {
             acc[k / NF][k % NF] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fa[0][k / NF], fb[0][k % NF], acc[k / NF][k % NF], 0, 0, 0);
@@ -290,6 +294,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gemm_tile_kernel(GemmArgs p, 
     auto half1 = [&](int s, int st, int nx, int k0, int on) __attribute__((always_inline)) {
         const int2 f = frags(nx, 0);
         cut(s, 1);
+        if (TM == 128) __builtin_amdgcn_s_setprio(0);
 #pragma unroll
         for (int k = 0; k < NK; ++k) {
             acc[k / NF][k % NF] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fa[1][k / NF], fb[1][k % NF], acc[k / NF][k % NF], 0, 0, 0);
