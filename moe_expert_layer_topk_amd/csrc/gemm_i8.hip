@@ -42,7 +42,7 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 // in an epilogue that no matrix instruction hides: gated 16384 x 512 x 2048
 // 37.2 us with it)
 __device__ __forceinline__ float glu_h(float g, float u) {
-    return g * u * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269504088896341f));
+    return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269504088896341f)) * u;   // (g u first could overflow)
 }
 
 // Workgroup barrier that waits for the wave's LDS traffic only (the fence of
@@ -111,18 +111,30 @@ __device__ __forceinline__ void store_each(const GemmArgs& p, int row, int col, 
 
 // ------------------------------------------------------------------ tiles
 // TM x TN outputs (glu: TN rows of B = TN / 2 columns of h) by WM x WN waves,
-// K in steps of 128 bytes through two LDS stages of TM + TN rows.
+// K in steps of 128 bytes through two LDS stages of TM + TN rows, each step two
+// sub-steps of 64 bytes.
 // A stage row's 16-byte chunk c sits at c ^ ((row / 2) & 7): 16-byte fragment
 // reads of 16 consecutive rows then meet every bank once.
 // B fragment f = nw NF + n, row m holds output column nw 16 NC + NC m + n (NC
 // = NF), so the columns a lane accumulates are adjacent (glu: NC = NF / 2; the
 // first half of a wave's fragments are gate rows, the second the matching up
 // rows).
-// Persistent: a workgroup's tiles form one stream of K steps. In the second
-// half of a step's matrix instructions every fragment of the step is in
-// registers; past a barrier its stage is refilled with the step two ahead (the
-// next tile's first ones at a tile's end, so they land during the epilogue)
-// and the next step's first fragments are read.
+// Persistent: a workgroup's tiles form one stream of K steps. Sub-step 0's
+// instructions run while sub-step 1's fragments are read. In sub-step 1 every
+// fragment of the step is in registers; past a barrier its stage is refilled
+// with the step two ahead (the next tile's first ones at a tile's end, so they
+// land during the epilogue) and the next step's first fragments are read.
+//
+// Bound by the chip's power: on random codes the loop runs at 1.6-1.9 GHz
+// (2.4 GHz on zeros, 1.4 times as fast), with the matrix pipe busy about 80% of
+// the clocks. So what counts is energy per output: 16x16x64 instructions
+// (registers only: 3950 TOPS on random codes; 32x32x32: 2920), tiles as large
+// as LDS allows, few instructions beside the matrix ones. 8192^3: 416 us, 2640
+// TOPS (a library product with int32 output on the same card 457-465 us); 4096
+// x 8192 x 8192 208 us (253); 16384 x 2048 x 2048 63 us (81); gated 16384 x 512
+// x 2048 31.5 us. Measured without gain: three or four stages of a 128-wide
+// tile, four 128 x 128 waves (the compiler spills), places of the barrier and
+// the loads between the matrix instructions.
 template <int V>
 struct IC {
     static constexpr int value = V;
@@ -145,7 +157,7 @@ struct Operand {
     }
 };
 
-template <int TM, int TN, int WM, int WN, int R, bool GLU, bool F32>
+template <int TM, int TN, int WM, int WN, bool GLU, bool F32>
 __global__ void __launch_bounds__(64 * WM * WN, 2) gemm_tile_kernel(GemmArgs p, int tiles_m, int tiles_n) {
     constexpr int WAVES = WM * WN;
     constexpr int MF = TM / WM / 16, NF = TN / WN / 16;
@@ -156,11 +168,11 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gemm_tile_kernel(GemmArgs p, 
     constexpr int META = TM + 2 * TN;                            // floats: row scales, column scales, bias
     static_assert(LA >= 1 && LB >= 1 && TM % (8 * WAVES) == 0 && TN % (8 * WAVES) == 0 && TM % 64 == 0 && TN % 64 == 0, "tile");
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-    float* s_meta = (float*)(smem + R * STAGE);                  // two tiles' worth
+    float* s_meta = (float*)(smem + 2 * STAGE);                  // two tiles' worth
     const int lane = lane_id();
     const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int mw = wv / WN, nw = wv % WN;
-    const int K = p.K, S = max(R, (K + 127) / 128);
+    const int K = p.K, S = max(2, (K + 127) / 128);             // (a second step past K multiplies zeros)
 
     // this workgroup's tiles: start + idx + per_x j, j < nj. Each XCD takes a
     // run of consecutive tiles (blocks are dealt to the 8 XCDs in turn), and
@@ -291,15 +303,15 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gemm_tile_kernel(GemmArgs p, 
     // are read and this one is refilled (the loads spread over the rest)
     constexpr int BAR = 2;
     constexpr int LS = (NK - BAR) / NL > 0 ? (NK - BAR) / NL : 1;
-    auto half1 = [&](int s, int st, int nx, int k0, int on) __attribute__((always_inline)) {
-        const int2 f = frags(nx, 0);
+    auto half1 = [&](int s, int st, int k0, int on) __attribute__((always_inline)) {
+        const int2 f = frags(st ^ 1, 0);
         cut(s, 1);
         if (TM == 128) __builtin_amdgcn_s_setprio(0);
 #pragma unroll
         for (int k = 0; k < NK; ++k) {
             acc[k / NF][k % NF] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fa[1][k / NF], fb[1][k % NF], acc[k / NF][k % NF], 0, 0, 0);
             if (k == BAR - 1) {
-                wait_vmcnt<(R - 2) * NL>();                       // (more in flight than that: waits for more)
+                wait_vmcnt<0>();
                 barrier_lds();
             }
             if (k >= BAR - 1 && k - BAR + 1 < NR) read(f, 0, k - BAR + 1);
@@ -372,27 +384,25 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gemm_tile_kernel(GemmArgs p, 
     setup(0);
     meta(0);
 #pragma unroll
-    for (int r = 0; r < R; ++r)
+    for (int l = 0; l < NL; ++l) dma(0, 1, 0, l);
 #pragma unroll
-        for (int l = 0; l < NL; ++l) dma(128 * r, 1, r, l);
+    for (int l = 0; l < NL; ++l) dma(128, 1, 1, l);
     zero_acc();
-    wait_vmcnt<(R - 1) * NL>();
+    wait_vmcnt<NL>();
     barrier_lds();
 #pragma unroll
     for (int i = 0; i < NR; ++i) read(frags(0, 0), 0, i);
-    int st = 0, nx = 1;
+    int st = 0;
     for (int j = 0; j < nj; ++j) {
         row0 = row1;
         col0 = col1;
         const int more = j + 1 < nj;
-        for (int s = 0; s < S; ++s) {
+        for (int s = 0; s < S; ++s, st ^= 1) {
             half0(s, st);
-            const bool next = s == S - R && more;
+            const bool next = s == S - 2 && more;
             if (next) setup(j + 1);                              // every load of tile j is out
-            half1(s, st, nx, (s + R < S ? s + R : s + R - S) * 128, s + R < S || more);
-            if (next) meta((j + 1) & 1);                         // (after half1's wait)
-            st = nx;
-            nx = nx + 1 == R ? 0 : nx + 1;
+            half1(s, st, (s + 2 < S ? s + 2 : s + 2 - S) * 128, s + 2 < S || more);
+            if (next) meta((j + 1) & 1);                         // (after half1's wait and barrier)
         }
         epilogue(j & 1);
         zero_acc();
@@ -402,11 +412,16 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gemm_tile_kernel(GemmArgs p, 
 // ------------------------------------------------------------------ few tiles
 // Smaller tiles, for outputs that large tiles would spread over too few CUs.
 // The waves of a workgroup share one TM x TN tile and split each step's K
-// instead: wave k multiplies the 32-byte sub-steps k, k + WK .. of the whole
-// tile, which reads half as much LDS per matrix instruction as splitting the
-// tile (a 64 x 64 tile in four 32 x 32 quarters), and their int32 sums meet in
-// LDS (the ring's memory, free by then), where the epilogue takes them in row
-// order.
+// instead: wave k multiplies 32-byte sub-step k of the whole tile, which reads
+// half as much LDS per matrix instruction as splitting the tile (a 64 x 64 tile
+// in four 32 x 32 quarters), and their int32 sums meet in LDS (the ring's
+// memory, free by then), where the epilogue takes them in row order. R stages
+// are in flight. With one row the weights stream at HBM's rate (1 x 8192 x
+// 8192: 11.3 us, 5.9 TB/s, most of it launch and first latency below 2048 x
+// 2048: 4.0 us); with more, bound by L2 to LDS loads (about 50 bytes a clock
+// and CU): 333 x 1000 x 4112 9.8 us, 256 x 2048 x 2048 6.4 us. A kernel that
+// streamed B straight into registers for up to 32 rows was no faster at one
+// row and up to 1.4 times slower at 16.
 template <int TM, int TN, int WK, int R, bool GLU, bool F32>
 __global__ void __launch_bounds__(64 * WK) gemm_split_kernel(GemmArgs p, int tiles_m, int tiles_n) {
     constexpr int MF = TM / 32, NF = TN / 32;
@@ -569,18 +584,18 @@ static hipError_t allow_lds(const void* kernel, int bytes, std::atomic<uint64_t>
     return e;
 }
 
-template <int TM, int TN, int WM, int WN, int R, bool GLU, bool F32>
+template <int TM, int TN, int WM, int WN, bool GLU, bool F32>
 static hipError_t launch_tile(GemmArgs p, int kid, hipStream_t stream) {
     constexpr int OUTN = GLU ? TN / 2 : TN, NC = OUTN / WN / 16;
-    constexpr int SMEM = R * (TM + TN) * 128 + 8 * (TM + 2 * TN);
+    constexpr int SMEM = 2 * (TM + TN) * 128 + 8 * (TM + 2 * TN);
     constexpr int PER_CU = 163840 / SMEM < 8 / (WM * WN) ? 163840 / SMEM : 8 / (WM * WN);
     static std::atomic<uint64_t> done{0};
-    const hipError_t e = allow_lds((const void*)gemm_tile_kernel<TM, TN, WM, WN, R, GLU, F32>, SMEM, done);
+    const hipError_t e = allow_lds((const void*)gemm_tile_kernel<TM, TN, WM, WN, GLU, F32>, SMEM, done);
     if (e != hipSuccess) return e;
     p.vec = p.vec && p.N % NC == 0;
     const int tm = (p.M + TM - 1) / TM, tn = (p.N + OUTN - 1) / OUTN;
     const int slots = (device_cus() * PER_CU + 7) / 8 * 8, grid = min(slots, (tm * tn + 7) / 8 * 8);
-    MOE_LAUNCH(kid, stream, (gemm_tile_kernel<TM, TN, WM, WN, R, GLU, F32>), dim3((unsigned)grid), dim3(64 * WM * WN),
+    MOE_LAUNCH(kid, stream, (gemm_tile_kernel<TM, TN, WM, WN, GLU, F32>), dim3((unsigned)grid), dim3(64 * WM * WN),
                SMEM, stream, p, tm, tn);
     return hipGetLastError();
 }
@@ -644,8 +659,8 @@ static int pick_shape(int M, long long rows_b, int K) {
 template <bool GLU, bool F32>
 static hipError_t launch_any(const GemmArgs& p, int kid, hipStream_t stream) {
     switch (pick_shape(p.M, (long long)p.N * (GLU ? 2 : 1), p.K)) {
-        case S_256x256: return launch_tile<256, 256, 4, 2, 2, GLU, F32>(p, kid, stream);
-        case S_128x128: return launch_tile<128, 128, 2, 2, 2, GLU, F32>(p, kid, stream);
+        case S_256x256: return launch_tile<256, 256, 4, 2, GLU, F32>(p, kid, stream);
+        case S_128x128: return launch_tile<128, 128, 2, 2, GLU, F32>(p, kid, stream);
         case S_64x64: return launch_split<64, 64, 4, 4, GLU, F32>(p, kid, stream);
         case S_32x64: return launch_split<32, 64, 8, 4, GLU, F32>(p, kid, stream);
         default: return launch_split<32, 32, 8, 4, GLU, F32>(p, kid, stream);

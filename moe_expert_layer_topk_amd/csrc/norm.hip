@@ -332,7 +332,6 @@ __global__ void __launch_bounds__(256) norm_elem_kernel(NormArgs p) {
     Peak peak;
 #pragma unroll
     for (int j = 0; j < NE; ++j) {
-        if (j * 256 >= p.cols) break;
         const int i = t + j * 256;
         const double u = vw_of(j);
         peak.add(u);

@@ -355,6 +355,17 @@ def test_glu_i8_wide_gates(gpu, M):
     _glu_case(gpu, M, 192, 512, gain=60.0)
 
 
+@pytest.mark.parametrize("M", [5, 50, 400])
+def test_glu_i8_closed_gates_of_huge_products(gpu, M):
+    """g far below zero with g u past fp32: silu(g) is 0 there, and so is h."""
+    import torch
+    a = _i8(np.full((M, 64), 127), gpu)
+    w = _i8(np.concatenate([np.full((40, 64), -127), np.full((40, 64), 127)]), gpu)
+    h = moe.glu_i8(a, torch.full((M,), 1e8, device=gpu), w, torch.full((80,), 1e8, device=gpu))
+    torch.cuda.synchronize()
+    assert (h == 0).all()
+
+
 def test_results_repeat_bit_for_bit(gpu):
     import torch
     r = _rng(25)
