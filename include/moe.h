@@ -326,13 +326,13 @@ int moe_quant_act(const uint16_t* d_x, int rows, int cols, uint8_t* d_codes, uin
  * d_sum and d_y may each be d_x or d_res itself (not the same one); no other
  * overlap is allowed. A row (FP8: a group) of y that holds NaN or a value past
  * the largest fp32 gets codes 0 and a NaN scale (FP8: the E8M0 NaN byte 255).
- * Limits: 1 <= rows, 1 <= cols <= 16384, eps > 0 and finite.
+ * Limits: 1 <= rows < 2^24, 1 <= cols <= 16384, eps > 0 and finite.
  * moe_quant_rows: MOE_Q_I8_ROW of the rows of d_x themselves (the codes are
  * exactly the definition's, ties included).
  * moe_dequant_rows: the way back, d_out bf16 [rows, cols] = code * scale
  * rounded once, for either kind of rows (MOE_Q_FP8_G128_POW2: those of
  * moe_quant_act too; cols % 128 == 0, d_codes and d_out 16-byte aligned);
- * rows * cols < 2^35 (2^32 where cols % 8 or an address is not 16-byte aligned). */
+ * rows * cols < 2^34 (2^31 where cols % 8 or an address is not 16-byte aligned). */
 enum { MOE_Q_NONE = 0, MOE_Q_I8_ROW = 1, MOE_Q_FP8_G128_POW2 = 2 };
 int moe_norm(const uint16_t* d_x, const uint16_t* d_res, const float* d_weight, float eps, int rows, int cols,
              int qmode, uint16_t* d_sum, uint16_t* d_y, uint8_t* d_codes, void* d_scales, void* stream);
@@ -349,7 +349,8 @@ int moe_dequant_rows(const uint8_t* d_codes, const void* d_scales, int rows, int
  *  moe_quant_rows write them (a factor per token, such as a shared expert's
  *  gate, can be multiplied into d_sa); d_b i8 [N, K], d_sb f32 [N];
  *  d_bias f32 [N] or NULL; d_add [M, N] of the output's type or NULL (it may
- *  be d_out itself); d_out bf16 [M, N] (MOE_OUT_BF16) or f32 (MOE_OUT_F32).
+ *  be d_out itself); d_out bf16 [M, N] (MOE_OUT_BF16) or f32 (MOE_OUT_F32), no
+ *  other overlap.
  * moe_glu_i8, a shared expert's first half in one kernel: with g and u the
  * products of a with rows [0, I) (gate) and [I, 2I) (up) of d_w13 i8 [2I, K]
  * and their scales d_s13 f32 [2I], h = silu(g) * u, d_h bf16 [M, I].

@@ -92,6 +92,11 @@ bool aligned16(const P*... p) {
     return (((uintptr_t)p | ... | (uintptr_t)0) & 15) == 0;
 }
 
+// rows of the norm kernels: a workgroup of 256 threads for each at most, and fewer than 2^32 threads in a launch
+bool valid_rows(int rows, int cols) {
+    return rows >= 1 && rows < (1 << 24) && cols >= 1 && cols <= moe::norm_max_cols();
+}
+
 // sizes of an int8 product: int32 sums cannot overflow, and tile counts fit an int
 bool valid_product(int M, int N, int K) {
     if (M < 1 || M > (1 << 30) || N < 1 || N > (1 << 30) || K < 16 || K % 16 || K > 131056) return false;
@@ -324,7 +329,7 @@ int moe_quant_act(const uint16_t* d_x, int rows, int cols, uint8_t* d_codes, uin
 
 int moe_norm(const uint16_t* d_x, const uint16_t* d_res, const float* d_weight, float eps, int rows, int cols,
              int qmode, uint16_t* d_sum, uint16_t* d_y, uint8_t* d_codes, void* d_scales, void* stream) {
-    if (!d_x || rows < 1 || cols < 1 || cols > moe::norm_max_cols()) return MOE_EINVAL;
+    if (!d_x || !valid_rows(rows, cols)) return MOE_EINVAL;
     if (!(eps > 0.f) || eps > 3.4028235e38f) return MOE_EINVAL;
     if (qmode < MOE_Q_NONE || qmode > MOE_Q_FP8_G128_POW2) return MOE_EINVAL;
     if (qmode == MOE_Q_NONE ? (d_codes || d_scales || (!d_sum && !d_y)) : (!d_codes || !d_scales)) return MOE_EINVAL;
@@ -337,7 +342,7 @@ int moe_norm(const uint16_t* d_x, const uint16_t* d_res, const float* d_weight, 
 }
 
 int moe_quant_rows(const uint16_t* d_x, int rows, int cols, int8_t* d_codes, float* d_scales, void* stream) {
-    if (!d_x || !d_codes || !d_scales || rows < 1 || cols < 1 || cols > moe::norm_max_cols()) return MOE_EINVAL;
+    if (!d_x || !d_codes || !d_scales || !valid_rows(rows, cols)) return MOE_EINVAL;
     clear_stale_error();
     return hip_status(moe::launch_quant_rows(d_x, rows, cols, d_codes, d_scales, aligned16(d_x, d_codes),
                                              (hipStream_t)stream));
@@ -349,7 +354,7 @@ int moe_dequant_rows(const uint8_t* d_codes, const void* d_scales, int rows, int
     if (qmode != MOE_Q_I8_ROW && qmode != MOE_Q_FP8_G128_POW2) return MOE_EINVAL;
     const bool vec = cols % 8 == 0 && aligned16(d_codes, d_out);
     if (qmode == MOE_Q_FP8_G128_POW2 && (cols % MOE_ACT_G || !vec)) return MOE_EINVAL;
-    if ((long long)rows * cols >= (vec ? 1LL << 35 : 1LL << 32)) return MOE_EINVAL;   // 32-bit vector (value) indices
+    if ((long long)rows * cols >= (vec ? 1LL << 34 : 1LL << 31)) return MOE_EINVAL;   // a launch has fewer than 2^32 threads
     clear_stale_error();
     return hip_status(moe::launch_dequant_rows(d_codes, d_scales, rows, cols, qmode, d_out, vec, (hipStream_t)stream));
 }

@@ -155,6 +155,7 @@ PyObject* py_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Out sum, y, codes, scales;
     if (res || a[6] != Py_None) sum = Out(a[6], x, T, H, BF16, "sum");
     if (with_y) y = Out(a[7], x, T, H, BF16, "y");
+    else if (a[7] != Py_None) refuse("y is written only with with_y");
     if (q == MOE_Q_FP8_G128_POW2) {
         codes = Out(a[8], x, T, H, U8, "codes");
         scales = Out(a[9], x, T, H / 128, U8, "scales");

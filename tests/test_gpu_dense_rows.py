@@ -174,3 +174,10 @@ def test_dequant_refusals(gpu):
                  lambda: moe.dequant_rows(c.t(), torch.zeros(64, device=gpu))):
         with pytest.raises(moe.MoeError):
             call()
+
+
+def test_norm_refuses_a_y_that_it_would_not_write(gpu):
+    import torch
+    x = torch.zeros(4, 64, dtype=torch.bfloat16, device=gpu)
+    with pytest.raises(moe.MoeError):
+        moe.norm(x, res=x, with_y=False, y=torch.empty_like(x))

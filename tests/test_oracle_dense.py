@@ -130,3 +130,13 @@ def test_binding_refuses_before_a_launch():
                  lambda: moe.glu_i8(a, s, a[:3], s[:3])):
         with pytest.raises(moe.MoeError):
             call()
+
+
+def test_launches_past_their_thread_count_are_refused(L):
+    """Sizes whose grid would hold 2^32 threads: a workgroup of 256 per row, or one thread per 8 codes (unaligned: per code)."""
+    f, g, n, odd = ctypes.c_void_p(0x1000), ctypes.c_void_p(0x2000), None, ctypes.c_void_p(0x1008)
+    for rows in (1 << 24, (1 << 31) - 1):
+        assert L.moe_norm(f, n, n, 1e-6, rows, 8, 0, n, g, n, n, n) == -1
+        assert L.moe_quant_rows(f, rows, 8, g, g, n) == -1
+    for codes, rows, cols in ((f, 1 << 20, 16384), (odd, 1 << 20, 2048), (f, 1 << 22, 516)):
+        assert L.moe_dequant_rows(codes, f, rows, cols, 1, g, n) == -1
