@@ -27,7 +27,7 @@ struct GemmArgs {
     const void* add;          // may be null; the output's type
     void* out;
     int M, N, K;              // N: output columns (glu: inter; b then has 2N rows)
-    int vec;                  // output (and add) rows take vector accesses of a lane's columns
+    int lines;                // output rows are whole 128-byte lines (and add's address is 16-byte aligned)
 };
 
 __device__ const uint8_t g_zero16[16] = {0};            // source of K bytes past a row's end
@@ -54,20 +54,27 @@ static __device__ __forceinline__ void barrier_lds() {
     asm volatile("" ::: "memory");
 }
 
-// NC adjacent output columns of one row. VEC: all of them exist or none (N %
-// NC == 0) and their address is a multiple of their size (up to 16 bytes);
-// otherwise one by one. Outputs are written once and not read here: stored
-// past the caches' order of use, so that a launch does not end by writing back
-// what its last tiles left in L2 (16384 x 2048 x 512 with the addend 45 -> 35
-// us, gated 16384 x 512 x 2048 35.0 -> 33.5, others the same).
-template <int NC, bool F32>
+// NC adjacent output columns of one row, all of them inside it, in accesses of
+// up to 16 bytes. !ANY: rows are whole 128-byte lines. Outputs are written once
+// and not read here, so they are stored past the caches' order of use, and a
+// launch does not end by writing back what its last tiles left in L2 (16384 x
+// 2048 x 512 with the addend 39 -> 35 us, gated 16384 x 512 x 2048 31.4 ->
+// 30.2, others the same).
+// ANY: rows of any length that start at any element. Here such stores would
+// write parts of lines to memory one by one (15007 x 1928 x 128 32 us, stored
+// through L2 19; 10357 x 752 x 208 with the addend 11.2 and 10.2). Accesses
+// that are not aligned to their size are split by the memory pipeline, which
+// is still fewer than one for each value (5324 x 437 x 1408 with the addend
+// 24.2 us one by one, 15.7 so; 4096 x 1999 x 2048 25.1 and 21.3).
+template <int NC, bool F32, bool ANY = false>
 struct Cols {
     typedef uint32_t word __attribute__((ext_vector_type(NC == 2 && !F32 ? 1 : NC * (F32 ? 4 : 2) / 4 < 4 ? NC * (F32 ? 4 : 2) / 4 : 4)));
+    typedef word place __attribute__((aligned(ANY ? (F32 ? 4 : 2) : sizeof(word))));
     static constexpr int W = sizeof(word) / 4;                   // dwords of an access
     static constexpr int NW = NC * (F32 ? 4 : 2) / (4 * W);      // accesses
     word w[NW];
     __device__ __forceinline__ void load(const void* p, size_t o) {
-        const word* q = (const word*)((const uint8_t*)p + o * (F32 ? 4 : 2));
+        const place* q = (const place*)((const uint8_t*)p + o * (F32 ? 4 : 2));
 #pragma unroll
         for (int h = 0; h < NW; ++h) w[h] = q[h];
     }
@@ -88,11 +95,15 @@ struct Cols {
             if (F32) c.w[d / W][d % W] = __float_as_uint(v[d]);
             else c.w[d / W][d % W] = pack_bf16(v[2 * d], v[2 * d + 1]);
         }
-        word* q = (word*)((uint8_t*)p + o * (F32 ? 4 : 2));
+        place* q = (place*)((uint8_t*)p + o * (F32 ? 4 : 2));
 #pragma unroll
-        for (int h = 0; h < NW; ++h) __builtin_nontemporal_store(c.w[h], q + h);
+        for (int h = 0; h < NW; ++h) {
+            if (ANY) q[h] = c.w[h];
+            else __builtin_nontemporal_store(c.w[h], q + h);
+        }
     }
 };
+// the columns of them that exist, one by one
 template <int NC, bool F32>
 __device__ __forceinline__ void store_each(const GemmArgs& p, int row, int col, float (&v)[NC]) {
     const size_t o = (size_t)row * p.N + col;
@@ -320,65 +331,84 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gemm_tile_kernel(GemmArgs p, 
         }
         static_assert((NK - 1 - BAR) / LS >= NL - 1 && NK - BAR + 1 > NR, "every load and read has its instruction");
     };
-    // KIND 0: aligned rows, 1: aligned rows with the addend, 2: any
+    // KIND 0: rows of whole lines, 1: with the addend, 2 and 3: any rows
     auto rows_out = [&](const float* md, auto kind) __attribute__((always_inline)) {
         constexpr int KIND = decltype(kind)::value;
+        constexpr bool ANY = KIND >= 2, ADD = KIND & 1;
         const int ln = opaque_lane(), m = ln & 15, q = ln >> 4;
         const int cw = nw * 16 * NC + NC * m, col = col0 + cw;
+        const bool full = ANY ? col + NC <= p.N : col < p.N;     // all of the lane's columns exist
         float sb[NF], bias[NC];
 #pragma unroll
         for (int n = 0; n < NF; ++n) sb[n] = md[TM + (GLU && n >= NC ? OUTN : 0) + cw + n % NC];
 #pragma unroll
         for (int n = 0; n < NC; ++n) bias[n] = GLU ? 0.f : md[TM + TN + cw + n];
         // lane (m, q), register i of fragment (a, n): row 16 (mw MF + a) + 4 q + i
+        auto values = [&](int a, int i, float sa, float (&v)[NC]) __attribute__((always_inline)) {
+#pragma unroll
+            for (int n = 0; n < NC; ++n) {
+                if constexpr (GLU) v[n] = glu_h((float)acc[a][n][i] * sa * sb[n], (float)acc[a][n + NC][i] * sa * sb[n + NC]);
+                else v[n] = (float)acc[a][n][i] * sa * sb[n] + bias[n];
+            }
+        };
 #pragma unroll
         for (int a = 0; a < MF; ++a) {
             const f32x4 sa = *(const f32x4*)(md + 16 * (mw * MF + a) + 4 * q);
             // the addends of NB rows are loaded together (rows and columns past
             // the output: from inside it, and dropped)
             constexpr int NB = F32 ? 2 : 4;
-            Cols<NC, F32> plus[KIND == 1 ? NB : 1];
+            Cols<NC, F32, ANY> plus[ADD ? NB : 1];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                if constexpr (KIND == 1) {
+                if constexpr (ADD) {
                     if (i % NB == 0) {
 #pragma unroll
                         for (int b = 0; b < NB; ++b) {
                             const int row = min(row0 + 16 * (mw * MF + a) + 4 * q + i + b, p.M - 1);
-                            plus[b].load(p.add, (size_t)row * p.N + (col < p.N ? col : 0));
+                            if (!ANY) plus[b].load(p.add, (size_t)row * p.N + (full ? col : 0));
+                            else {
+                                plus[b] = {};
+                                if (full) plus[b].load(p.add, (size_t)row * p.N + col);
+                            }
                         }
                     }
                 }
                 const int row = row0 + 16 * (mw * MF + a) + 4 * q + i;
                 float v[NC];
+                values(a, i, sa[i], v);
+                if constexpr (ADD) {
+                    plus[i % NB].add_to(v);
+                    // used outside the masked store: otherwise the wait for
+                    // the addends sinks into it, and where no lane stores
+                    // they stay in flight and the step loop waits, every
+                    // step, before it reuses their registers (226 -> 242 us
+                    // at 4096 x 8192 x 8192, which has no addend)
 #pragma unroll
-                for (int n = 0; n < NC; ++n) {
-                    if constexpr (GLU) v[n] = glu_h((float)acc[a][n][i] * sa[i] * sb[n], (float)acc[a][n + NC][i] * sa[i] * sb[n + NC]);
-                    else v[n] = (float)acc[a][n][i] * sa[i] * sb[n] + bias[n];
+                    for (int n = 0; n < NC; ++n) asm volatile("" : "+v"(v[n]));
                 }
-                if constexpr (KIND == 2) {
-                    if (row < p.M) store_each<NC, F32>(p, row, col, v);
-                } else {
-                    if constexpr (KIND == 1) {
-                        plus[i % NB].add_to(v);
-                        // used outside the masked store: otherwise the wait for
-                        // the addends sinks into it, and where no lane stores
-                        // they stay in flight and the step loop waits, every
-                        // step, before it reuses their registers (226 -> 242 us
-                        // at 4096 x 8192 x 8192, which has no addend)
+                if (row < p.M && full) Cols<NC, F32, ANY>::store(p.out, (size_t)row * p.N + col, v);
+            }
+        }
+        if (!ANY || __ballot(!full && col < p.N) == 0) return;   // a wave in which the output's rows end inside a lane
 #pragma unroll
-                        for (int n = 0; n < NC; ++n) asm volatile("" : "+v"(v[n]));
-                    }
-                    if (row < p.M && col < p.N) Cols<NC, F32>::store(p.out, (size_t)row * p.N + col, v);
-                }
+        for (int a = 0; a < MF; ++a) {
+            const f32x4 sa = *(const f32x4*)(md + 16 * (mw * MF + a) + 4 * q);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int row = row0 + 16 * (mw * MF + a) + 4 * q + i;
+                float v[NC];
+                values(a, i, sa[i], v);
+                if (row < p.M && !full) store_each<NC, F32>(p, row, col, v);
             }
         }
     };
     auto epilogue = [&](int slot) __attribute__((always_inline)) {
         const float* md = s_meta + slot * META;
-        if (!p.vec) rows_out(md, IC<2>{});
-        else if (!GLU && p.add) rows_out(md, IC<GLU ? 0 : 1>{});
-        else rows_out(md, IC<0>{});
+        if (!GLU && p.add) {
+            if (p.lines) rows_out(md, IC<GLU ? 0 : 1>{});
+            else rows_out(md, IC<GLU ? 2 : 3>{});
+        } else if (p.lines) rows_out(md, IC<0>{});
+        else rows_out(md, IC<2>{});
     };
 
     setup(0);
@@ -558,16 +588,23 @@ __global__ void __launch_bounds__(64 * WK) gemm_split_kernel(GemmArgs p, int til
             if constexpr (GLU) v[n] = glu_h(v[n], (float)u[n] * sa * s_sb[OUTN + c + n]);
             else if (p.bias) v[n] += s_bias[c + n];
         }
-        if (!p.vec) store_each<4, F32>(p, row0 + r, col0 + c, v);
-        else if (col0 + c < p.N) {
-            const size_t o = (size_t)(row0 + r) * p.N + col0 + c;
+        const size_t o = (size_t)(row0 + r) * p.N + col0 + c;
+        if (p.lines) {
+            if (col0 + c >= p.N) continue;
             if (!GLU && p.add) {
                 Cols<4, F32> plus;
                 plus.load(p.add, o);
                 plus.add_to(v);
             }
             Cols<4, F32>::store(p.out, o, v);
-        }
+        } else if (col0 + c + 4 <= p.N) {
+            if (!GLU && p.add) {
+                Cols<4, F32, true> plus;
+                plus.load(p.add, o);
+                plus.add_to(v);
+            }
+            Cols<4, F32, true>::store(p.out, o, v);
+        } else store_each<4, F32>(p, row0 + r, col0 + c, v);
     }
 }
 
@@ -585,14 +622,13 @@ static hipError_t allow_lds(const void* kernel, int bytes, std::atomic<uint64_t>
 }
 
 template <int TM, int TN, int WM, int WN, bool GLU, bool F32>
-static hipError_t launch_tile(GemmArgs p, int kid, hipStream_t stream) {
-    constexpr int OUTN = GLU ? TN / 2 : TN, NC = OUTN / WN / 16;
+static hipError_t launch_tile(const GemmArgs& p, int kid, hipStream_t stream) {
+    constexpr int OUTN = GLU ? TN / 2 : TN;
     constexpr int SMEM = 2 * (TM + TN) * 128 + 8 * (TM + 2 * TN);
     constexpr int PER_CU = 163840 / SMEM < 8 / (WM * WN) ? 163840 / SMEM : 8 / (WM * WN);
     static std::atomic<uint64_t> done{0};
     const hipError_t e = allow_lds((const void*)gemm_tile_kernel<TM, TN, WM, WN, GLU, F32>, SMEM, done);
     if (e != hipSuccess) return e;
-    p.vec = p.vec && p.N % NC == 0;
     const int tm = (p.M + TM - 1) / TM, tn = (p.N + OUTN - 1) / OUTN;
     const int slots = (device_cus() * PER_CU + 7) / 8 * 8, grid = min(slots, (tm * tn + 7) / 8 * 8);
     MOE_LAUNCH(kid, stream, (gemm_tile_kernel<TM, TN, WM, WN, GLU, F32>), dim3((unsigned)grid), dim3(64 * WM * WN),
@@ -601,13 +637,12 @@ static hipError_t launch_tile(GemmArgs p, int kid, hipStream_t stream) {
 }
 
 template <int TM, int TN, int WK, int R, bool GLU, bool F32>
-static hipError_t launch_split(GemmArgs p, int kid, hipStream_t stream) {
+static hipError_t launch_split(const GemmArgs& p, int kid, hipStream_t stream) {
     constexpr int OUTN = GLU ? TN / 2 : TN;
     constexpr int SMEM = R * (TM + TN) * 32 * WK + 256 * ((TM + 63) / 64 + 2 * ((TN + 63) / 64));
     static std::atomic<uint64_t> done{0};
     const hipError_t e = allow_lds((const void*)gemm_split_kernel<TM, TN, WK, R, GLU, F32>, SMEM, done);
     if (e != hipSuccess) return e;
-    p.vec = p.vec && p.N % 4 == 0;
     const int tm = (p.M + TM - 1) / TM, tn = (p.N + OUTN - 1) / OUTN;
     MOE_LAUNCH(kid, stream, (gemm_split_kernel<TM, TN, WK, R, GLU, F32>), dim3((unsigned)(tm * tn)), dim3(64 * WK),
                SMEM, stream, p, tm, tn);
@@ -667,15 +702,17 @@ static hipError_t launch_any(const GemmArgs& p, int kid, hipStream_t stream) {
     }
 }
 
+static bool whole_lines(const void* p, int cols, int size) { return ((uintptr_t)p | (uintptr_t)cols * size) % 128 == 0; }
+
 hipError_t launch_gemm_i8(const int8_t* a, const float* sa, const int8_t* b, const float* sb, const float* bias,
-                          const void* add, int M, int N, int K, bool f32, void* out, bool vec, hipStream_t stream) {
-    const GemmArgs p{a, sa, b, sb, bias, add, out, M, N, K, vec};
+                          const void* add, int M, int N, int K, bool f32, void* out, bool aligned, hipStream_t stream) {
+    const GemmArgs p{a, sa, b, sb, bias, add, out, M, N, K, aligned && whole_lines(out, N, f32 ? 4 : 2)};
     return f32 ? launch_any<false, true>(p, K_GEMM_I8, stream) : launch_any<false, false>(p, K_GEMM_I8, stream);
 }
 
 hipError_t launch_glu_i8(const int8_t* a, const float* sa, const int8_t* w13, const float* s13, int M, int I, int K,
-                         uint16_t* h, bool vec, hipStream_t stream) {
-    const GemmArgs p{a, sa, w13, s13, nullptr, nullptr, h, M, I, K, vec};
+                         uint16_t* h, bool aligned, hipStream_t stream) {
+    const GemmArgs p{a, sa, w13, s13, nullptr, nullptr, h, M, I, K, aligned && whole_lines(h, I, 2)};
     return launch_any<true, false>(p, K_GLU_I8, stream);
 }
 

@@ -121,11 +121,11 @@ hipError_t launch_quant_rows(const uint16_t* x, int rows, int cols, int8_t* code
 hipError_t launch_dequant_rows(const uint8_t* codes, const void* scales, int rows, int cols, int qmode, uint16_t* out,
                                bool vec, hipStream_t stream);
 
-// int8 products (gemm_i8.hip); vec: out (and add) are 16-byte aligned
+// int8 products (gemm_i8.hip); aligned: out (and add) are 16-byte aligned
 hipError_t launch_gemm_i8(const int8_t* a, const float* sa, const int8_t* b, const float* sb, const float* bias,
-                          const void* add, int M, int N, int K, bool f32, void* out, bool vec, hipStream_t stream);
+                          const void* add, int M, int N, int K, bool f32, void* out, bool aligned, hipStream_t stream);
 hipError_t launch_glu_i8(const int8_t* a, const float* sa, const int8_t* w13, const float* s13, int M, int I, int K,
-                         uint16_t* h, bool vec, hipStream_t stream);
+                         uint16_t* h, bool aligned, hipStream_t stream);
 
 // pool validation (pool_check.hip): d_err += unusable slots; status[slot] optional
 hipError_t launch_pool_check(const PoolArgs& pa, int32_t* err, uint8_t* status, hipStream_t stream);

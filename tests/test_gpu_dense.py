@@ -515,3 +515,22 @@ def test_refusals_on_the_device(gpu):
         with pytest.raises(moe.MoeError):
             call()
             _say("not refused:", k)
+
+
+@pytest.mark.parametrize("M,N,K", [(4100, 1101, 160), (2300, 2047, 384), (700, 1023, 208), (90, 259, 144), (5000, 5, 64), (3000, 1030, 96)])
+def test_products_of_rows_that_start_anywhere(gpu, M, N, K):
+    """Odd row lengths (any start of a row, lanes that end inside one) in every tile size, with and without addend."""
+    import torch
+    for bias, add, f32 in ((False, False, False), (True, True, False), (False, True, True)):
+        _gemm_case(gpu, M, N, K, bias, add, f32, key=9)
+    _glu_case(gpu, M, N, K)
+    r = _rng(M, N, K, 31)
+    a, sa, b, sb = _operands(r, M, N, K)
+    args = (_i8(a, gpu), _f32(sa, gpu), _i8(b, gpu), _f32(sb, gpu))
+    for t, shift in ((torch.bfloat16, 1), (torch.bfloat16, 4), (torch.float32, 1)):
+        want = moe.gemm_i8(*args, out_dtype=t)
+        buf = torch.full((M * N + 64,), 7.0, dtype=t, device=gpu)
+        moe.gemm_i8(*args, out=buf[shift:shift + M * N].view(M, N))
+        torch.cuda.synchronize()
+        assert torch.equal(buf[shift:shift + M * N].view(M, N), want)
+        assert (buf[:shift] == 7).all() and (buf[shift + M * N:] == 7).all()
