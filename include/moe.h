@@ -332,7 +332,7 @@ int moe_quant_act(const uint16_t* d_x, int rows, int cols, uint8_t* d_codes, uin
  * moe_dequant_rows: the way back, d_out bf16 [rows, cols] = code * scale
  * rounded once, for either kind of rows (MOE_Q_FP8_G128_POW2: those of
  * moe_quant_act too; cols % 128 == 0, d_codes and d_out 16-byte aligned);
- * rows * cols < 2^34 (2^31 where cols % 8 or an address is not 16-byte aligned). */
+ * rows * cols < 2^34 (2^31 where cols % 8 != 0 or an address is not 16-byte aligned). */
 enum { MOE_Q_NONE = 0, MOE_Q_I8_ROW = 1, MOE_Q_FP8_G128_POW2 = 2 };
 int moe_norm(const uint16_t* d_x, const uint16_t* d_res, const float* d_weight, float eps, int rows, int cols,
              int qmode, uint16_t* d_sum, uint16_t* d_y, uint8_t* d_codes, void* d_scales, void* stream);

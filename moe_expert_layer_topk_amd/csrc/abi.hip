@@ -352,11 +352,12 @@ int moe_dequant_rows(const uint8_t* d_codes, const void* d_scales, int rows, int
                      void* stream) {
     if (!d_codes || !d_scales || !d_out || rows < 1 || cols < 1 || cols > moe::norm_max_cols()) return MOE_EINVAL;
     if (qmode != MOE_Q_I8_ROW && qmode != MOE_Q_FP8_G128_POW2) return MOE_EINVAL;
-    const bool vec = cols % 8 == 0 && aligned16(d_codes, d_out);
-    if (qmode == MOE_Q_FP8_G128_POW2 && (cols % MOE_ACT_G || !vec)) return MOE_EINVAL;
-    if ((long long)rows * cols >= (vec ? 1LL << 34 : 1LL << 31)) return MOE_EINVAL;   // a launch has fewer than 2^32 threads
+    const bool aligned = aligned16(d_codes, d_out);
+    if (qmode == MOE_Q_FP8_G128_POW2 && (cols % MOE_ACT_G || !aligned)) return MOE_EINVAL;
+    // (a launch has fewer than 2^32 threads, each with 8 values or one; values are counted in 32 bits except in rows of whole vectors)
+    if ((long long)rows * cols >= (aligned && cols % 8 == 0 ? 1LL << 34 : 1LL << 31)) return MOE_EINVAL;
     clear_stale_error();
-    return hip_status(moe::launch_dequant_rows(d_codes, d_scales, rows, cols, qmode, d_out, vec, (hipStream_t)stream));
+    return hip_status(moe::launch_dequant_rows(d_codes, d_scales, rows, cols, qmode, d_out, aligned, (hipStream_t)stream));
 }
 
 int moe_gemm_i8(const int8_t* d_a, const float* d_sa, const int8_t* d_b, const float* d_sb, const float* d_bias,

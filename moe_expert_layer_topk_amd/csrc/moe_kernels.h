@@ -112,14 +112,14 @@ hipError_t launch_dequant(const PoolArgs& pa, int slot, float* w13, float* w2, h
 hipError_t launch_quant_act(const uint16_t* x, int rows, int cols, uint8_t* codes, uint8_t* exps, hipStream_t stream);
 
 // residual addition + RMS norm with optional 8-bit rows, the int8 row quantizer, and 8-bit rows back to bf16 (norm.hip);
-// aligned: every pointer of the rows is 16-byte aligned; vec: and cols is a multiple of 8
+// aligned: every pointer of the rows is 16-byte aligned
 int norm_max_cols();
 hipError_t launch_norm(const uint16_t* x, const uint16_t* res, const float* w, float eps, int rows, int cols, int qmode,
                        uint16_t* sum, uint16_t* y, uint8_t* codes, void* scales, bool aligned, hipStream_t stream);
 hipError_t launch_quant_rows(const uint16_t* x, int rows, int cols, int8_t* codes, float* scales, bool aligned,
                              hipStream_t stream);
 hipError_t launch_dequant_rows(const uint8_t* codes, const void* scales, int rows, int cols, int qmode, uint16_t* out,
-                               bool vec, hipStream_t stream);
+                               bool aligned, hipStream_t stream);
 
 // int8 products (gemm_i8.hip); aligned: out (and add) are 16-byte aligned
 hipError_t launch_gemm_i8(const int8_t* a, const float* sa, const int8_t* b, const float* sb, const float* bias,

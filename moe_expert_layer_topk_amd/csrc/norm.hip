@@ -353,15 +353,19 @@ __global__ void __launch_bounds__(256) norm_elem_kernel(NormArgs p) {
 }
 
 // ------------------------------------------------------------------ 8-bit rows -> bf16
-// 8 values per thread and step (ELEM: one); code * scale in fp32, rounded once.
-template <int QMODE, bool ELEM>
+// 8 values per thread (ELEM: one, where an address is not aligned), over the
+// whole tensor: code * scale in fp32, rounded once. SHIFT (int8, cols no
+// multiple of 8): 8 values may belong to two rows or more; the division that
+// finds the row, and the walk over rows, cost little beside one value a thread
+// (5708 x 5878: 47 us so, 16.5 with 8).
+template <int QMODE, bool ELEM, bool SHIFT>
 __global__ void __launch_bounds__(256) dequant_rows_kernel(const uint8_t* codes, const void* scales, int cols, size_t n,
                                                            uint16_t* out) {
-    // (the caller keeps the number of vectors below 2^32)
+    // (the caller keeps the number of vectors below 2^32, and that of values too where they are counted)
     const uint32_t iv = blockIdx.x * 256u + threadIdx.x;
     const size_t i = (size_t)iv * (ELEM ? 1 : 8);
     if (i >= n) return;
-    const uint32_t row = iv / (uint32_t)(ELEM ? cols : cols / 8);
+    const uint32_t row = ELEM || SHIFT ? (uint32_t)i / (uint32_t)cols : iv / (uint32_t)(cols / 8);
     float sc;
     if (QMODE == MOE_Q_I8_ROW) sc = ((const float*)scales)[row];
     else {
@@ -372,6 +376,27 @@ __global__ void __launch_bounds__(256) dequant_rows_kernel(const uint8_t* codes,
         out[i] = (uint16_t)pack_bf16((float)(int8_t)codes[i] * sc, 0.f);
         return;
     }
+    float s[8];
+#pragma unroll
+    for (int d = 0; d < 8; ++d) s[d] = sc;
+    if (SHIFT) {
+        uint32_t r = row, c = (uint32_t)i - row * (uint32_t)cols;
+        if (c + 8 > (uint32_t)cols) {
+#pragma unroll
+            for (int d = 0; d < 8; ++d) {
+                if (c == (uint32_t)cols) {
+                    c = 0;
+                    if (i + d < n) sc = ((const float*)scales)[++r];
+                }
+                s[d] = sc;
+                ++c;
+            }
+        }
+        if (i + 8 > n) {                                                 // the tensor ends in this vector
+            for (int d = 0; i + d < n; ++d) out[i + d] = (uint16_t)pack_bf16((float)(int8_t)codes[i + d] * s[d], 0.f);
+            return;
+        }
+    }
     const uint2 c = *(const uint2*)(codes + i);
     i32x4 o;
 #pragma unroll
@@ -379,21 +404,23 @@ __global__ void __launch_bounds__(256) dequant_rows_kernel(const uint8_t* codes,
         const uint32_t w = (d < 2 ? c.x : c.y) >> (16 * (d & 1));
         const float a = QMODE == MOE_Q_I8_ROW ? (float)(int8_t)w : e4m3_to_f32(w & 0xFF);
         const float b = QMODE == MOE_Q_I8_ROW ? (float)(int8_t)(w >> 8) : e4m3_to_f32((w >> 8) & 0xFF);
-        o[d] = (int)pack_bf16(a * sc, b * sc);
+        o[d] = (int)pack_bf16(a * s[2 * d], b * s[2 * d + 1]);
     }
     *(i32x4*)(out + i) = o;
 }
 
 int norm_max_cols() { return 16384; }
 
-// A wave per row needs no exchange through LDS; a workgroup per row reads a row
-// sooner. Measured (norm with int8 rows, us): 16384 x 512 int8 rows alone 10.8
-// a wave, 19.4 a workgroup; 16384 x 1112 42 and 47; 16384 x 2048 57 and 59; 1 x
-// 2048 6.6 and 5.0; 512 x 2048 8.6 and 6.8; 1000 x 2048 11.3 and 9.1.
+// A wave per row needs no exchange through LDS and leaves no threads idle on
+// short rows; a workgroup per row spreads few rows over more CUs. Measured (us,
+// a wave / a workgroup a row): int8 rows alone 8192 x 512 5.0 / 11.0, 1536 x 512
+// 4.1 / 4.4; norm with int8 rows 1024 x 512 4.5 / 5.4, 512 x 768 5.5 / 4.3, 1024
+// x 2048 10.7 / 7.6, 2048 x 2048 13.4 / 11.6, 4096 x 2048 18.4 / 19.5, 4096 x
+// 1032 14.5 / 15.6.
 template <bool NORM, bool SHIFT>
 static hipError_t launch_vec(const NormArgs& p, int nvec, int kid, hipStream_t stream) {
     const dim3 b(256), R((unsigned)p.rows), R4(((unsigned)p.rows + 3) / 4);
-    if (nvec <= 256 && p.rows >= 1024) {
+    if (nvec <= 256 && p.rows >= (nvec <= 128 ? 1024 : 2049)) {
         if (nvec <= 64) MOE_LAUNCH(kid, stream, (norm_vec_kernel<64, 1, NORM, SHIFT>), R4, b, 0, stream, p);
         else if (nvec <= 128) MOE_LAUNCH(kid, stream, (norm_vec_kernel<64, 2, NORM, SHIFT>), R4, b, 0, stream, p);
         else MOE_LAUNCH(kid, stream, (norm_vec_kernel<64, 4, NORM, SHIFT>), R4, b, 0, stream, p);
@@ -427,15 +454,17 @@ hipError_t launch_quant_rows(const uint16_t* x, int rows, int cols, int8_t* code
 }
 
 hipError_t launch_dequant_rows(const uint8_t* codes, const void* scales, int rows, int cols, int qmode, uint16_t* out,
-                               bool vec, hipStream_t stream) {
+                               bool aligned, hipStream_t stream) {
     const size_t n = (size_t)rows * cols;
-    const dim3 g((unsigned)((n + (vec ? 2047 : 255)) / (vec ? 2048 : 256))), b(256);
+    const dim3 g((unsigned)((n + (aligned ? 2047 : 255)) / (aligned ? 2048 : 256))), b(256);
     if (qmode == MOE_Q_FP8_G128_POW2)
-        MOE_LAUNCH(K_DEQUANT_ROWS, stream, (dequant_rows_kernel<MOE_Q_FP8_G128_POW2, false>), g, b, 0, stream, codes, scales, cols, n, out);
-    else if (vec)
-        MOE_LAUNCH(K_DEQUANT_ROWS, stream, (dequant_rows_kernel<MOE_Q_I8_ROW, false>), g, b, 0, stream, codes, scales, cols, n, out);
+        MOE_LAUNCH(K_DEQUANT_ROWS, stream, (dequant_rows_kernel<MOE_Q_FP8_G128_POW2, false, false>), g, b, 0, stream, codes, scales, cols, n, out);
+    else if (!aligned)
+        MOE_LAUNCH(K_DEQUANT_ROWS, stream, (dequant_rows_kernel<MOE_Q_I8_ROW, true, false>), g, b, 0, stream, codes, scales, cols, n, out);
+    else if (cols % 8)
+        MOE_LAUNCH(K_DEQUANT_ROWS, stream, (dequant_rows_kernel<MOE_Q_I8_ROW, false, true>), g, b, 0, stream, codes, scales, cols, n, out);
     else
-        MOE_LAUNCH(K_DEQUANT_ROWS, stream, (dequant_rows_kernel<MOE_Q_I8_ROW, true>), g, b, 0, stream, codes, scales, cols, n, out);
+        MOE_LAUNCH(K_DEQUANT_ROWS, stream, (dequant_rows_kernel<MOE_Q_I8_ROW, false, false>), g, b, 0, stream, codes, scales, cols, n, out);
     return hipGetLastError();
 }
 

@@ -181,3 +181,28 @@ def test_norm_refuses_a_y_that_it_would_not_write(gpu):
     x = torch.zeros(4, 64, dtype=torch.bfloat16, device=gpu)
     with pytest.raises(moe.MoeError):
         moe.norm(x, res=x, with_y=False, y=torch.empty_like(x))
+
+
+@pytest.mark.parametrize("T,H", [(2049, 1032), (2050, 2047), (2100, 2048), (2060, 1025)])
+def test_norm_codes_are_exact_in_many_long_rows(gpu, T, H):
+    """From 2049 rows on a wave takes rows of more than 1024 columns too."""
+    test_norm_codes_are_exact(gpu, T, H)
+    if H % 128 == 0:
+        test_norm_e4m3_codes_are_exact(gpu, T, H)
+
+
+@pytest.mark.parametrize("T,H", [(1, 1), (9, 1), (40, 2), (33, 7), (70, 9), (1001, 333), (5, 4099)])
+@pytest.mark.parametrize("shift", [0, 1])
+def test_dequant_rows_of_any_length(gpu, T, H, shift):
+    """Eight values at a time over rows of any length: several rows in one vector, a tensor that ends inside one."""
+    import torch
+    r = _rng(T, H, 61)
+    buf = torch.zeros(T * H + shift, dtype=torch.int8, device=gpu)
+    codes = buf[shift:].view(T, H)
+    codes.copy_(torch.from_numpy(r.integers(-128, 128, (T, H)).astype(np.int8)))
+    scales = _f32(np.exp(r.normal(size=T)), gpu)
+    guard = torch.full((T * H + 64,), 7.0, dtype=torch.bfloat16, device=gpu)
+    out = moe.dequant_rows(codes, scales, out=guard[:T * H].view(T, H))
+    torch.cuda.synchronize()
+    want = (codes.float() * scales[:, None]).to(torch.bfloat16)      # one product, one rounding: the same bits
+    assert torch.equal(out, want) and (guard[T * H:] == 7).all()
