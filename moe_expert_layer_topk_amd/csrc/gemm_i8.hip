@@ -65,7 +65,7 @@ static __device__ __forceinline__ void barrier_lds() {
 // through L2 19; 10357 x 752 x 208 with the addend 11.2 and 10.2). Accesses
 // that are not aligned to their size are split by the memory pipeline, which
 // is still fewer than one for each value (5324 x 437 x 1408 with the addend
-// 24.2 us one by one, 15.7 so; 4096 x 1999 x 2048 25.1 and 21.3).
+// 24.2 us one by one, 16.3 so; 4096 x 1999 x 2048 25.1 and 21.5).
 template <int NC, bool F32, bool ANY = false>
 struct Cols {
     typedef uint32_t word __attribute__((ext_vector_type(NC == 2 && !F32 ? 1 : NC * (F32 ? 4 : 2) / 4 < 4 ? NC * (F32 ? 4 : 2) / 4 : 4)));
@@ -103,20 +103,29 @@ struct Cols {
         }
     }
 };
-// the columns of them that exist, one by one
+// the columns of them that exist, one by one: addends, outputs. Up to four
+// columns load without a branch (past the row's end its last addend), so that
+// no load waits in a branch of its own (10357 x 755 x 208 with the addend 18.5
+// -> 14.5 us); with eight the addresses would take registers from the step loop
+// of a 256 x 256 tile (8192 x 8191 x 8192 408 -> 452 us).
 template <int NC, bool F32>
-__device__ __forceinline__ void store_each(const GemmArgs& p, int row, int col, float (&v)[NC]) {
+__device__ __forceinline__ void add_each(const GemmArgs& p, int row, int col, float (&v)[NC]) {
+    const size_t o = (size_t)min(row, p.M - 1) * p.N;
+#pragma unroll
+    for (int n = 0; n < NC; ++n) {
+        if (NC > 4 && col + n >= p.N) continue;
+        const size_t i = o + min(col + n, p.N - 1);
+        v[n] += F32 ? ((const float*)p.add)[i] : bf16_to_f32(((const uint16_t*)p.add)[i]);
+    }
+}
+template <int NC, bool F32>
+__device__ __forceinline__ void store_each(const GemmArgs& p, int row, int col, const float (&v)[NC]) {
     const size_t o = (size_t)row * p.N + col;
 #pragma unroll
     for (int n = 0; n < NC; ++n) {
         if (col + n >= p.N) continue;
-        if (F32) {
-            if (p.add) v[n] += ((const float*)p.add)[o + n];
-            ((float*)p.out)[o + n] = v[n];
-        } else {
-            if (p.add) v[n] += bf16_to_f32(((const uint16_t*)p.add)[o + n]);
-            ((uint16_t*)p.out)[o + n] = (uint16_t)pack_bf16(v[n], 0.f);
-        }
+        if (F32) ((float*)p.out)[o + n] = v[n];
+        else ((uint16_t*)p.out)[o + n] = (uint16_t)pack_bf16(v[n], 0.f);
     }
 }
 
@@ -168,7 +177,7 @@ struct Operand {
     }
 };
 
-template <int TM, int TN, int WM, int WN, bool GLU, bool F32>
+template <int TM, int TN, int WM, int WN, bool GLU, bool F32, bool ANY>
 __global__ void __launch_bounds__(64 * WM * WN, 2) gemm_tile_kernel(GemmArgs p, int tiles_m, int tiles_n) {
     constexpr int WAVES = WM * WN;
     constexpr int MF = TM / WM / 16, NF = TN / WN / 16;
@@ -331,10 +340,8 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gemm_tile_kernel(GemmArgs p, 
         }
         static_assert((NK - 1 - BAR) / LS >= NL - 1 && NK - BAR + 1 > NR, "every load and read has its instruction");
     };
-    // KIND 0: rows of whole lines, 1: with the addend, 2 and 3: any rows
-    auto rows_out = [&](const float* md, auto kind) __attribute__((always_inline)) {
-        constexpr int KIND = decltype(kind)::value;
-        constexpr bool ANY = KIND >= 2, ADD = KIND & 1;
+    auto rows_out = [&](const float* md, auto with_add) __attribute__((always_inline)) {
+        constexpr bool ADD = decltype(with_add)::value;
         const int ln = opaque_lane(), m = ln & 15, q = ln >> 4;
         const int cw = nw * 16 * NC + NC * m, col = col0 + cw;
         const bool full = ANY ? col + NC <= p.N : col < p.N;     // all of the lane's columns exist
@@ -389,26 +396,36 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gemm_tile_kernel(GemmArgs p, 
                 if (row < p.M && full) Cols<NC, F32, ANY>::store(p.out, (size_t)row * p.N + col, v);
             }
         }
-        if (!ANY || __ballot(!full && col < p.N) == 0) return;   // a wave in which the output's rows end inside a lane
+        // a wave in which the output's rows end inside a lane: that lane's
+        // columns (the addends of RB rows before their stores, which could be
+        // the same memory: one after the other, each would wait for memory)
+        if (!ANY || __ballot(!full && col < p.N) == 0) return;
+        constexpr int RB = NC <= 4 ? 4 : 1;
 #pragma unroll
         for (int a = 0; a < MF; ++a) {
             const f32x4 sa = *(const f32x4*)(md + 16 * (mw * MF + a) + 4 * q);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int row = row0 + 16 * (mw * MF + a) + 4 * q + i;
-                float v[NC];
-                values(a, i, sa[i], v);
-                if (row < p.M && !full) store_each<NC, F32>(p, row, col, v);
+            for (int i0 = 0; i0 < 4; i0 += RB) {
+                const int row = row0 + 16 * (mw * MF + a) + 4 * q + i0;
+                float v[RB][NC];
+                __builtin_amdgcn_sched_barrier(0);       // (every row's values at once would spill)
+#pragma unroll
+                for (int i = 0; i < RB; ++i) values(a, i0 + i, sa[i0 + i], v[i]);
+                if (full) continue;
+                if constexpr (ADD) {
+#pragma unroll
+                    for (int i = 0; i < RB; ++i) add_each<NC, F32>(p, row + i, col, v[i]);
+                }
+#pragma unroll
+                for (int i = 0; i < RB; ++i)
+                    if (row + i < p.M) store_each<NC, F32>(p, row + i, col, v[i]);
             }
         }
     };
     auto epilogue = [&](int slot) __attribute__((always_inline)) {
         const float* md = s_meta + slot * META;
-        if (!GLU && p.add) {
-            if (p.lines) rows_out(md, IC<GLU ? 0 : 1>{});
-            else rows_out(md, IC<GLU ? 2 : 3>{});
-        } else if (p.lines) rows_out(md, IC<0>{});
-        else rows_out(md, IC<2>{});
+        if (!GLU && p.add) rows_out(md, IC<!GLU>{});
+        else rows_out(md, IC<0>{});
     };
 
     setup(0);
@@ -604,7 +621,10 @@ __global__ void __launch_bounds__(64 * WK) gemm_split_kernel(GemmArgs p, int til
                 plus.add_to(v);
             }
             Cols<4, F32, true>::store(p.out, o, v);
-        } else store_each<4, F32>(p, row0 + r, col0 + c, v);
+        } else {
+            if (!GLU && p.add) add_each<4, F32>(p, row0 + r, col0 + c, v);
+            store_each<4, F32>(p, row0 + r, col0 + c, v);
+        }
     }
 }
 
@@ -621,17 +641,17 @@ static hipError_t allow_lds(const void* kernel, int bytes, std::atomic<uint64_t>
     return e;
 }
 
-template <int TM, int TN, int WM, int WN, bool GLU, bool F32>
+template <int TM, int TN, int WM, int WN, bool GLU, bool F32, bool ANY>
 static hipError_t launch_tile(const GemmArgs& p, int kid, hipStream_t stream) {
     constexpr int OUTN = GLU ? TN / 2 : TN;
     constexpr int SMEM = 2 * (TM + TN) * 128 + 8 * (TM + 2 * TN);
     constexpr int PER_CU = 163840 / SMEM < 8 / (WM * WN) ? 163840 / SMEM : 8 / (WM * WN);
     static std::atomic<uint64_t> done{0};
-    const hipError_t e = allow_lds((const void*)gemm_tile_kernel<TM, TN, WM, WN, GLU, F32>, SMEM, done);
+    const hipError_t e = allow_lds((const void*)gemm_tile_kernel<TM, TN, WM, WN, GLU, F32, ANY>, SMEM, done);
     if (e != hipSuccess) return e;
     const int tm = (p.M + TM - 1) / TM, tn = (p.N + OUTN - 1) / OUTN;
     const int slots = (device_cus() * PER_CU + 7) / 8 * 8, grid = min(slots, (tm * tn + 7) / 8 * 8);
-    MOE_LAUNCH(kid, stream, (gemm_tile_kernel<TM, TN, WM, WN, GLU, F32>), dim3((unsigned)grid), dim3(64 * WM * WN),
+    MOE_LAUNCH(kid, stream, (gemm_tile_kernel<TM, TN, WM, WN, GLU, F32, ANY>), dim3((unsigned)grid), dim3(64 * WM * WN),
                SMEM, stream, p, tm, tn);
     return hipGetLastError();
 }
@@ -694,8 +714,12 @@ static int pick_shape(int M, long long rows_b, int K) {
 template <bool GLU, bool F32>
 static hipError_t launch_any(const GemmArgs& p, int kid, hipStream_t stream) {
     switch (pick_shape(p.M, (long long)p.N * (GLU ? 2 : 1), p.K)) {
-        case S_256x256: return launch_tile<256, 256, 4, 2, GLU, F32>(p, kid, stream);
-        case S_128x128: return launch_tile<128, 128, 2, 2, GLU, F32>(p, kid, stream);
+        case S_256x256:
+            return p.lines ? launch_tile<256, 256, 4, 2, GLU, F32, false>(p, kid, stream)
+                           : launch_tile<256, 256, 4, 2, GLU, F32, true>(p, kid, stream);
+        case S_128x128:
+            return p.lines ? launch_tile<128, 128, 2, 2, GLU, F32, false>(p, kid, stream)
+                           : launch_tile<128, 128, 2, 2, GLU, F32, true>(p, kid, stream);
         case S_64x64: return launch_split<64, 64, 4, 4, GLU, F32>(p, kid, stream);
         case S_32x64: return launch_split<32, 64, 8, 4, GLU, F32>(p, kid, stream);
         default: return launch_split<32, 32, 8, 4, GLU, F32>(p, kid, stream);
