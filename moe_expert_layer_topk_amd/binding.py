@@ -1,8 +1,9 @@
-"""ctypes binding over libmoe.so (include/moe.h): argument marshalling only.
+"""Python binding over libmoe.so (include/moe.h): argument marshalling only,
+through ctypes and, for the dense operators, _marshal.so (csrc/marshal.cpp).
 
 Every step of the layer runs in the library's HIP kernels. PyTorch supplies
 device memory and the current stream; outputs the caller does not pass are
-allocated with torch before the call. If the library is missing the first
+allocated with torch before the call. If a library is missing the first
 call raises: there is no other implementation to fall back to.
 """
 import ctypes

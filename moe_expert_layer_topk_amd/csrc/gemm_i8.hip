@@ -149,10 +149,10 @@ __device__ __forceinline__ void store_each(const GemmArgs& p, int row, int col, 
 // (2.4 GHz on zeros, 1.4 times as fast), with the matrix pipe busy about 80% of
 // the clocks. So what counts is energy per output: 16x16x64 instructions
 // (registers only: 3950 TOPS on random codes; 32x32x32: 2920), tiles as large
-// as LDS allows, few instructions beside the matrix ones. 8192^3: 416 us, 2640
+// as LDS allows, few instructions beside the matrix ones. 8192^3: 408 us, 2690
 // TOPS (a library product with int32 output on the same card 457-465 us); 4096
-// x 8192 x 8192 208 us (253); 16384 x 2048 x 2048 63 us (81); gated 16384 x 512
-// x 2048 31.5 us. Measured without gain: three or four stages of a 128-wide
+// x 8192 x 8192 210 us (253); 16384 x 2048 x 2048 61 us (81); gated 16384 x 512
+// x 2048 30.4 us. Measured without gain: three or four stages of a 128-wide
 // tile, four 128 x 128 waves (the compiler spills), places of the barrier and
 // the loads between the matrix instructions.
 template <int V>
@@ -674,10 +674,10 @@ static hipError_t launch_split(const GemmArgs& p, int kid, hipStream_t stream) {
 // round's prologue and epilogue (`round`). Large tiles move fewer bytes per
 // output, small ones reach more CUs. The figures are a fit to 400 products
 // with random sizes (1..16384 rows, 64..8192 columns, K 128..8192), each timed
-// with every shape: the shape picked by them is 1.8% slower than the best of
-// the five on average. E.g. 333 x 1000 x 4112: 32x64 9.6 us, 128x128 26;
-// 2048^3: 128x128 16 us, 256x256 26, 64x64 23; 16384 x 2048 x 2048: 256x256 64
-// us, 128x128 73. 256x128, 128x64 and 64x32 tiles were measured beside these
+// with every shape: on 500 others the shape picked by them is 2.1% slower than
+// the best of the five on average. E.g. 333 x 1000 x 4112: 32x64 9.2 us,
+// 128x128 24; 2048^3: 128x128 15 us, 256x256 24, 64x64 21.5; 16384 x 2048 x
+// 2048: 256x256 59 us, 128x128 65. 256x128, 128x64 and 64x32 tiles were measured beside these
 // and gain less than 1% together.
 struct Shape {
     int tm, tn, per_cu;
