@@ -130,3 +130,24 @@ def test_rows_past_2_to_the_32(gpu, T, H):
     else:
         with pytest.raises(moe.MoeError):                             # one thread a value: below 2^31
             moe.dequant_rows(codes, scales)
+
+
+@pytest.mark.parametrize("M,N", [((1 << 26) + 1, 1), ((1 << 25) + 3, 5), (1, (1 << 26) + 3), (2, (1 << 25) + 1)])
+def test_products_one_side_of_which_is_very_long(gpu, M, N):
+    """Outputs narrower than a lane's columns, and a million tiles in a row."""
+    import torch
+    K = 16
+    _say(f"[long product] {M} x {N}")
+    a, b = _codes(gpu, M, K, 7), _codes(gpu, N, K, 8)
+    sa, sb = torch.ones(M, device=gpu), torch.ones(N, device=gpu)
+    add = torch.full((M, N), 0.5, device=gpu)
+    out = moe.gemm_i8(a, sa, b, sb, add=add, out_dtype=torch.float32)
+    want = a.float() @ b.float().t() + 0.5                            # below 2^19 and a half: exact in fp32
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+    w13 = torch.cat([b, b.flip(0)])
+    h = moe.glu_i8(a, sa * 2.0 ** -9, w13, torch.cat([sb, sb]))
+    pick = _rows_around(M, 1, 1 << 25) if M > N else sorted({0, M - 1})
+    few = moe.glu_i8(a[pick].contiguous(), sa[:len(pick)] * 2.0 ** -9, w13, torch.cat([sb, sb]))
+    torch.cuda.synchronize()
+    assert torch.equal(h[pick], few)
