@@ -9,9 +9,10 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
-#include <ATen/hip/EmptyTensor.h>
+#include <ATen/EmptyTensor.h>
+#include <ATen/hip/impl/HIPCachingAllocatorMasqueradingAsCUDA.h>
 #include <ATen/hip/impl/HIPStreamMasqueradingAsCUDA.h>
-#include <c10/core/DeviceGuard.h>
+#include <c10/hip/HIPFunctions.h>
 
 #include <string>
 
@@ -48,6 +49,18 @@ bool plain(const at::Tensor& t, at::ScalarType type) {
     return t.is_cuda() && t.scalar_type() == type && t.layout() == at::kStrided && t.is_contiguous() && !t.is_neg() &&
            !t.is_conj();
 }
+
+// a device made current, and the one before it again at the end
+struct Current {
+    c10::DeviceIndex before, now;
+    explicit Current(c10::Device d) : before(c10::hip::current_device()), now(d.index()) {
+        if (now != before) c10::hip::set_device(now);
+    }
+    ~Current() {
+        if (now != before) (void)hipSetDevice(before);
+    }
+    Current(const Current&) = delete;
+};
 
 struct Matrix {
     const at::Tensor& t;
@@ -94,25 +107,24 @@ struct Out {
             p = beside(t, m, rows, cols, type, name);
             return;
         }
-        // (the allocator's own entry: past the dispatcher, which takes longer than it)
+        // (past the dispatcher, which takes longer than the allocator; m's device is current)
         const int64_t size[2] = {rows, cols};
-        t = at::detail::empty_cuda(at::IntArrayRef(size, cols < 0 ? 1 : 2), type, m.dev, std::nullopt);
+        t = at::detail::empty_generic(at::IntArrayRef(size, cols < 0 ? 1 : 2),
+                                      c10::hip::HIPCachingAllocatorMasqueradingAsCUDA::get(),
+                                      c10::DispatchKeySet(c10::DispatchKey::CUDA), type, std::nullopt);
         p = t.data_ptr();
     }
 };
 
-// the call with its device current, on that device's current stream; the GIL is free meanwhile
+// the call on the (current) device's current stream; the GIL is free meanwhile
 template <typename F>
 void run(const Matrix& m, F call) {
     int status, hip = 0;
-    {
-        c10::DeviceGuard guard(m.dev);
-        void* stream = (void*)c10::hip::getCurrentHIPStreamMasqueradingAsCUDA(m.dev.index()).stream();
-        Py_BEGIN_ALLOW_THREADS
-        status = call(stream);
-        if (status != MOE_OK) hip = moe_last_hip_error();
-        Py_END_ALLOW_THREADS
-    }
+    void* stream = (void*)c10::hip::getCurrentHIPStreamMasqueradingAsCUDA(m.dev.index()).stream();
+    Py_BEGIN_ALLOW_THREADS
+    status = call(stream);
+    if (status != MOE_OK) hip = moe_last_hip_error();
+    Py_END_ALLOW_THREADS
     if (status != MOE_OK)
         refuse(std::string("libmoe: ") + moe_strerror(status) + " (status " + std::to_string(status) + ", hip error " +
                std::to_string(hip) + ")");
@@ -145,6 +157,7 @@ PyObject* py_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
     count(n, 10, "norm");
     const Matrix x = matrix(a[0], BF16, "x");
+    const Current on(x.dev);
     const int T = x.rows, H = x.cols;
     const float* w = (const float*)given(a[1], x, H, -1, F32, "weight");
     const double eps = PyFloat_AsDouble(a[2]);
@@ -177,6 +190,7 @@ PyObject* py_quant_rows(PyObject*, PyObject* const* a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
     count(n, 3, "quant_rows");
     const Matrix x = matrix(a[0], BF16, "x");
+    const Current on(x.dev);
     const Out codes(a[1], x, x.rows, x.cols, I8, "codes"), scales(a[2], x, x.rows, -1, F32, "scales");
     run(x, [&](void* st) {
         return moe_quant_rows((const uint16_t*)x.t.data_ptr(), x.rows, x.cols, (int8_t*)codes.p, (float*)scales.p, st);
@@ -192,6 +206,7 @@ PyObject* py_dequant_rows(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor& t = tensor(a[0], "codes");
     const bool i8 = t.defined() && t.scalar_type() == I8;
     const Matrix c = matrix(a[0], i8 ? I8 : U8, "codes");
+    const Current on(c.dev);
     const void* scales = i8 ? needed(a[1], c, c.rows, -1, F32, "scales") : needed(a[1], c, c.rows, c.cols / 128, U8, "scales");
     const Out out(a[2], c, c.rows, c.cols, BF16, "out");
     run(c, [&](void* st) {
@@ -213,6 +228,7 @@ PyObject* py_gemm_i8(PyObject*, PyObject* const* v, Py_ssize_t n) {
     count(n, 8, "gemm_i8");
     const Matrix a = matrix(v[0], I8, "a"), b = matrix(v[2], I8, "b");
     fit(a, b, "b");
+    const Current on(a.dev);
     at::ScalarType ot = BF16;
     if (v[7] != Py_None) {
         if (!THPDtype_Check(v[7])) refuse("out_dtype must be a dtype");
@@ -239,6 +255,7 @@ PyObject* py_glu_i8(PyObject*, PyObject* const* v, Py_ssize_t n) {
     count(n, 5, "glu_i8");
     const Matrix a = matrix(v[0], I8, "a"), w = matrix(v[2], I8, "w13");
     fit(a, w, "w13");
+    const Current on(a.dev);
     if (w.rows % 2) refuse("w13 holds gate and up rows, as many of each: got " + std::to_string(w.rows) + " rows");
     const int M = a.rows, I = w.rows / 2;
     const void* sa = needed(v[1], a, M, -1, F32, "sa");
