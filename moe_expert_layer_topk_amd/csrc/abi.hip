@@ -336,14 +336,12 @@ int moe_norm(const uint16_t* d_x, const uint16_t* d_res, const float* d_weight, 
     if (d_sum && d_sum == d_y) return MOE_EINVAL;
     const bool aligned = aligned16(d_x, d_res, d_weight, d_sum, d_y, d_codes);
     if (qmode == MOE_Q_FP8_G128_POW2 && (cols % MOE_ACT_G || !aligned)) return MOE_EINVAL;
-    clear_stale_error();
     return hip_status(moe::launch_norm(d_x, d_res, d_weight, eps, rows, cols, qmode, d_sum, d_y, d_codes, d_scales,
                                        aligned, (hipStream_t)stream));
 }
 
 int moe_quant_rows(const uint16_t* d_x, int rows, int cols, int8_t* d_codes, float* d_scales, void* stream) {
     if (!d_x || !d_codes || !d_scales || !valid_rows(rows, cols)) return MOE_EINVAL;
-    clear_stale_error();
     return hip_status(moe::launch_quant_rows(d_x, rows, cols, d_codes, d_scales, aligned16(d_x, d_codes),
                                              (hipStream_t)stream));
 }
@@ -356,7 +354,6 @@ int moe_dequant_rows(const uint8_t* d_codes, const void* d_scales, int rows, int
     if (qmode == MOE_Q_FP8_G128_POW2 && (cols % MOE_ACT_G || !aligned)) return MOE_EINVAL;
     // (a launch has fewer than 2^32 threads, each with 8 values or one; values are counted in 32 bits except in rows of whole vectors)
     if ((long long)rows * cols >= (aligned && cols % 8 == 0 ? 1LL << 34 : 1LL << 31)) return MOE_EINVAL;
-    clear_stale_error();
     return hip_status(moe::launch_dequant_rows(d_codes, d_scales, rows, cols, qmode, d_out, aligned, (hipStream_t)stream));
 }
 
@@ -364,7 +361,6 @@ int moe_gemm_i8(const int8_t* d_a, const float* d_sa, const int8_t* d_b, const f
                 const void* d_add, int M, int N, int K, int out_type, void* d_out, void* stream) {
     if (!d_a || !d_sa || !d_b || !d_sb || !d_out || !valid_product(M, N, K) || !aligned16(d_a, d_b)) return MOE_EINVAL;
     if (out_type != MOE_OUT_BF16 && out_type != MOE_OUT_F32) return MOE_EINVAL;
-    clear_stale_error();
     return hip_status(moe::launch_gemm_i8(d_a, d_sa, d_b, d_sb, d_bias, d_add, M, N, K, out_type == MOE_OUT_F32, d_out,
                                           aligned16(d_out, d_add), (hipStream_t)stream));
 }
@@ -373,7 +369,6 @@ int moe_glu_i8(const int8_t* d_a, const float* d_sa, const int8_t* d_w13, const 
                uint16_t* d_h, void* stream) {
     if (!d_a || !d_sa || !d_w13 || !d_s13 || !d_h || !valid_product(M, I, K) || !aligned16(d_a, d_w13))
         return MOE_EINVAL;
-    clear_stale_error();
     return hip_status(moe::launch_glu_i8(d_a, d_sa, d_w13, d_s13, M, I, K, d_h, aligned16(d_h), (hipStream_t)stream));
 }
 

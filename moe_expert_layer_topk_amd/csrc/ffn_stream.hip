@@ -1346,10 +1346,14 @@ int stream_max_tokens() { return STREAM_MAX_T; }
 
 // compute units of the current device (cached per device id)
 int device_cus() {
+    int dev = 0;
+    return hipGetDevice(&dev) == hipSuccess ? device_cus(dev) : 256;
+}
+
+int device_cus(int dev) {
     // per device, filled once; racing callers store the same value
     static std::atomic<int> cached[64];
-    int dev = 0;
-    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 256;
+    if (dev < 0 || dev >= 64) return 256;
     int c = cached[dev].load(std::memory_order_relaxed);
     if (c <= 0) {
         int n = 0;

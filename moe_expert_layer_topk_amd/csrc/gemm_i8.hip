@@ -631,42 +631,38 @@ __global__ void __launch_bounds__(64 * WK) gemm_split_kernel(GemmArgs p, int til
 // ------------------------------------------------------------------ launch
 // Raises a kernel's dynamic LDS limit, once for each device (the call costs
 // more than the launch's other checks together; racing callers repeat it).
-static hipError_t allow_lds(const void* kernel, int bytes, std::atomic<uint64_t>& done) {
-    int dev = 0;
-    hipError_t e = hipGetDevice(&dev);
+static hipError_t allow_lds(const void* kernel, int bytes, int dev, std::atomic<uint64_t>& done) {
     const uint64_t bit = 1ull << (dev & 63);
-    if (e != hipSuccess || (dev < 64 && (done.load(std::memory_order_relaxed) & bit))) return e;
-    e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (dev < 64 && (done.load(std::memory_order_relaxed) & bit)) return hipSuccess;
+    const hipError_t e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e == hipSuccess && dev < 64) done.fetch_or(bit, std::memory_order_relaxed);
     return e;
 }
 
 template <int TM, int TN, int WM, int WN, bool GLU, bool F32, bool ANY>
-static hipError_t launch_tile(const GemmArgs& p, int kid, hipStream_t stream) {
+static hipError_t launch_tile(const GemmArgs& p, int dev, int kid, hipStream_t stream) {
     constexpr int OUTN = GLU ? TN / 2 : TN;
     constexpr int SMEM = 2 * (TM + TN) * 128 + 8 * (TM + 2 * TN);
     constexpr int PER_CU = 163840 / SMEM < 8 / (WM * WN) ? 163840 / SMEM : 8 / (WM * WN);
     static std::atomic<uint64_t> done{0};
-    const hipError_t e = allow_lds((const void*)gemm_tile_kernel<TM, TN, WM, WN, GLU, F32, ANY>, SMEM, done);
+    const hipError_t e = allow_lds((const void*)gemm_tile_kernel<TM, TN, WM, WN, GLU, F32, ANY>, SMEM, dev, done);
     if (e != hipSuccess) return e;
     const int tm = (p.M + TM - 1) / TM, tn = (p.N + OUTN - 1) / OUTN;
-    const int slots = (device_cus() * PER_CU + 7) / 8 * 8, grid = min(slots, (tm * tn + 7) / 8 * 8);
-    MOE_LAUNCH(kid, stream, (gemm_tile_kernel<TM, TN, WM, WN, GLU, F32, ANY>), dim3((unsigned)grid), dim3(64 * WM * WN),
-               SMEM, stream, p, tm, tn);
-    return hipGetLastError();
+    const int slots = (device_cus(dev) * PER_CU + 7) / 8 * 8, grid = min(slots, (tm * tn + 7) / 8 * 8);
+    return launch_kernel(kid, stream, gemm_tile_kernel<TM, TN, WM, WN, GLU, F32, ANY>, dim3((unsigned)grid),
+                         dim3(64 * WM * WN), SMEM, p, tm, tn);
 }
 
 template <int TM, int TN, int WK, int R, bool GLU, bool F32>
-static hipError_t launch_split(const GemmArgs& p, int kid, hipStream_t stream) {
+static hipError_t launch_split(const GemmArgs& p, int dev, int kid, hipStream_t stream) {
     constexpr int OUTN = GLU ? TN / 2 : TN;
     constexpr int SMEM = R * (TM + TN) * 32 * WK + 256 * ((TM + 63) / 64 + 2 * ((TN + 63) / 64));
     static std::atomic<uint64_t> done{0};
-    const hipError_t e = allow_lds((const void*)gemm_split_kernel<TM, TN, WK, R, GLU, F32>, SMEM, done);
+    const hipError_t e = allow_lds((const void*)gemm_split_kernel<TM, TN, WK, R, GLU, F32>, SMEM, dev, done);
     if (e != hipSuccess) return e;
     const int tm = (p.M + TM - 1) / TM, tn = (p.N + OUTN - 1) / OUTN;
-    MOE_LAUNCH(kid, stream, (gemm_split_kernel<TM, TN, WK, R, GLU, F32>), dim3((unsigned)(tm * tn)), dim3(64 * WK),
-               SMEM, stream, p, tm, tn);
-    return hipGetLastError();
+    return launch_kernel(kid, stream, gemm_split_kernel<TM, TN, WK, R, GLU, F32>, dim3((unsigned)(tm * tn)),
+                         dim3(64 * WK), SMEM, p, tm, tn);
 }
 
 // The tile shapes, and what they cost (us): a K step of 128 with at most one
@@ -692,8 +688,7 @@ static const Shape kShapes[S_COUNT] = {{256, 256, 1, 1.17f, 1.17f, 2.6f},
 
 // The shape that the costs above make the fastest for this many output rows
 // and B rows.
-static int pick_shape(int M, long long rows_b, int K) {
-    const long long cus = device_cus();
+static int pick_shape(int M, long long rows_b, int K, long long cus) {
     const float steps = (float)((K + 127) / 128);
     int best = 0;
     float least = 3.4e38f;
@@ -713,16 +708,19 @@ static int pick_shape(int M, long long rows_b, int K) {
 
 template <bool GLU, bool F32>
 static hipError_t launch_any(const GemmArgs& p, int kid, hipStream_t stream) {
-    switch (pick_shape(p.M, (long long)p.N * (GLU ? 2 : 1), p.K)) {
+    int dev = 0;
+    const hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess) return e;
+    switch (pick_shape(p.M, (long long)p.N * (GLU ? 2 : 1), p.K, device_cus(dev))) {
         case S_256x256:
-            return p.lines ? launch_tile<256, 256, 4, 2, GLU, F32, false>(p, kid, stream)
-                           : launch_tile<256, 256, 4, 2, GLU, F32, true>(p, kid, stream);
+            return p.lines ? launch_tile<256, 256, 4, 2, GLU, F32, false>(p, dev, kid, stream)
+                           : launch_tile<256, 256, 4, 2, GLU, F32, true>(p, dev, kid, stream);
         case S_128x128:
-            return p.lines ? launch_tile<128, 128, 2, 2, GLU, F32, false>(p, kid, stream)
-                           : launch_tile<128, 128, 2, 2, GLU, F32, true>(p, kid, stream);
-        case S_64x64: return launch_split<64, 64, 4, 4, GLU, F32>(p, kid, stream);
-        case S_32x64: return launch_split<32, 64, 8, 4, GLU, F32>(p, kid, stream);
-        default: return launch_split<32, 32, 8, 4, GLU, F32>(p, kid, stream);
+            return p.lines ? launch_tile<128, 128, 2, 2, GLU, F32, false>(p, dev, kid, stream)
+                           : launch_tile<128, 128, 2, 2, GLU, F32, true>(p, dev, kid, stream);
+        case S_64x64: return launch_split<64, 64, 4, 4, GLU, F32>(p, dev, kid, stream);
+        case S_32x64: return launch_split<32, 64, 8, 4, GLU, F32>(p, dev, kid, stream);
+        default: return launch_split<32, 32, 8, 4, GLU, F32>(p, dev, kid, stream);
     }
 }
 

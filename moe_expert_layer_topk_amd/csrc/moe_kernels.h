@@ -4,6 +4,7 @@
 #include <hip/hip_ext.h>
 #include <stddef.h>
 #include <stdint.h>
+#include <tuple>
 
 namespace moe {
 
@@ -26,6 +27,25 @@ bool prof_events(int kid, hipStream_t s, hipEvent_t* start, hipEvent_t* stop);
         else                                                                                            \
             hipLaunchKernelGGL(kernel, grid, block, shmem, strm, __VA_ARGS__);                          \
     } while (0)
+
+// The same as a function, for calls of a few microseconds: the launch's own
+// status instead of the last error (two lookups fewer, and no launch
+// configuration pushed and popped: 0.2 us of host time).
+template <typename... P, typename... A>
+inline hipError_t launch_kernel(int kid, hipStream_t stream, void (*kernel)(P...), dim3 grid, dim3 block, size_t shmem, A... a) {
+    std::tuple<P...> v{a...};
+    hipEvent_t ev0, ev1;
+    return std::apply(
+        [&](auto&... p) {
+            void* args[] = {(void*)&p...};
+            const hipError_t e = prof_events(kid, stream, &ev0, &ev1)
+                ? hipExtLaunchKernel((const void*)kernel, grid, block, args, shmem, stream, ev0, ev1, 0)
+                : hipLaunchKernel((const void*)kernel, grid, block, args, shmem, stream);
+            if (e != hipSuccess) (void)hipGetLastError();        // reported here, not by the next caller's check
+            return e;
+        },
+        v);
+}
 
 struct PoolArgs {
     const void* base;
@@ -66,6 +86,7 @@ hipError_t launch_align(const int32_t* ids, int T, int k, int E, int block_m, co
 
 int stream_max_tokens();
 int device_cus();
+int device_cus(int dev);
 size_t stream_workspace_bytes(int T, int k, int H, int I, int cap);
 hipError_t launch_combine_f32(const float* ybuf, const float* topk_w, int T, int k, int H, uint16_t* out,
                               hipStream_t stream);

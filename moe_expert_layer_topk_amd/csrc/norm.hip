@@ -421,14 +421,13 @@ template <bool NORM, bool SHIFT>
 static hipError_t launch_vec(const NormArgs& p, int nvec, int kid, hipStream_t stream) {
     const dim3 b(256), R((unsigned)p.rows), R4(((unsigned)p.rows + 3) / 4);
     if (nvec <= 256 && p.rows >= (nvec <= 128 ? 1024 : 2049)) {
-        if (nvec <= 64) MOE_LAUNCH(kid, stream, (norm_vec_kernel<64, 1, NORM, SHIFT>), R4, b, 0, stream, p);
-        else if (nvec <= 128) MOE_LAUNCH(kid, stream, (norm_vec_kernel<64, 2, NORM, SHIFT>), R4, b, 0, stream, p);
-        else MOE_LAUNCH(kid, stream, (norm_vec_kernel<64, 4, NORM, SHIFT>), R4, b, 0, stream, p);
-    } else if (nvec <= 256) MOE_LAUNCH(kid, stream, (norm_vec_kernel<256, 1, NORM, SHIFT>), R, b, 0, stream, p);
-    else if (nvec <= 512) MOE_LAUNCH(kid, stream, (norm_vec_kernel<256, 2, NORM, SHIFT>), R, b, 0, stream, p);
-    else if (nvec <= 1024) MOE_LAUNCH(kid, stream, (norm_vec_kernel<256, 4, NORM, SHIFT>), R, b, 0, stream, p);
-    else MOE_LAUNCH(kid, stream, (norm_vec_kernel<256, 8, NORM, SHIFT>), R, b, 0, stream, p);
-    return hipGetLastError();
+        if (nvec <= 64) return launch_kernel(kid, stream, norm_vec_kernel<64, 1, NORM, SHIFT>, R4, b, 0, p);
+        else if (nvec <= 128) return launch_kernel(kid, stream, norm_vec_kernel<64, 2, NORM, SHIFT>, R4, b, 0, p);
+        else return launch_kernel(kid, stream, norm_vec_kernel<64, 4, NORM, SHIFT>, R4, b, 0, p);
+    } else if (nvec <= 256) return launch_kernel(kid, stream, norm_vec_kernel<256, 1, NORM, SHIFT>, R, b, 0, p);
+    else if (nvec <= 512) return launch_kernel(kid, stream, norm_vec_kernel<256, 2, NORM, SHIFT>, R, b, 0, p);
+    else if (nvec <= 1024) return launch_kernel(kid, stream, norm_vec_kernel<256, 4, NORM, SHIFT>, R, b, 0, p);
+    else return launch_kernel(kid, stream, norm_vec_kernel<256, 8, NORM, SHIFT>, R, b, 0, p);
 }
 
 template <bool NORM>
@@ -437,9 +436,8 @@ static hipError_t launch_rows(const NormArgs& p, bool aligned, int kid, hipStrea
     if (aligned && p.cols % 8 == 0) return launch_vec<NORM, false>(p, p.cols / 8, kid, stream);
     if (aligned && nvec <= 2048) return launch_vec<NORM, true>(p, nvec, kid, stream);
     const dim3 b(256), R((unsigned)p.rows);
-    if (p.cols <= 2048) MOE_LAUNCH(kid, stream, (norm_elem_kernel<8, NORM>), R, b, 0, stream, p);
-    else MOE_LAUNCH(kid, stream, (norm_elem_kernel<64, NORM>), R, b, 0, stream, p);
-    return hipGetLastError();
+    if (p.cols <= 2048) return launch_kernel(kid, stream, norm_elem_kernel<8, NORM>, R, b, 0, p);
+    else return launch_kernel(kid, stream, norm_elem_kernel<64, NORM>, R, b, 0, p);
 }
 
 hipError_t launch_norm(const uint16_t* x, const uint16_t* res, const float* w, float eps, int rows, int cols, int qmode,
@@ -458,14 +456,13 @@ hipError_t launch_dequant_rows(const uint8_t* codes, const void* scales, int row
     const size_t n = (size_t)rows * cols;
     const dim3 g((unsigned)((n + (aligned ? 2047 : 255)) / (aligned ? 2048 : 256))), b(256);
     if (qmode == MOE_Q_FP8_G128_POW2)
-        MOE_LAUNCH(K_DEQUANT_ROWS, stream, (dequant_rows_kernel<MOE_Q_FP8_G128_POW2, false, false>), g, b, 0, stream, codes, scales, cols, n, out);
+        return launch_kernel(K_DEQUANT_ROWS, stream, dequant_rows_kernel<MOE_Q_FP8_G128_POW2, false, false>, g, b, 0, codes, scales, cols, n, out);
     else if (!aligned)
-        MOE_LAUNCH(K_DEQUANT_ROWS, stream, (dequant_rows_kernel<MOE_Q_I8_ROW, true, false>), g, b, 0, stream, codes, scales, cols, n, out);
+        return launch_kernel(K_DEQUANT_ROWS, stream, dequant_rows_kernel<MOE_Q_I8_ROW, true, false>, g, b, 0, codes, scales, cols, n, out);
     else if (cols % 8)
-        MOE_LAUNCH(K_DEQUANT_ROWS, stream, (dequant_rows_kernel<MOE_Q_I8_ROW, false, true>), g, b, 0, stream, codes, scales, cols, n, out);
+        return launch_kernel(K_DEQUANT_ROWS, stream, dequant_rows_kernel<MOE_Q_I8_ROW, false, true>, g, b, 0, codes, scales, cols, n, out);
     else
-        MOE_LAUNCH(K_DEQUANT_ROWS, stream, (dequant_rows_kernel<MOE_Q_I8_ROW, false, false>), g, b, 0, stream, codes, scales, cols, n, out);
-    return hipGetLastError();
+        return launch_kernel(K_DEQUANT_ROWS, stream, dequant_rows_kernel<MOE_Q_I8_ROW, false, false>, g, b, 0, codes, scales, cols, n, out);
 }
 
 }  // namespace moe
