@@ -94,9 +94,10 @@ __device__ __forceinline__ double rcp_f64(double a) {
 
 // int8 scale of a row and the multiplier of its v w values, from the threads'
 // peaks of |v w| and the row's r (both positive: rounding keeps their order).
-// mul 0: the row holds NaN or infinity, or a value past fp32.
+// mul 0: the row holds NaN or infinity, or a value past fp32. quick: mul in
+// fp32, or 0 where a product of it could leave fp32's normal range.
 template <int TPR>
-__device__ __forceinline__ void i8_scale(Peak p, double r, double* s_max, uint32_t* s_bad, float* scale, double* mul) {
+__device__ __forceinline__ void i8_scale(Peak p, double r, double* s_max, uint32_t* s_bad, float* scale, double* mul, float* quick) {
     uint32_t bad = __ballot(p.hi >= 0x7FF00000u) != 0;
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) p.m = fmax(p.m, __shfl_xor(p.m, o, 64));
@@ -114,10 +115,12 @@ __device__ __forceinline__ void i8_scale(Peak p, double r, double* s_max, uint32
     if (bad || !(r > 0.0) || m > 3.4028234663852886e38) {
         *scale = __uint_as_float(0x7FC00000u);
         *mul = 0.0;
+        *quick = 0.f;
         return;
     }
     *scale = (float)(m * (1.0 / 127.0));
     *mul = r * (127.0 * rcp_f64(m));
+    *quick = p.m >= 0x1p-100 && p.m <= 0x1p+120 ? (float)*mul : 0.f;
 }
 // the low byte of the result is the code
 template <bool NORM>
@@ -205,6 +208,22 @@ __global__ void __launch_bounds__(256) norm_vec_kernel(NormArgs p) {
             for (int d = 0; d < 8; ++d) ss = fma((double)v[j][d], (double)v[j][d], ss);
         r = rsqrt_f64(fma(row_sum<TPR>(ss, s_sum), p.inv_cols, (double)p.eps));
     }
+    // the weights of vector j
+    auto weights = [&](int j, float (&w)[8]) __attribute__((always_inline)) {
+        int i = min(t + j * TPR, nvec - 1);
+        asm volatile("" : "+v"(i));                     // (loaded again where they are needed again)
+        if (!whole(i)) {
+            for (int d = 0; d < 8; ++d) w[d] = p.w[min(max(8 * i + d - off, 0), p.cols - 1)];
+            return;
+        }
+        typedef f32x4 f32x4_dword __attribute__((aligned(4)));       // (vector loads need whole dwords only)
+        const f32x4 w0 = *(const f32x4_dword*)(p.w + 8 * i - off), w1 = *(const f32x4_dword*)(p.w + 8 * i - off + 4);
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+            w[d] = w0[d];
+            w[4 + d] = w1[d];
+        }
+    };
     // v w of vector j (exact: two 24-bit factors), formed again where it is
     // needed; y is that times r
     auto vw_of = [&](int j, double (&u)[8]) __attribute__((always_inline)) {
@@ -214,19 +233,10 @@ __global__ void __launch_bounds__(256) norm_vec_kernel(NormArgs p) {
             u[d] = (double)v[j][d];
         }
         if (NORM && p.w) {
-            int i = min(t + j * TPR, nvec - 1);
-            asm volatile("" : "+v"(i));                 // (and the weights loaded again)
-            if (!whole(i)) {
-                for (int d = 0; d < 8; ++d) u[d] *= (double)p.w[min(max(8 * i + d - off, 0), p.cols - 1)];
-                return;
-            }
-            typedef f32x4 f32x4_dword __attribute__((aligned(4)));   // (vector loads need whole dwords only)
-            const f32x4 w0 = *(const f32x4_dword*)(p.w + 8 * i - off), w1 = *(const f32x4_dword*)(p.w + 8 * i - off + 4);
+            float w[8];
+            weights(j, w);
 #pragma unroll
-            for (int d = 0; d < 4; ++d) {
-                u[d] *= (double)w0[d];
-                u[4 + d] *= (double)w1[d];
-            }
+            for (int d = 0; d < 8; ++d) u[d] *= (double)w[d];
         }
     };
     Peak peak;
@@ -281,17 +291,37 @@ __global__ void __launch_bounds__(256) norm_vec_kernel(NormArgs p) {
     if (p.qmode == MOE_Q_I8_ROW) {
         float scale;
         double mul;                                     // 127 r / m: what v w is multiplied by
-        i8_scale<TPR>(peak, r, s_max, s_bad, &scale, &mul);
+        float quick;
+        i8_scale<TPR>(peak, r, s_max, s_bad, &scale, &mul, &quick);
         if (t == 0) ((float*)p.scales)[row] = scale;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             if (j * TPR >= nvec) break;
             const int i = t + j * TPR;
-            double u[8];
-            vw_of(j, u);
-            uint32_t o[2] = {0, 0};
+            // In fp32 first: z is within 3 2^-24 of its value, so the code is
+            // certain where z is 2^-22 of itself and more away from a border
+            // (z + 3 2^22 is rounded to an integer, in its low byte).
+            float w[8];
+            if (NORM && p.w) weights(j, w);
+            bool redo = quick == 0.f;
+            uint32_t f[8], o[2];
 #pragma unroll
-            for (int d = 0; d < 8; ++d) o[d / 4] |= (uint32_t)(i8_code<NORM>(u[d], mul) & 0xFF) << (8 * (d % 4));
+            for (int d = 0; d < 8; ++d) {
+                const float z = (NORM && p.w ? v[j][d] * w[d] : v[j][d]) * quick, n = z + 12582912.f;
+                redo |= fmaf(fabsf(z), 0x1p-22f, fabsf(z - (n - 12582912.f))) > 0.5f;
+                f[d] = __float_as_uint(n);
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h)                 // (byte 0 of each)
+                o[h] = __builtin_amdgcn_perm(__builtin_amdgcn_perm(f[4 * h + 3], f[4 * h + 2], 0x0C0C0400u),
+                                             __builtin_amdgcn_perm(f[4 * h + 1], f[4 * h], 0x0C0C0400u), 0x05040100u);
+            if (__ballot(redo)) {                       // the wave's vectors again, in fp64
+                double u[8];
+                vw_of(j, u);
+                o[0] = o[1] = 0;
+#pragma unroll
+                for (int d = 0; d < 8; ++d) o[d / 4] |= (uint32_t)(i8_code<NORM>(u[d], mul) & 0xFF) << (8 * (d % 4));
+            }
             if (i >= nvec) continue;
             if (whole(i)) *((uint2*)(p.codes + base) + i) = make_uint2(o[0], o[1]);
             else
@@ -342,7 +372,8 @@ __global__ void __launch_bounds__(256) norm_elem_kernel(NormArgs p) {
     if (p.qmode == MOE_Q_I8_ROW) {
         float scale;
         double mul;
-        i8_scale<256>(peak, r, s_max, s_bad, &scale, &mul);
+        float quick;
+        i8_scale<256>(peak, r, s_max, s_bad, &scale, &mul, &quick);
         if (t == 0) ((float*)p.scales)[row] = scale;
 #pragma unroll
         for (int j = 0; j < NE; ++j) {
