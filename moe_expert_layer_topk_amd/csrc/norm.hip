@@ -23,7 +23,7 @@
 // Bound by HBM: each input is read once and each output written once. A row
 // stays in registers between the reductions and the stores (so the outputs
 // may be the inputs' own memory): one pass, up to 16384 columns. 16384 x 2048
-// with the residual, both bf16 outputs and int8 rows: 57 us, 5.3 TB/s (a 1 GiB
+// with the residual, both bf16 outputs and int8 rows: 55 us, 5.5 TB/s (a 1 GiB
 // copy on the same card: 5.1; with fp32 arithmetic 51 us); without 8-bit rows
 // 45 us. Reading a row twice would have added a third to its bytes.
 #include "moe_common.h"
@@ -65,12 +65,40 @@ struct Peak {
     }
 };
 
+// Reductions of a wave by lane moves in the vector unit (a step through LDS
+// waits some 100 clocks: 16384 x 512 with int8 rows 19.0 us, these 17.8; int8
+// rows alone 6887 x 1200 10.6 and 9.7).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp_sum_step(double v) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, ROWS, 0xF, false);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), CTRL, ROWS, 0xF, false);
+    return v + __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ double wave_sum_f64(double v) {
+    v = dpp_sum_step<0x111, 0xF>(v);   // row_shr:1
+    v = dpp_sum_step<0x112, 0xF>(v);   // row_shr:2
+    v = dpp_sum_step<0x114, 0xF>(v);   // row_shr:4
+    v = dpp_sum_step<0x118, 0xF>(v);   // row_shr:8  -> lane 15 of each row holds the row's sum
+    v = dpp_sum_step<0x142, 0xA>(v);   // row_bcast:15 into rows 1 and 3
+    v = dpp_sum_step<0x143, 0xC>(v);   // row_bcast:31 into rows 2 and 3 -> lane 63 holds the sum
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, 63);
+    return __builtin_bit_cast(double, (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), 63) << 32 | lo);
+}
+// largest of 16 consecutive lanes (a group of 128 columns), in each of them
+__device__ __forceinline__ uint32_t group_max_u32(uint32_t v) {
+    v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xF, 0xF, true));     // quad_perm [1,0,3,2]
+    v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4E, 0xF, 0xF, true));     // quad_perm [2,3,0,1]
+    v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x124, 0xF, 0xF, true));    // row_ror:4
+    return max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x128, 0xF, 0xF, true)); // row_ror:8
+}
+
 // Sum over the TPR threads of a row (64: one wave; 256: the workgroup, through
 // four LDS words that no other reduction of the kernel uses).
 template <int TPR>
 __device__ __forceinline__ double row_sum(double v, double* s) {
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
+    v = wave_sum_f64(v);
     if (TPR == 64) return v;
     if (lane_id() == 0) s[threadIdx.x / 64] = v;
     __syncthreads();
@@ -99,8 +127,8 @@ __device__ __forceinline__ double rcp_f64(double a) {
 template <int TPR>
 __device__ __forceinline__ void i8_scale(Peak p, double r, double* s_max, uint32_t* s_bad, float* scale, double* mul, float* quick) {
     uint32_t bad = __ballot(p.hi >= 0x7FF00000u) != 0;
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) p.m = fmax(p.m, __shfl_xor(p.m, o, 64));
+    // (of positive doubles the bits keep the order)
+    p.m = __builtin_bit_cast(double, wave_max_u64_dpp(__builtin_bit_cast(uint64_t, p.m)));
     if (TPR != 64) {
         if (lane_id() == 0) {
             s_max[threadIdx.x / 64] = p.m;
@@ -156,8 +184,10 @@ __global__ void __launch_bounds__(256) norm_vec_kernel(NormArgs p) {
     auto whole = [&](int i) { return !SHIFT || (8 * i >= off && 8 * i + 8 <= end); };
     auto load = [&](const uint16_t* src, int i) __attribute__((always_inline)) {
         if (SHIFT && base + 8 * i + 8 > (size_t)p.rows * p.cols) {
-            i32x4 x = {0, 0, 0, 0};
-            for (int d = 0; 8 * i + d < end; ++d) x[d / 2] |= (int)((uint32_t)src[base + 8 * i + d] << (16 * (d & 1)));
+            i32x4 x = {0, 0, 0, 0};                     // (past the end: its last value, dropped below)
+#pragma unroll
+            for (int d = 0; d < 8; ++d)
+                x[d / 2] |= (int)((uint32_t)src[min(base + 8 * i + d, (size_t)p.rows * p.cols - 1)] << (16 * (d & 1)));
             return x;
         }
         return __builtin_nontemporal_load((const i32x4*)(src + base) + i);
@@ -212,12 +242,34 @@ __global__ void __launch_bounds__(256) norm_vec_kernel(NormArgs p) {
     auto weights = [&](int j, float (&w)[8]) __attribute__((always_inline)) {
         int i = min(t + j * TPR, nvec - 1);
         asm volatile("" : "+v"(i));                     // (loaded again where they are needed again)
-        if (!whole(i)) {
+        if (SHIFT && p.cols < 8) {
+#pragma unroll
             for (int d = 0; d < 8; ++d) w[d] = p.w[min(max(8 * i + d - off, 0), p.cols - 1)];
             return;
         }
+        // vectors that reach past the row: the eight weights at its end,
+        // rotated into place (loads in a branch of their own would wait there)
+        const int at = 8 * i - off, in = SHIFT ? min(max(at, 0), p.cols - 8) : at;
         typedef f32x4 f32x4_dword __attribute__((aligned(4)));       // (vector loads need whole dwords only)
-        const f32x4 w0 = *(const f32x4_dword*)(p.w + 8 * i - off), w1 = *(const f32x4_dword*)(p.w + 8 * i - off + 4);
+        f32x4 w0 = *(const f32x4_dword*)(p.w + in), w1 = *(const f32x4_dword*)(p.w + in + 4);
+        if (SHIFT && __ballot(at != in)) {
+            const int by = at - in;
+            if (by & 1) {
+                const float x = w0[0];
+                w0 = f32x4{w0[1], w0[2], w0[3], w1[0]};
+                w1 = f32x4{w1[1], w1[2], w1[3], x};
+            }
+            if (by & 2) {
+                const f32x4 x = w0;
+                w0 = f32x4{w0[2], w0[3], w1[0], w1[1]};
+                w1 = f32x4{w1[2], w1[3], x[0], x[1]};
+            }
+            if (by & 4) {
+                const f32x4 x = w0;
+                w0 = w1;
+                w1 = x;
+            }
+        }
 #pragma unroll
         for (int d = 0; d < 4; ++d) {
             w[d] = w0[d];
@@ -273,8 +325,7 @@ __global__ void __launch_bounds__(256) norm_vec_kernel(NormArgs p) {
                 z[d] = to_odd(u[d] * r);
                 gm = max(gm, __float_as_uint(z[d]) & 0x7FFFFFFFu);
             }
-#pragma unroll
-            for (int o = 1; o < 16; o <<= 1) gm = max(gm, (uint32_t)__shfl_xor((int)gm, o, 64));
+            gm = group_max_u32(gm);
             if (i >= nvec) continue;
             const bool bad = gm >= 0x7F800000u;
             int s = bad ? 0 : pow2_exponent_448(__uint_as_float(gm));
@@ -444,10 +495,10 @@ int norm_max_cols() { return 16384; }
 
 // A wave per row needs no exchange through LDS and leaves no threads idle on
 // short rows; a workgroup per row spreads few rows over more CUs. Measured (us,
-// a wave / a workgroup a row): int8 rows alone 8192 x 512 5.0 / 11.0, 1536 x 512
-// 4.1 / 4.4; norm with int8 rows 1024 x 512 4.5 / 5.4, 512 x 768 5.5 / 4.3, 1024
-// x 2048 10.7 / 7.6, 2048 x 2048 13.4 / 11.6, 4096 x 2048 18.4 / 19.5, 4096 x
-// 1032 14.5 / 15.6.
+// a wave / a workgroup a row): int8 rows alone 8192 x 512 4.9 / 9.9, 2048 x 512
+// 4.1 / 4.2; norm with int8 rows 1024 x 512 4.9 / 5.2, 512 x 768 4.6 / 4.4, 1024
+// x 2048 9.2 / 6.3, 2048 x 2048 13.2 / 10.8, 4096 x 1536 14.6 / 15.9, 4096 x 1032
+// 13.9 / 14.4, 16384 x 2048 54.8 / 56.5.
 template <bool NORM, bool SHIFT>
 static hipError_t launch_vec(const NormArgs& p, int nvec, int kid, hipStream_t stream) {
     const dim3 b(256), R((unsigned)p.rows), R4(((unsigned)p.rows + 3) / 4);
