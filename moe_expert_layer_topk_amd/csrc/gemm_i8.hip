@@ -177,7 +177,7 @@ struct Operand {
     }
 };
 
-template <int TM, int TN, int WM, int WN, bool GLU, bool F32, bool ANY>
+template <int TM, int TN, int WM, int WN, int R, bool GLU, bool F32, bool ANY>
 __global__ void __launch_bounds__(64 * WM * WN, 2) gemm_tile_kernel(GemmArgs p, int tiles_m, int tiles_n) {
     constexpr int WAVES = WM * WN;
     constexpr int MF = TM / WM / 16, NF = TN / WN / 16;
@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gemm_tile_kernel(GemmArgs p, 
     constexpr int META = TM + 2 * TN;                            // floats: row scales, column scales, bias
     static_assert(LA >= 1 && LB >= 1 && TM % (8 * WAVES) == 0 && TN % (8 * WAVES) == 0 && TM % 64 == 0 && TN % 64 == 0, "tile");
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-    float* s_meta = (float*)(smem + 2 * STAGE);                  // two tiles' worth
+    float* s_meta = (float*)(smem + R * STAGE);                  // two tiles' worth
     const int lane = lane_id();
     const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int mw = wv / WN, nw = wv % WN;
@@ -324,14 +324,14 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gemm_tile_kernel(GemmArgs p, 
     constexpr int BAR = 2;
     constexpr int LS = (NK - BAR) / NL > 0 ? (NK - BAR) / NL : 1;
     auto half1 = [&](int s, int st, int k0, int on) __attribute__((always_inline)) {
-        const int2 f = frags(st ^ 1, 0);
+        const int2 f = frags(R == 2 ? st ^ 1 : (st + 1) % R, 0);
         cut(s, 1);
         if (TM == 128) __builtin_amdgcn_s_setprio(0);
 #pragma unroll
         for (int k = 0; k < NK; ++k) {
             acc[k / NF][k % NF] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fa[1][k / NF], fb[1][k % NF], acc[k / NF][k % NF], 0, 0, 0);
             if (k == BAR - 1) {
-                wait_vmcnt<0>();
+                wait_vmcnt<(R - 2) * NL>();
                 barrier_lds();
             }
             if (k >= BAR - 1 && k - BAR + 1 < NR) read(f, 0, k - BAR + 1);
@@ -431,15 +431,25 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gemm_tile_kernel(GemmArgs p, 
     setup(0);
     meta(0);
 #pragma unroll
-    for (int l = 0; l < NL; ++l) dma(0, 1, 0, l);
+    for (int r = 0; r < R; ++r)
 #pragma unroll
-    for (int l = 0; l < NL; ++l) dma(128, 1, 1, l);
+        for (int l = 0; l < NL; ++l) dma(128 * r, 1, r, l);
     zero_acc();
-    wait_vmcnt<NL>();
+    wait_vmcnt<(R - 1) * NL>();
     barrier_lds();
 #pragma unroll
     for (int i = 0; i < NR; ++i) read(frags(0, 0), 0, i);
     int st = 0;
+    if constexpr (R > 2) {                                       // (one tile a workgroup)
+        row0 = row1;
+        col0 = col1;
+        for (int s = 0; s < S; ++s, st = (st + 1) % R) {
+            half0(s, st);
+            half1(s, st, (s + R) * 128, s + R < S);
+        }
+        epilogue(0);
+        return;
+    }
     for (int j = 0; j < nj; ++j) {
         row0 = row1;
         col0 = col1;
@@ -639,17 +649,17 @@ static hipError_t allow_lds(const void* kernel, int bytes, int dev, std::atomic<
     return e;
 }
 
-template <int TM, int TN, int WM, int WN, bool GLU, bool F32, bool ANY>
+template <int TM, int TN, int WM, int WN, int R, bool GLU, bool F32, bool ANY>
 static hipError_t launch_tile(const GemmArgs& p, int dev, int kid, hipStream_t stream) {
     constexpr int OUTN = GLU ? TN / 2 : TN;
-    constexpr int SMEM = 2 * (TM + TN) * 128 + 8 * (TM + 2 * TN);
+    constexpr int SMEM = R * (TM + TN) * 128 + 8 * (TM + 2 * TN);
     constexpr int PER_CU = 163840 / SMEM < 8 / (WM * WN) ? 163840 / SMEM : 8 / (WM * WN);
     static std::atomic<uint64_t> done{0};
-    const hipError_t e = allow_lds((const void*)gemm_tile_kernel<TM, TN, WM, WN, GLU, F32, ANY>, SMEM, dev, done);
+    const hipError_t e = allow_lds((const void*)gemm_tile_kernel<TM, TN, WM, WN, R, GLU, F32, ANY>, SMEM, dev, done);
     if (e != hipSuccess) return e;
     const int tm = (p.M + TM - 1) / TM, tn = (p.N + OUTN - 1) / OUTN;
     const int slots = (device_cus(dev) * PER_CU + 7) / 8 * 8, grid = min(slots, (tm * tn + 7) / 8 * 8);
-    return launch_kernel(kid, stream, gemm_tile_kernel<TM, TN, WM, WN, GLU, F32, ANY>, dim3((unsigned)grid),
+    return launch_kernel(kid, stream, gemm_tile_kernel<TM, TN, WM, WN, R, GLU, F32, ANY>, dim3((unsigned)grid),
                          dim3(64 * WM * WN), SMEM, p, tm, tn);
 }
 
@@ -713,11 +723,14 @@ static hipError_t launch_any(const GemmArgs& p, int kid, hipStream_t stream) {
     if (e != hipSuccess) return e;
     switch (pick_shape(p.M, (long long)p.N * (GLU ? 2 : 1), p.K, device_cus(dev))) {
         case S_256x256:
-            return p.lines ? launch_tile<256, 256, 4, 2, GLU, F32, false>(p, dev, kid, stream)
-                           : launch_tile<256, 256, 4, 2, GLU, F32, true>(p, dev, kid, stream);
+            return p.lines ? launch_tile<256, 256, 4, 2, 2, GLU, F32, false>(p, dev, kid, stream)
+                           : launch_tile<256, 256, 4, 2, 2, GLU, F32, true>(p, dev, kid, stream);
         case S_128x128:
-            return p.lines ? launch_tile<128, 128, 2, 2, GLU, F32, false>(p, dev, kid, stream)
-                           : launch_tile<128, 128, 2, 2, GLU, F32, true>(p, dev, kid, stream);
+            if (((p.M + 127LL) / 128) * (((long long)p.N * (GLU ? 2 : 1) + 127) / 128) <= device_cus(dev))
+                return p.lines ? launch_tile<128, 128, 2, 2, 4, GLU, F32, false>(p, dev, kid, stream)
+                               : launch_tile<128, 128, 2, 2, 4, GLU, F32, true>(p, dev, kid, stream);
+            return p.lines ? launch_tile<128, 128, 2, 2, 2, GLU, F32, false>(p, dev, kid, stream)
+                           : launch_tile<128, 128, 2, 2, 2, GLU, F32, true>(p, dev, kid, stream);
         case S_64x64: return launch_split<64, 64, 4, 4, GLU, F32>(p, dev, kid, stream);
         case S_32x64: return launch_split<32, 64, 8, 4, GLU, F32>(p, dev, kid, stream);
         default: return launch_split<32, 32, 8, 4, GLU, F32>(p, dev, kid, stream);
