@@ -131,7 +131,7 @@ __device__ __forceinline__ void store_each(const GemmArgs& p, int row, int col, 
 
 // ------------------------------------------------------------------ tiles
 // TM x TN outputs (glu: TN rows of B = TN / 2 columns of h) by WM x WN waves,
-// K in steps of 128 bytes through two LDS stages of TM + TN rows, each step two
+// K in steps of 128 bytes through R LDS stages of TM + TN rows, each step two
 // sub-steps of 64 bytes.
 // A stage row's 16-byte chunk c sits at c ^ ((row / 2) & 7): 16-byte fragment
 // reads of 16 consecutive rows then meet every bank once.
@@ -142,8 +142,10 @@ __device__ __forceinline__ void store_each(const GemmArgs& p, int row, int col, 
 // Persistent: a workgroup's tiles form one stream of K steps. Sub-step 0's
 // instructions run while sub-step 1's fragments are read. In sub-step 1 every
 // fragment of the step is in registers; past a barrier its stage is refilled
-// with the step two ahead (the next tile's first ones at a tile's end, so they
-// land during the epilogue) and the next step's first fragments are read.
+// with the step R ahead (R = 2: the next tile's first ones at a tile's end, so
+// they land during the epilogue) and the next step's first fragments are read.
+// R = 4 has a loop of its own for one tile a workgroup: the loop over tiles
+// with it took 14.5 us at 2048^3 instead of 12.7.
 //
 // Bound by the chip's power: on random codes the loop runs at 1.6-1.9 GHz
 // (2.4 GHz on zeros, 1.4 times as fast), with the matrix pipe busy about 80% of
@@ -152,9 +154,9 @@ __device__ __forceinline__ void store_each(const GemmArgs& p, int row, int col, 
 // as LDS allows, few instructions beside the matrix ones. 8192^3: 408 us, 2690
 // TOPS (a library product with int32 output on the same card 457-465 us); 4096
 // x 8192 x 8192 210 us (253); 16384 x 2048 x 2048 61 us (81); gated 16384 x 512
-// x 2048 30.4 us. Measured without gain: three or four stages of a 128-wide
-// tile, four 128 x 128 waves (the compiler spills), places of the barrier and
-// the loads between the matrix instructions.
+// x 2048 30.4 us. Measured without gain: 256 x 128 tiles with three stages, four
+// 128 x 128 waves (the compiler spills), places of the barrier and the loads
+// between the matrix instructions.
 template <int V>
 struct IC {
     static constexpr int value = V;
@@ -680,9 +682,9 @@ static hipError_t launch_split(const GemmArgs& p, int dev, int kid, hipStream_t 
 // round's prologue and epilogue (`round`). Large tiles move fewer bytes per
 // output, small ones reach more CUs. The figures are a fit to 400 products
 // with random sizes (1..16384 rows, 64..8192 columns, K 128..8192), each timed
-// with every shape: on 500 others the shape picked by them is 2.1% slower than
+// with every shape: on 900 others the shape picked by them is 2.0% slower than
 // the best of the five on average. E.g. 333 x 1000 x 4112: 32x64 9.2 us,
-// 128x128 24; 2048^3: 128x128 15 us, 256x256 24, 64x64 21.5; 16384 x 2048 x
+// 128x128 24; 2048^3: 128x128 13 us, 256x256 24, 64x64 21.5; 16384 x 2048 x
 // 2048: 256x256 59 us, 128x128 65. 256x128, 128x64 and 64x32 tiles were measured beside these
 // and gain less than 1% together.
 struct Shape {
@@ -726,6 +728,10 @@ static hipError_t launch_any(const GemmArgs& p, int kid, hipStream_t stream) {
             return p.lines ? launch_tile<256, 256, 4, 2, 2, GLU, F32, false>(p, dev, kid, stream)
                            : launch_tile<256, 256, 4, 2, 2, GLU, F32, true>(p, dev, kid, stream);
         case S_128x128:
+            // at most one tile a CU: one stage in flight does not cover a load
+            // (us with two stages / with four: 16384 x 256 x 7168 52.9 / 41.4,
+            // 2048 x 2048 x 8192 42.0 / 36.4, 2048^3 14.2 / 12.7, 2048 x 2048 x
+            // 512 6.6 / 6.7); with more, two of two stages share the CU's LDS
             if (((p.M + 127LL) / 128) * (((long long)p.N * (GLU ? 2 : 1) + 127) / 128) <= device_cus(dev))
                 return p.lines ? launch_tile<128, 128, 2, 2, 4, GLU, F32, false>(p, dev, kid, stream)
                                : launch_tile<128, 128, 2, 2, 4, GLU, F32, true>(p, dev, kid, stream);
