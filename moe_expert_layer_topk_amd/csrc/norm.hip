@@ -9,11 +9,12 @@
 //        zeros.
 // e4m3:  per 128 columns, the power-of-two scale of moe_quant_act.
 //
-// The squares' sum, r, y and the code's argument are fp64: a code changes where
-// its argument passes a border, so an error of 2^-24 would change some ten
-// codes in a million, and double-precision vector arithmetic is fast enough
-// here to hide behind memory (measured below). e4m3 codes come from y rounded
-// to odd, which a second rounding to fewer bits leaves correctly rounded.
+// The squares' sum, r and y are fp64, and so is every code that could depend on
+// it: a code changes where its argument passes a border, so an error of 2^-24
+// would change some ten codes in a million. int8 codes are formed in fp32
+// first, and again in fp64 where their argument lies near a border. e4m3 codes
+// come from y rounded to odd, which a second rounding to fewer bits leaves
+// correctly rounded.
 // Rows of int8 read from bf16 (quant_rows): 127 x / m is a border exactly, or
 // at least 1 / 512 away from it, so rounding the fp64 product to fp32 first
 // puts the exact ties back on the border.
