@@ -470,28 +470,31 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gemm_tile_kernel(GemmArgs p, 
 
 // ------------------------------------------------------------------ few tiles
 // Smaller tiles, for outputs that large tiles would spread over too few CUs.
-// The waves of a workgroup share one TM x TN tile and split each step's K
-// instead: wave k multiplies 32-byte sub-step k of the whole tile, which reads
-// half as much LDS per matrix instruction as splitting the tile (a 64 x 64 tile
-// in four 32 x 32 quarters), and their int32 sums meet in LDS (the ring's
-// memory, free by then), where the epilogue takes them in row order. R stages
-// are in flight. With one row the weights stream at HBM's rate (1 x 8192 x
-// 8192: 11.3 us, 5.9 TB/s, most of it launch and first latency below 2048 x
-// 2048: 4.0 us); with more, bound by L2 to LDS loads (about 50 bytes a clock
-// and CU): 333 x 1000 x 4112 9.8 us, 256 x 2048 x 2048 6.4 us. A kernel that
+// The waves of a workgroup share one TM x TN tile and take turns at its K
+// segments of 128 bytes: wave k multiplies segments k, k + WK, ... of the whole
+// tile, which reads half as much LDS per matrix instruction as splitting the
+// tile (a 64 x 64 tile in four 32 x 32 quarters), and their int32 sums meet in
+// LDS at the end, where the epilogue takes them in row order.
+// Each wave has a stage of its own, fills it, waits for its own loads alone and
+// refills it once the fragments are in registers: no barrier in the loop, and
+// waves that drift apart cover each other's waits. One stage and more waves, or
+// more workgroups on a CU, beat more stages (a barrier for each step and four
+// shared stages: 333 x 1000 x 4112 9.8 us, this 8.9; 256 x 2048 x 2048 5.6 and
+// 5.0; 481 x 2496 x 1632 10.9 and 9.6; two or three stages a wave in between).
+// With one row the weights stream at HBM's rate (1 x 8192 x 8192: 10.6 us, 6.3
+// TB/s, most of it launch and first latency below 2048 x 2048: 4.0 us); with
+// more, bound by L2 to LDS loads (about 50 bytes a clock and CU). A kernel that
 // streamed B straight into registers for up to 32 rows was no faster at one
 // row and up to 1.4 times slower at 16.
-template <int TM, int TN, int WK, int R, bool GLU, bool F32>
+template <int TM, int TN, int WK, bool GLU, bool F32>
 __global__ void __launch_bounds__(64 * WK) gemm_split_kernel(GemmArgs p, int tiles_m, int tiles_n) {
     constexpr int MF = TM / 32, NF = TN / 32;
-    constexpr int BK = 32 * WK;                                  // a step: one sub-step for each wave
-    constexpr int SEG = BK / 128;                                // 128-byte segments of a step, each a block of rows
-    constexpr int STAGE = (TM + TN) * BK;
-    constexpr int LD = (TM + TN) * SEG / 8 / WK;                 // 8-row loads per wave and step
+    constexpr int STAGE = (TM + TN) * 128;                       // 128 K bytes of the tile's rows
+    constexpr int LD = (TM + TN) / 8;                            // 8-row loads of a stage
     constexpr int OUTN = GLU ? TN / 2 : TN;
-    static_assert(BK % 128 == 0 && (TM + TN) * SEG % (8 * WK) == 0 && WK * TM * TN * 4 <= R * STAGE, "tile");
+    static_assert(TM * TN * 4 <= STAGE, "the waves' sums fit their stages");
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-    float* s_sa = (float*)(smem + R * STAGE);
+    float* s_sa = (float*)(smem + WK * STAGE);
     float* s_sb = s_sa + 64 * ((TM + 63) / 64);
     float* s_bias = s_sb + 64 * ((TN + 63) / 64);
     const int lane = lane_id();
@@ -504,37 +507,27 @@ __global__ void __launch_bounds__(64 * WK) gemm_split_kernel(GemmArgs p, int til
         L = x * per + min(x, rem) + i;
     }
     const int row0 = (L % tiles_m) * TM, col0 = (L / tiles_m) * OUTN;
-    const int K = p.K, S = (K + BK - 1) / BK;
+    const int K = p.K, segs = (K + 127) / 128;
 
-    // load j of this wave: 8 stage rows; lane i row i / 8 of them, chunk (i % 8) ^ ((row / 2) & 7)
+    // load j: 8 stage rows; lane i row i / 8 of them, chunk (i % 8) ^ ((row / 2)
+    // & 7). A segment that K ends in runs on into the next row, and past the
+    // operand's end nothing is read: the multiply side zeroes A there.
+    uint8_t* stage = smem + wv * STAGE;
+    Operand bA, bB, bU;                                          // A, B (glu: its gate rows), glu's up rows
+    bA.set(p.a + (size_t)row0 * K, (size_t)(p.M - row0) * K);
+    bB.set(p.b + (size_t)col0 * K, (size_t)(p.N - col0) * K);
+    if (GLU) bU.set(p.b + ((size_t)p.N + col0) * K, (size_t)(p.N - col0) * K);
     uint32_t off[LD];
-    const uint8_t* base[LD];
-    auto chunk = [&](int r8) { return 16 * ((lane & 7) ^ ((4 * r8 + (lane >> 4)) & 7)); };
-    auto kpos = [&](int j) { return (wv * LD + j) / ((TM + TN) / 8) * 128 + chunk(wv * LD + j); };   // K byte inside the step
 #pragma unroll
     for (int j = 0; j < LD; ++j) {
-        const int r = (wv * LD + j) % ((TM + TN) / 8) * 8;       // first stage row of the load
-        const int sub = r + (lane >> 3);
-        if (r < TM) {
-            base[j] = (const uint8_t*)p.a + (size_t)row0 * K;
-            off[j] = (uint32_t)min(sub, p.M - 1 - row0) * K + kpos(j);
-        } else {
-            const int up = GLU && r - TM >= OUTN;
-            base[j] = (const uint8_t*)p.b + ((size_t)col0 + (up ? p.N : 0)) * K;
-            off[j] = (uint32_t)min(sub - TM - (up ? OUTN : 0), p.N - 1 - col0) * K + kpos(j);
-        }
+        const int r = 8 * j + (lane >> 3), ch = 16 * ((lane & 7) ^ ((4 * j + (lane >> 4)) & 7));
+        if (8 * j < TM) off[j] = (uint32_t)min(r, p.M - 1 - row0) * K + ch;
+        else off[j] = (uint32_t)min(r - TM - (GLU && 8 * j - TM >= OUTN ? OUTN : 0), p.N - 1 - col0) * K + ch;
     }
-    auto fill = [&](int s) __attribute__((always_inline)) {
-        uint8_t* st = smem + (s % R) * STAGE;
-        const int k0 = s * BK;
-        if (k0 + BK <= K) {
+    auto fill = [&](int seg) __attribute__((always_inline)) {
 #pragma unroll
-            for (int j = 0; j < LD; ++j) lds_dma16(base[j] + k0 + off[j], st + 1024 * (wv * LD + j));
-        } else {                                                 // K ends in this step, or before it: zeros
-#pragma unroll
-            for (int j = 0; j < LD; ++j)
-                lds_dma16(k0 + kpos(j) < K ? base[j] + k0 + off[j] : g_zero16, st + 1024 * (wv * LD + j));
-        }
+        for (int j = 0; j < LD; ++j)
+            (8 * j < TM ? bA : GLU && 8 * j - TM >= OUTN ? bU : bB).load_lds(stage + 1024 * j, off[j], seg * 128, 1);
     };
     for (int i = wv; i < (TM + 63) / 64; i += WK)
         lds_dma4(p.sa + min(row0 + 64 * i + lane, p.M - 1), (uint8_t*)(s_sa + 64 * i));
@@ -544,8 +537,7 @@ __global__ void __launch_bounds__(64 * WK) gemm_split_kernel(GemmArgs p, int til
         lds_dma4(p.sb + n, (uint8_t*)(s_sb + 64 * i));
         if (!GLU && p.bias) lds_dma4(p.bias + n, (uint8_t*)(s_bias + 64 * i));
     }
-#pragma unroll
-    for (int s = 0; s < R; ++s) fill(s);
+    if (wv < segs) fill(wv);
 
     i32x16 acc[MF][NF];
 #pragma unroll
@@ -555,39 +547,44 @@ __global__ void __launch_bounds__(64 * WK) gemm_split_kernel(GemmArgs p, int til
 #pragma unroll
             for (int i = 0; i < 16; ++i) acc[a][n][i] = 0;
     const int m = lane & 31, hi = lane >> 5;
-    const int lo = (wv / 4) * (TM + TN) * 128 + m * 128 + (((2 * (wv & 3) + hi) ^ ((m >> 1) & 7)) << 4);
-    i32x4 fa[2][MF], fb[2][NF];
-    auto read = [&](int s, int u) __attribute__((always_inline)) {
-        const uint8_t* sg = smem + (s % R) * STAGE + lo;
+    // lane (m, hi) holds 16 K bytes of fragment row m, chunk 2 u + hi of sub-step u
+    int lo[4];
 #pragma unroll
-        for (int a = 0; a < MF; ++a) fa[u][a] = *(const i32x4*)(sg + a * 4096);
+    for (int u = 0; u < 4; ++u) lo[u] = m * 128 + (((2 * u + hi) ^ ((m >> 1) & 7)) << 4);
+    for (int seg = wv; seg < segs; seg += WK) {
+        wait_vmcnt<0>();
+        i32x4 fa[4][MF], fb[4][NF];
 #pragma unroll
-        for (int n = 0; n < NF; ++n) fb[u][n] = *(const i32x4*)(sg + TM * 128 + n * 4096);
-    };
-    // step s is in register set u: past the barrier its stage is free for step
-    // s + R, and step s + 1, which has landed, goes to the other set while s is
-    // multiplied
-    auto step = [&](int s, int u) __attribute__((always_inline)) {
-        wait_vmcnt<(R - 2) * LD>();
-        barrier_lds();
-        read(s + 1, u ^ 1);
+        for (int u = 0; u < 4; ++u) {
+#pragma unroll
+            for (int a = 0; a < MF; ++a) fa[u][a] = *(const i32x4*)(stage + lo[u] + a * 4096);
+#pragma unroll
+            for (int n = 0; n < NF; ++n) fb[u][n] = *(const i32x4*)(stage + lo[u] + TM * 128 + n * 4096);
+        }
+        if (128 * (seg + 1) > K) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const bool out = 128 * seg + 32 * u + 16 * hi >= K;
+#pragma unroll
+                for (int a = 0; a < MF; ++a)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) fa[u][a][i] = out ? 0 : fa[u][a][i];
+            }
+        }
+        // the fragments are in registers before their stage is refilled
         __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int a = 0; a < MF; ++a)
-#pragma unroll
-            for (int n = 0; n < NF; ++n)
-                acc[a][n] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fa[u][a], fb[u][n], acc[a][n], 0, 0, 0);
+        __builtin_amdgcn_s_waitcnt(0xC07F);                      // lgkmcnt(0)
         __builtin_amdgcn_sched_barrier(0);
-        fill(s + R);
-    };
-    wait_vmcnt<(R - 1) * LD>();
-    barrier_lds();
-    read(0, 0);
-    for (int s = 0; s < S; s += 2) {                             // (a step past the end multiplies zeros)
-        step(s, 0);
-        step(s + 1, 1);
+        if (seg + WK < segs) fill(seg + WK);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int a = 0; a < MF; ++a)
+#pragma unroll
+                for (int n = 0; n < NF; ++n)
+                    acc[a][n] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fa[u][a], fb[u][n], acc[a][n], 0, 0, 0);
     }
-    wait_vmcnt<0>();                                             // the last fills land before their memory is reused
+    wait_vmcnt<0>();                                             // (a wave without a segment: its scales)
     barrier_lds();
     int* s_acc = (int*)smem;
 #pragma unroll
@@ -665,38 +662,39 @@ static hipError_t launch_tile(const GemmArgs& p, int dev, int kid, hipStream_t s
                          dim3(64 * WM * WN), SMEM, p, tm, tn);
 }
 
-template <int TM, int TN, int WK, int R, bool GLU, bool F32>
+template <int TM, int TN, int WK, bool GLU, bool F32>
 static hipError_t launch_split(const GemmArgs& p, int dev, int kid, hipStream_t stream) {
     constexpr int OUTN = GLU ? TN / 2 : TN;
-    constexpr int SMEM = R * (TM + TN) * 32 * WK + 256 * ((TM + 63) / 64 + 2 * ((TN + 63) / 64));
+    constexpr int SMEM = WK * (TM + TN) * 128 + 256 * ((TM + 63) / 64 + 2 * ((TN + 63) / 64));
     static std::atomic<uint64_t> done{0};
-    const hipError_t e = allow_lds((const void*)gemm_split_kernel<TM, TN, WK, R, GLU, F32>, SMEM, dev, done);
+    const hipError_t e = allow_lds((const void*)gemm_split_kernel<TM, TN, WK, GLU, F32>, SMEM, dev, done);
     if (e != hipSuccess) return e;
     const int tm = (p.M + TM - 1) / TM, tn = (p.N + OUTN - 1) / OUTN;
-    return launch_kernel(kid, stream, gemm_split_kernel<TM, TN, WK, R, GLU, F32>, dim3((unsigned)(tm * tn)),
+    return launch_kernel(kid, stream, gemm_split_kernel<TM, TN, WK, GLU, F32>, dim3((unsigned)(tm * tn)),
                          dim3(64 * WK), SMEM, p, tm, tn);
 }
 
 // The tile shapes, and what they cost (us): a K step of 128 with at most one
 // workgroup on each CU (`one`) and with all `per_cu` of them (`full`), and a
 // round's prologue and epilogue (`round`). Large tiles move fewer bytes per
-// output, small ones reach more CUs. The figures are a fit to 400 products
+// output, small ones reach more CUs. The figures are a fit to 1100 products
 // with random sizes (1..16384 rows, 64..8192 columns, K 128..8192), each timed
-// with every shape: on 900 others the shape picked by them is 2.0% slower than
-// the best of the five on average. E.g. 333 x 1000 x 4112: 32x64 9.2 us,
-// 128x128 24; 2048^3: 128x128 13 us, 256x256 24, 64x64 21.5; 16384 x 2048 x
-// 2048: 256x256 59 us, 128x128 65. 256x128, 128x64 and 64x32 tiles were measured beside these
-// and gain less than 1% together.
+// with every shape: where the best takes 5.5 us and more, the shape picked by
+// them is 0.6% slower than it on average (below, the five differ by little more
+// than two runs of one). E.g. 333 x 1000 x 4112: 32x64 8.9 us, 64x64 11.4,
+// 128x128 22; 400 x 2048 x 2048: 64x64 6.7, 32x32 8.3, 128x128 11; 2048^3:
+// 128x128 12.6 us, 64x64 21, 256x256 24; 16384 x 2048 x 2048: 256x256 59 us,
+// 128x128 71. 256x128 tiles were measured beside these and gain nothing.
 struct Shape {
     int tm, tn, per_cu;
     float one, full, round;
 };
 enum { S_256x256, S_128x128, S_64x64, S_32x64, S_32x32, S_COUNT };
-static const Shape kShapes[S_COUNT] = {{256, 256, 1, 1.17f, 1.17f, 2.6f},
-                                       {128, 128, 2, 0.43f, 0.79f, 0.7f},
-                                       {64, 64, 2, 0.16f, 0.38f, 0.9f},
-                                       {32, 64, 1, 0.16f, 0.16f, 0.8f},
-                                       {32, 32, 2, 0.03f, 0.23f, 1.0f}};
+static const Shape kShapes[S_COUNT] = {{256, 256, 1, 1.17f, 1.17f, 2.45f},
+                                       {128, 128, 2, 0.41f, 0.79f, 1.09f},
+                                       {64, 64, 2, 0.10f, 0.41f, 1.13f},
+                                       {32, 64, 3, 0.06f, 0.42f, 0.70f},
+                                       {32, 32, 2, 0.012f, 0.19f, 1.06f}};
 
 // The shape that the costs above make the fastest for this many output rows
 // and B rows.
@@ -723,7 +721,9 @@ static hipError_t launch_any(const GemmArgs& p, int kid, hipStream_t stream) {
     int dev = 0;
     const hipError_t e = hipGetDevice(&dev);
     if (e != hipSuccess) return e;
-    switch (pick_shape(p.M, (long long)p.N * (GLU ? 2 : 1), p.K, device_cus(dev))) {
+    const long long cus = device_cus(dev), rows_b = (long long)p.N * (GLU ? 2 : 1);
+    auto tiles = [&](int tm, int tn) { return (p.M + tm - 1LL) / tm * ((rows_b + tn - 1) / tn); };
+    switch (pick_shape(p.M, rows_b, p.K, cus)) {
         case S_256x256:
             return p.lines ? launch_tile<256, 256, 4, 2, 2, GLU, F32, false>(p, dev, kid, stream)
                            : launch_tile<256, 256, 4, 2, 2, GLU, F32, true>(p, dev, kid, stream);
@@ -732,14 +732,22 @@ static hipError_t launch_any(const GemmArgs& p, int kid, hipStream_t stream) {
             // (us with two stages / with four: 16384 x 256 x 7168 52.9 / 41.4,
             // 2048 x 2048 x 8192 42.0 / 36.4, 2048^3 14.2 / 12.7, 2048 x 2048 x
             // 512 6.6 / 6.7); with more, two of two stages share the CU's LDS
-            if (((p.M + 127LL) / 128) * (((long long)p.N * (GLU ? 2 : 1) + 127) / 128) <= device_cus(dev))
+            if (tiles(128, 128) <= cus)
                 return p.lines ? launch_tile<128, 128, 2, 2, 4, GLU, F32, false>(p, dev, kid, stream)
                                : launch_tile<128, 128, 2, 2, 4, GLU, F32, true>(p, dev, kid, stream);
             return p.lines ? launch_tile<128, 128, 2, 2, 2, GLU, F32, false>(p, dev, kid, stream)
                            : launch_tile<128, 128, 2, 2, 2, GLU, F32, true>(p, dev, kid, stream);
-        case S_64x64: return launch_split<64, 64, 4, 4, GLU, F32>(p, dev, kid, stream);
-        case S_32x64: return launch_split<32, 64, 8, 4, GLU, F32>(p, dev, kid, stream);
-        default: return launch_split<32, 32, 8, 4, GLU, F32>(p, dev, kid, stream);
+        // at most one workgroup a CU: more waves in it (us with eight waves /
+        // with four: 400 x 2048 x 2048 6.8 / 7.2 and 333 x 1000 x 4112 9.0 / 9.5
+        // so; 978 x 704 x 5248 gated 21.0 / 17.4 and 481 x 2496 x 1632 11.9 /
+        // 9.6 with more tiles than CUs)
+        case S_64x64:
+            return tiles(64, 64) <= cus ? launch_split<64, 64, 8, GLU, F32>(p, dev, kid, stream)
+                                        : launch_split<64, 64, 4, GLU, F32>(p, dev, kid, stream);
+        case S_32x64:
+            return tiles(32, 64) <= cus ? launch_split<32, 64, 8, GLU, F32>(p, dev, kid, stream)
+                                        : launch_split<32, 64, 4, GLU, F32>(p, dev, kid, stream);
+        default: return launch_split<32, 32, 8, GLU, F32>(p, dev, kid, stream);
     }
 }
 
