@@ -553,6 +553,7 @@ __global__ void __launch_bounds__(64 * WK) gemm_split_kernel(GemmArgs p, int til
     for (int u = 0; u < 4; ++u) lo[u] = m * 128 + (((2 * u + hi) ^ ((m >> 1) & 7)) << 4);
     for (int seg = wv; seg < segs; seg += WK) {
         wait_vmcnt<0>();
+        asm volatile("" ::: "memory");                           // no read of the stage before the wait
         i32x4 fa[4][MF], fb[4][NF];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
