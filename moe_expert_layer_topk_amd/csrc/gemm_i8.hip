@@ -11,6 +11,7 @@
 // which K bytes a lane holds.
 #include "moe_common.h"
 #include "moe_kernels.h"
+#include "gemm_i8_plan.h"
 
 #include <atomic>
 
@@ -163,19 +164,24 @@ struct IC {
 };
 
 // Rows of an operand from a tile's first one on, as a buffer: accesses past its
-// end return nothing.
+// end return nothing. Each K position has a descriptor of its own, based there
+// and holding the records that are left, and no scalar offset. The check that
+// drops an access then compares the lane's offset alone, which every
+// description of it agrees on; of a scalar offset the compiler's intrinsic says
+// that it is left out of the check, the MI300 instruction set that it is taken
+// off the record count, and neither what happens where it exceeds that count.
 struct Operand {
-    const void* p;
-    uint32_t bytes;
-    __device__ __forceinline__ void set(const void* first, size_t n) {
-        p = first;
-        bytes = n > 0xFFFFFFF0ull ? 0xFFFFFFF0u : (uint32_t)n;
+    const uint8_t* p;
+    int bytes;
+    __device__ __forceinline__ void set(const int8_t* first, size_t n) {
+        p = (const uint8_t*)first;
+        bytes = records(n);
     }
-    // 16 bytes a lane, from lane offset o + scalar offset k, to dst + 16 lane
-    __device__ __forceinline__ void load_lds(uint8_t* dst, uint32_t o, int k, int on) const {
+    // 16 bytes a lane, from lane offset o at K position k, to dst + 16 lane
+    __device__ __forceinline__ void load_lds(uint8_t* dst, uint32_t o, int k) const {
         __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            __builtin_amdgcn_make_buffer_rsrc((void*)p, 0, on ? (int)bytes : 0, 0x00027000),
-            (__attribute__((address_space(3))) void*)dst, 16, (int)o, k, 0, 0);
+            __builtin_amdgcn_make_buffer_rsrc((void*)(p + k), 0, records_from(bytes, k), 0x00027000),
+            (__attribute__((address_space(3))) void*)dst, 16, (int)o, 0, 0, 0);
     }
 };
 
@@ -216,10 +222,11 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gemm_tile_kernel(GemmArgs p, 
     // ---- load side: load j of this wave fills stage rows 8 (wv LA + j) ..
     // (A; B after TM rows likewise); lane i: row i / 8 of them, chunk
     // (i % 8) ^ ((row / 2) & 7) of its source row. Buffer loads: 32-bit lane
-    // offsets from the tile's first row, the K position as a scalar, no
-    // address arithmetic in the step loop. A step that K ends in runs on into
-    // the next row, and past the operand's end the buffer's bounds check drops
-    // the access: the multiply side zeroes A there.
+    // offsets from the tile's first row, the K position in the descriptor, no
+    // vector address arithmetic in the step loop. A step that K ends in runs on
+    // into the next row, and past the operand's end the buffer's bounds check
+    // drops the access, as it does for every access of a step past K in the
+    // last row: the multiply side zeroes A there.
     // (Per-lane constants used once a tile are formed there, from an opaque copy
     // of the lane id: held across the step loop they would spill.)
     auto opaque_lane = [&]() __attribute__((always_inline)) {
@@ -239,14 +246,14 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gemm_tile_kernel(GemmArgs p, 
 #pragma unroll
         for (int i = 0; i < LA; ++i) {
             const int r8 = wv * LA + i;
-            oA[i] = (uint32_t)min(8 * r8 + sub, p.M - 1 - row1) * K + (ch0 ^ (64 * (r8 & 1)));
+            oA[i] = row_offset(8 * r8 + sub, p.M - 1 - row1, K, ch0 ^ (64 * (r8 & 1)));
         }
 #pragma unroll
         for (int i = 0; i < LB; ++i) {
             const int r8 = wv * LB + i, f = r8 / 2, m = 8 * (r8 & 1) + sub;
             const int w = f / NF, n = f % NF;
             const int c = w * 16 * NC + NC * m + n % NC;         // output column in the tile
-            oB[i] = (uint32_t)min(c, p.N - 1 - col1) * K + (ch0 ^ (64 * (r8 & 1)));
+            oB[i] = row_offset(c, p.N - 1 - col1, K, ch0 ^ (64 * (r8 & 1)));
         }
     };
     // the loaded tile's scales into metadata slot `slot`
@@ -262,13 +269,13 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gemm_tile_kernel(GemmArgs p, 
             if (!GLU) lds_dma4(p.bias ? p.bias + n : (const float*)g_zero16, (uint8_t*)(md + TM + TN + 64 * i));
         }
     };
-    // load l of the 128 K bytes from k0 on into stage st (on = 0: no access)
-    auto dma = [&](int k0, int on, int st, int l) __attribute__((always_inline)) {
+    // load l of the 128 K bytes from k0 on (NOWHERE: no access) into stage st
+    auto dma = [&](int k0, int st, int l) __attribute__((always_inline)) {
         const int j = l < LA ? l : 0, i = l < LA ? 0 : l - LA;
         uint8_t* dst = smem + st * STAGE + (l < LA ? 1024 * (wv * LA + j) : TM * 128 + 1024 * (wv * LB + i));
-        if (l < LA) bA.load_lds(dst, oA[j], k0, on);
-        else if (GLU && (wv * LB + i) / 2 % NF >= NC) bU.load_lds(dst, oB[i], k0, on);
-        else bB.load_lds(dst, oB[i], k0, on);
+        if (l < LA) bA.load_lds(dst, oA[j], k0);
+        else if (GLU && (wv * LB + i) / 2 % NF >= NC) bU.load_lds(dst, oB[i], k0);
+        else bB.load_lds(dst, oB[i], k0);
     };
 
     // ---- multiply side: lane (m, q) holds 16 K bytes of fragment row m, chunk 4 u + q in sub-step u
@@ -325,7 +332,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gemm_tile_kernel(GemmArgs p, 
     // are read and this one is refilled (the loads spread over the rest)
     constexpr int BAR = 2;
     constexpr int LS = (NK - BAR) / NL > 0 ? (NK - BAR) / NL : 1;
-    auto half1 = [&](int s, int st, int k0, int on) __attribute__((always_inline)) {
+    auto half1 = [&](int s, int st, int k0) __attribute__((always_inline)) {
         const int2 f = frags(R == 2 ? st ^ 1 : (st + 1) % R, 0);
         cut(s, 1);
         if (TM == 128) __builtin_amdgcn_s_setprio(0);
@@ -337,7 +344,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gemm_tile_kernel(GemmArgs p, 
                 barrier_lds();
             }
             if (k >= BAR - 1 && k - BAR + 1 < NR) read(f, 0, k - BAR + 1);
-            if (k >= BAR && (k - BAR) % LS == 0 && (k - BAR) / LS < NL) dma(k0, on, st, (k - BAR) / LS);
+            if (k >= BAR && (k - BAR) % LS == 0 && (k - BAR) / LS < NL) dma(k0, st, (k - BAR) / LS);
             __builtin_amdgcn_sched_barrier(0);
         }
         static_assert((NK - 1 - BAR) / LS >= NL - 1 && NK - BAR + 1 > NR, "every load and read has its instruction");
@@ -435,7 +442,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gemm_tile_kernel(GemmArgs p, 
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int l = 0; l < NL; ++l) dma(128 * r, 1, r, l);
+        for (int l = 0; l < NL; ++l) dma(128 * r, r, l);
     zero_acc();
     wait_vmcnt<(R - 1) * NL>();
     barrier_lds();
@@ -447,7 +454,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gemm_tile_kernel(GemmArgs p, 
         col0 = col1;
         for (int s = 0; s < S; ++s, st = (st + 1) % R) {
             half0(s, st);
-            half1(s, st, (s + R) * 128, s + R < S);
+            half1(s, st, s + R < S ? (s + R) * 128 : NOWHERE);
         }
         epilogue(0);
         return;
@@ -460,7 +467,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gemm_tile_kernel(GemmArgs p, 
             half0(s, st);
             const bool next = s == S - 2 && more;
             if (next) setup(j + 1);                              // every load of tile j is out
-            half1(s, st, (s + 2 < S ? s + 2 : s + 2 - S) * 128, s + 2 < S || more);
+            half1(s, st, s + 2 < S ? (s + 2) * 128 : more ? (s + 2 - S) * 128 : NOWHERE);
             if (next) meta((j + 1) & 1);                         // (after half1's wait and barrier)
         }
         epilogue(j & 1);
@@ -521,13 +528,13 @@ __global__ void __launch_bounds__(64 * WK) gemm_split_kernel(GemmArgs p, int til
 #pragma unroll
     for (int j = 0; j < LD; ++j) {
         const int r = 8 * j + (lane >> 3), ch = 16 * ((lane & 7) ^ ((4 * j + (lane >> 4)) & 7));
-        if (8 * j < TM) off[j] = (uint32_t)min(r, p.M - 1 - row0) * K + ch;
-        else off[j] = (uint32_t)min(r - TM - (GLU && 8 * j - TM >= OUTN ? OUTN : 0), p.N - 1 - col0) * K + ch;
+        if (8 * j < TM) off[j] = row_offset(r, p.M - 1 - row0, K, ch);
+        else off[j] = row_offset(r - TM - (GLU && 8 * j - TM >= OUTN ? OUTN : 0), p.N - 1 - col0, K, ch);
     }
     auto fill = [&](int seg) __attribute__((always_inline)) {
 #pragma unroll
         for (int j = 0; j < LD; ++j)
-            (8 * j < TM ? bA : GLU && 8 * j - TM >= OUTN ? bU : bB).load_lds(stage + 1024 * j, off[j], seg * 128, 1);
+            (8 * j < TM ? bA : GLU && 8 * j - TM >= OUTN ? bU : bB).load_lds(stage + 1024 * j, off[j], seg * 128);
     };
     for (int i = wv; i < (TM + 63) / 64; i += WK)
         lds_dma4(p.sa + min(row0 + 64 * i + lane, p.M - 1), (uint8_t*)(s_sa + 64 * i));
