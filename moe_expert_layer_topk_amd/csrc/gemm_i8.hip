@@ -682,56 +682,15 @@ static hipError_t launch_split(const GemmArgs& p, int dev, int kid, hipStream_t 
                          dim3(64 * WK), SMEM, p, tm, tn);
 }
 
-// The tile shapes, and what they cost (us): a K step of 128 with at most one
-// workgroup on each CU (`one`) and with all `per_cu` of them (`full`), and a
-// round's prologue and epilogue (`round`). Large tiles move fewer bytes per
-// output, small ones reach more CUs. The figures are a fit to 1100 products
-// with random sizes (1..16384 rows, 64..8192 columns, K 128..8192), each timed
-// with every shape: where the best takes 5.5 us and more, the shape picked by
-// them is 0.6% slower than it on average (below, the five differ by little more
-// than two runs of one). E.g. 333 x 1000 x 4112: 32x64 8.9 us, 64x64 11.4,
-// 128x128 22; 400 x 2048 x 2048: 64x64 6.7, 32x32 8.3, 128x128 11; 2048^3:
-// 128x128 12.6 us, 64x64 21, 256x256 24; 16384 x 2048 x 2048: 256x256 59 us,
-// 128x128 71. 256x128 tiles were measured beside these and gain nothing.
-struct Shape {
-    int tm, tn, per_cu;
-    float one, full, round;
-};
-enum { S_256x256, S_128x128, S_64x64, S_32x64, S_32x32, S_COUNT };
-static const Shape kShapes[S_COUNT] = {{256, 256, 1, 1.17f, 1.17f, 2.45f},
-                                       {128, 128, 2, 0.41f, 0.79f, 1.09f},
-                                       {64, 64, 2, 0.10f, 0.41f, 1.13f},
-                                       {32, 64, 3, 0.06f, 0.42f, 0.70f},
-                                       {32, 32, 2, 0.012f, 0.19f, 1.06f}};
-
-// The shape that the costs above make the fastest for this many output rows
-// and B rows.
-static int pick_shape(int M, long long rows_b, int K, long long cus) {
-    const float steps = (float)((K + 127) / 128);
-    int best = 0;
-    float least = 3.4e38f;
-    for (int i = 0; i < S_COUNT; ++i) {
-        const Shape& c = kShapes[i];
-        const long long tiles = ((M + c.tm - 1) / c.tm) * ((rows_b + c.tn - 1) / c.tn), slots = cus * c.per_cu;
-        const long long rounds = tiles / slots, rest = tiles % slots;
-        const float t = (float)rounds * (c.full * steps + c.round) +
-                        (rest ? (rest <= cus ? c.one : c.full) * steps + c.round : 0.f);
-        if (t < least) {
-            least = t;
-            best = i;
-        }
-    }
-    return best;
-}
-
 template <bool GLU, bool F32>
 static hipError_t launch_any(const GemmArgs& p, int kid, hipStream_t stream) {
     int dev = 0;
     const hipError_t e = hipGetDevice(&dev);
     if (e != hipSuccess) return e;
     const long long cus = device_cus(dev), rows_b = (long long)p.N * (GLU ? 2 : 1);
-    auto tiles = [&](int tm, int tn) { return (p.M + tm - 1LL) / tm * ((rows_b + tn - 1) / tn); };
-    switch (pick_shape(p.M, rows_b, p.K, cus)) {
+    const int shape = pick_shape(p.M, rows_b, p.K, cus);
+    const bool few = shape_tiles(shape, p.M, rows_b) <= cus;             // at most one tile a CU
+    switch (shape) {
         case S_256x256:
             return p.lines ? launch_tile<256, 256, 4, 2, 2, GLU, F32, false>(p, dev, kid, stream)
                            : launch_tile<256, 256, 4, 2, 2, GLU, F32, true>(p, dev, kid, stream);
@@ -740,22 +699,18 @@ static hipError_t launch_any(const GemmArgs& p, int kid, hipStream_t stream) {
             // (us with two stages / with four: 16384 x 256 x 7168 52.9 / 41.4,
             // 2048 x 2048 x 8192 42.0 / 36.4, 2048^3 14.2 / 12.7, 2048 x 2048 x
             // 512 6.6 / 6.7); with more, two of two stages share the CU's LDS
-            if (tiles(128, 128) <= cus)
+            if (few)
                 return p.lines ? launch_tile<128, 128, 2, 2, 4, GLU, F32, false>(p, dev, kid, stream)
                                : launch_tile<128, 128, 2, 2, 4, GLU, F32, true>(p, dev, kid, stream);
             return p.lines ? launch_tile<128, 128, 2, 2, 2, GLU, F32, false>(p, dev, kid, stream)
                            : launch_tile<128, 128, 2, 2, 2, GLU, F32, true>(p, dev, kid, stream);
-        // at most one workgroup a CU: more waves in it (us with eight waves /
-        // with four: 400 x 2048 x 2048 6.8 / 7.2 and 333 x 1000 x 4112 9.0 / 9.5
-        // so; 978 x 704 x 5248 gated 21.0 / 17.4 and 481 x 2496 x 1632 11.9 /
-        // 9.6 with more tiles than CUs)
         case S_64x64:
-            return tiles(64, 64) <= cus ? launch_split<64, 64, 8, GLU, F32>(p, dev, kid, stream)
-                                        : launch_split<64, 64, 4, GLU, F32>(p, dev, kid, stream);
+            return few ? launch_split<64, 64, split_waves(S_64x64, true), GLU, F32>(p, dev, kid, stream)
+                       : launch_split<64, 64, split_waves(S_64x64, false), GLU, F32>(p, dev, kid, stream);
         case S_32x64:
-            return tiles(32, 64) <= cus ? launch_split<32, 64, 8, GLU, F32>(p, dev, kid, stream)
-                                        : launch_split<32, 64, 4, GLU, F32>(p, dev, kid, stream);
-        default: return launch_split<32, 32, 8, GLU, F32>(p, dev, kid, stream);
+            return few ? launch_split<32, 64, split_waves(S_32x64, true), GLU, F32>(p, dev, kid, stream)
+                       : launch_split<32, 64, split_waves(S_32x64, false), GLU, F32>(p, dev, kid, stream);
+        default: return launch_split<32, 32, split_waves(S_32x32, false), GLU, F32>(p, dev, kid, stream);
     }
 }
 

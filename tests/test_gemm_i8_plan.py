@@ -1,6 +1,7 @@
-"""What the int8 products load, decided on the host (no GPU): the functions of
-csrc/gemm_i8_plan.h, which the kernels call too, in a small C++ program, and
-the loads of the built library.
+"""What the int8 products load, and which tile shape they take, decided on the
+host (no GPU): the functions of csrc/gemm_i8_plan.h, which the kernels and
+their launches call too, in a small C++ program, and the loads of the built
+library.
 
 A read past an operand cannot be seen in a result (A counts as zero past K), so
 it is looked for here.
@@ -59,6 +60,37 @@ def test_loads_stay_inside_the_operand(tmp_path):
     if (records((size_t)1 << 40) % 16) return printf("a count inside an access\\n"), 0;
     printf("ok %ld\\n", checked);""")
     assert out.startswith("ok "), out
+
+
+def test_every_documented_size_has_a_launch(tmp_path):
+    """Up to 2^30 rows on either side (gated: 2^31 B rows) the picked shape's
+    launch holds fewer than 2^32 threads, and sizes that had one keep theirs."""
+    out = _run_cpp(tmp_path, """
+    int shapes[S_COUNT] = {};
+    for (long long cus : {256, 304, 64})
+        for (int K : {16, 128, 256, 2048, 131056})
+            for (int few : {1, 2, 5, 7, 8, 31, 32, 33, 64, 200, 256, 300})
+                for (int e = 0; e <= 30; ++e)
+                    for (int d = -3; d <= 3; d += 3)
+                        for (int side = 0; side < 3; ++side) {
+                            // a; b; b of a gated product, whose gate and up rows both count
+                            const long long many = (1LL << e) + d;
+                            if (many < 1 || many > 1LL << 30 || (many + 15) / 16 * ((few + 7) / 8) >= 1LL << 31) continue;
+                            const int M = side == 0 ? (int)many : few;
+                            const long long rows_b = side == 0 ? few : side == 1 ? many : 2 * many;
+                            const int s = pick_shape(M, rows_b, K, cus);
+                            const long long tiles = shape_tiles(s, M, rows_b), threads = tiles * 64 * split_waves(s, tiles <= cus);
+                            ++shapes[s];
+                            if (threads >= 1LL << 32) return printf("%d x %lld x %d, %lld CUs: shape %d, %lld threads\\n", M, rows_b, K, cus, s, threads), 0;
+                        }
+    for (int i = 0; i < S_COUNT; ++i)
+        if (!shapes[i]) return printf("shape %d is never picked\\n", i), 0;
+    const struct { int M, N, K, s; } known[] = {{1, 2048, 2048, S_32x32}, {32, 2048, 512, S_32x64}, {333, 1000, 4112, S_32x64}, {400, 2048, 2048, S_64x64},
+        {2048, 2048, 2048, S_128x128}, {16384, 256, 7168, S_128x128}, {16384, 2048, 2048, S_256x256}};
+    for (const auto& k : known)
+        if (pick_shape(k.M, k.N, k.K, 256) != k.s) return printf("%d x %d x %d: %d\\n", k.M, k.N, k.K, pick_shape(k.M, k.N, k.K, 256)), 0;
+    printf("ok\\n");""")
+    assert out.startswith("ok"), out
 
 
 @pytest.mark.skipif(not os.path.exists(OBJDUMP), reason="no disassembler for the built kernels")

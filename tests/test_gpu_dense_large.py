@@ -153,3 +153,38 @@ def test_products_one_side_of_which_is_very_long(gpu, M, N):
     few = moe.glu_i8(a[pick].contiguous(), sa[:len(pick)] * 2.0 ** -9, w13, torch.cat([sb, sb]))
     torch.cuda.synchronize()
     assert torch.equal(h[pick], few)
+
+
+@pytest.mark.parametrize("M,N", [(1 << 30, 1), (1, 1 << 30), ((1 << 29) + 77, 3)])
+def test_products_of_the_longest_sides(gpu, M, N):
+    """2^30 rows of either operand: more small tiles than a launch has threads for."""
+    import torch
+    K = 16
+    _say(f"[longest product] {M} x {N}")
+    a, b = _codes(gpu, M, K, 9), _codes(gpu, N, K, 10)
+    sa, sb = torch.full((M,), 2.0 ** -4, device=gpu), torch.ones(N, device=gpu)
+    out = torch.full((M, N), 7.0, dtype=torch.bfloat16, device=gpu)
+    moe.gemm_i8(a, sa, b, sb, out=out)
+    tall, few, got = (a, b, out) if M > N else (b, a, out.t())
+    for r in range(0, max(M, N), 1 << 26):
+        part = tall[r:r + (1 << 26)].float()
+        for j in range(few.shape[0]):
+            want = torch.zeros(part.shape[0], device=gpu)             # below 2^19: exact in fp32
+            for k in range(K):
+                want += part[:, k] * few[j, k].float()
+            assert torch.equal(got[r:r + (1 << 26), j], (want * 2.0 ** -4).to(torch.bfloat16)), (r, j)
+
+
+def test_gated_product_of_the_longest_side(gpu):
+    """2^29 gate and as many up rows: equal rows give equal outputs to a small call's."""
+    import torch
+    I, K, M = 1 << 29, 16, 2
+    _say(f"[longest gated product] {M} x {I}")
+    w, a = _codes(gpu, 2 * I, K, 11), _codes(gpu, M, K, 12)
+    sa, sw = torch.ones(M, device=gpu), torch.full((2 * I,), 2.0 ** -9, device=gpu)
+    h = torch.full((M, I), 7.0, dtype=torch.bfloat16, device=gpu)
+    moe.glu_i8(a, sa, w, sw, out=h)
+    for r in sorted({0, 1 << 20, I // 2 - 50, I - (1 << 16)}):
+        n = min(1 << 16, I - r)
+        few = torch.cat([w[r:r + n], w[I + r:I + r + n]])
+        assert torch.equal(h[:, r:r + n], moe.glu_i8(a, sa, few, sw[:2 * n])), r
