@@ -344,7 +344,9 @@ int moe_dequant_rows(const uint8_t* d_codes, const void* d_scales, int rows, int
  * The dense products that run for every token beside the routed experts (a
  * shared expert, the projections around the layer), on int8 matrix cores:
  *    out[m][n] = (sum_k a[m][k] * b[n][k]) * sa[m] * sb[n] (+ bias[n]) (+ add[m][n]);
- * the sum is an exact int32, the rest fp32, one rounding to the output type.
+ * the sum is an exact int32, the rest fp32 in this order: the sum as fp32, times
+ * sa, times sb plus bias in one rounding, plus add; one rounding to the output
+ * type.
  *  d_a i8 [M, K], d_sa f32 [M]: rows and scales as moe_norm and
  *  moe_quant_rows write them (a factor per token, such as a shared expert's
  *  gate, can be multiplied into d_sa); d_b i8 [N, K], d_sb f32 [N];
@@ -354,8 +356,9 @@ int moe_dequant_rows(const uint8_t* d_codes, const void* d_scales, int rows, int
  * moe_glu_i8, a shared expert's first half in one kernel: with g and u the
  * products of a with rows [0, I) (gate) and [I, 2I) (up) of d_w13 i8 [2I, K]
  * and their scales d_s13 f32 [2I], h = silu(g) * u, d_h bf16 [M, I].
- * Codes are any int8 (-128 included). The results do not depend on how the
- * work is split and repeat bit for bit.
+ * Codes are any int8 (-128 included). The results repeat bit for bit and do
+ * not depend on how the work is split: a row and column of a product is what a
+ * product of that row and column alone gives.
  * Limits: 1 <= M, N, I <= 2^30; K a multiple of 16, 16 <= K <= 131056; fewer than
  * 2^31 tiles of 16 x 8 outputs; d_a, d_b and d_w13 16-byte aligned. No
  * workspace is needed. */

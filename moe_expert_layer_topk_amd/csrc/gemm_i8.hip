@@ -31,7 +31,15 @@ struct GemmArgs {
     int lines;                // output rows are whole 128-byte lines (and add's address is 16-byte aligned)
 };
 
-__device__ const uint8_t g_zero16[16] = {0};            // source of K bytes past a row's end
+__device__ const float g_no_bias = -0.0f;               // (x + -0 is x for every x, zeros of both signs too)
+
+// One output before its addend, in this order in every kernel, so that its bits
+// do not depend on the tile: the sum in fp32, the row's scale, the column's
+// scale and the bias in one rounding. Addends come after it, and the compiler
+// may not draw their addition into the product (contract(off) there).
+__device__ __forceinline__ float scaled(int sum, float sa, float sb, float bias) {
+    return __builtin_fmaf((float)sum * sa, sb, bias);
+}
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     typedef float f2 __attribute__((ext_vector_type(2)));
@@ -80,6 +88,7 @@ struct Cols {
         for (int h = 0; h < NW; ++h) w[h] = q[h];
     }
     __device__ __forceinline__ void add_to(float (&v)[NC]) const {
+#pragma clang fp contract(off)
 #pragma unroll
         for (int n = 0; n < NC; ++n) {
             if (F32) v[n] += __uint_as_float(w[n / W][n % W]);
@@ -111,6 +120,7 @@ struct Cols {
 // of a 256 x 256 tile (8192 x 8191 x 8192 408 -> 452 us).
 template <int NC, bool F32>
 __device__ __forceinline__ void add_each(const GemmArgs& p, int row, int col, float (&v)[NC]) {
+#pragma clang fp contract(off)
     const size_t o = (size_t)min(row, p.M - 1) * p.N;
 #pragma unroll
     for (int n = 0; n < NC; ++n) {
@@ -266,7 +276,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gemm_tile_kernel(GemmArgs p, 
             const int c = 64 * i + ln;
             const int n = GLU ? min(col1 + c % OUTN, p.N - 1) + (c >= OUTN ? p.N : 0) : min(col1 + c, p.N - 1);
             lds_dma4(p.sb + n, (uint8_t*)(md + TM + 64 * i));
-            if (!GLU) lds_dma4(p.bias ? p.bias + n : (const float*)g_zero16, (uint8_t*)(md + TM + TN + 64 * i));
+            if (!GLU) lds_dma4(p.bias ? p.bias + n : &g_no_bias, (uint8_t*)(md + TM + TN + 64 * i));
         }
     };
     // load l of the 128 K bytes from k0 on (NOWHERE: no access) into stage st
@@ -358,13 +368,13 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gemm_tile_kernel(GemmArgs p, 
 #pragma unroll
         for (int n = 0; n < NF; ++n) sb[n] = md[TM + (GLU && n >= NC ? OUTN : 0) + cw + n % NC];
 #pragma unroll
-        for (int n = 0; n < NC; ++n) bias[n] = GLU ? 0.f : md[TM + TN + cw + n];
+        for (int n = 0; n < NC; ++n) bias[n] = GLU ? -0.f : md[TM + TN + cw + n];
         // lane (m, q), register i of fragment (a, n): row 16 (mw MF + a) + 4 q + i
         auto values = [&](int a, int i, float sa, float (&v)[NC]) __attribute__((always_inline)) {
 #pragma unroll
             for (int n = 0; n < NC; ++n) {
-                if constexpr (GLU) v[n] = glu_h((float)acc[a][n][i] * sa * sb[n], (float)acc[a][n + NC][i] * sa * sb[n + NC]);
-                else v[n] = (float)acc[a][n][i] * sa * sb[n] + bias[n];
+                v[n] = scaled(acc[a][n][i], sa, sb[n], bias[n]);
+                if constexpr (GLU) v[n] = glu_h(v[n], scaled(acc[a][n + NC][i], sa, sb[n + NC], -0.f));
             }
         };
 #pragma unroll
@@ -618,9 +628,8 @@ __global__ void __launch_bounds__(64 * WK) gemm_split_kernel(GemmArgs p, int til
         float v[4];
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
-            v[n] = (float)g[n] * sa * s_sb[c + n];
-            if constexpr (GLU) v[n] = glu_h(v[n], (float)u[n] * sa * s_sb[OUTN + c + n]);
-            else if (p.bias) v[n] += s_bias[c + n];
+            v[n] = scaled(g[n], sa, s_sb[c + n], !GLU && p.bias ? s_bias[c + n] : -0.f);
+            if constexpr (GLU) v[n] = glu_h(v[n], scaled(u[n], sa, s_sb[OUTN + c + n], -0.f));
         }
         const size_t o = (size_t)(row0 + r) * p.N + col0 + c;
         if (p.lines) {
