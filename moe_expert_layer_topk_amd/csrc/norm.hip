@@ -15,9 +15,12 @@
 // first, and again in fp64 where their argument lies near a border. e4m3 codes
 // come from y rounded to odd, which a second rounding to fewer bits leaves
 // correctly rounded.
-// Rows of int8 read from bf16 (quant_rows): 127 x / m is a border exactly, or
-// at least 1 / 512 away from it, so rounding the fp64 product to fp32 first
-// puts the exact ties back on the border.
+// Rows of int8 read from bf16 (quant_rows): with 8-bit mantissas X and M and x
+// j binades below m, 127 x / m = 127 X / (M 2^j) is a border exactly, or at
+// least 2^-16 of itself away from it (the least distance is 1 / 502 at j = 1,
+// 1 / 64768 at j = 8; from j = 9 on it is below 1 / 2). That is 2^8 half steps of fp32,
+// so rounding the fp64 product to fp32 first puts the exact ties back on the
+// border and moves nothing else across one.
 // A row (e4m3: a group) that holds NaN or infinity gets codes 0 and a NaN scale
 // (e4m3: the E8M0 NaN byte): an 8-bit code cannot carry them.
 //

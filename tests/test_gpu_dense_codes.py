@@ -1,0 +1,106 @@
+"""8-bit rows of the norm and the quantizer where a code is hardest to decide:
+arguments next to a border, weights, every output mode and kernel form.
+
+Tolerances: v = x + res is one fp32 rounding, and the reference takes it from
+there; sums, r and y are fp64 (relative errors of some 2^-50), so a code is the
+definition's wherever its argument is 2^-40 and more away from a border, and a
+bf16 output is two roundings away from y, to fp32 and to bf16: 2^-24 + 2^-8 of
+it, or 2^-134 below bf16's normal values (half a step).
+"""
+import numpy as np
+import pytest
+
+import moe_expert_layer_topk_amd as moe
+from oracle import dense, e4m3_decode
+from test_gpu_dense import HB, U, _bf16, _close, _f32, _f64, _rng, _rows_values, _say
+from test_gpu_dense_rows import _exact_rint, _i8_exact
+
+pytestmark = pytest.mark.gpu
+
+EPS = 1e-6
+
+
+def _e4m3_exact(codes, scales, y):
+    """e4m3 codes and E8M0 bytes against the definition of the unrounded y."""
+    T, H = y.shape
+    g = y.reshape(T, H // 128, 128)
+    m = np.abs(g).max(axis=2)
+    e = np.where(m > 0, np.ceil(np.log2(np.where(m > 0, m, 1.0) / 448)), 0).clip(-127, 127).astype(np.int64)
+    assert np.array_equal(scales.cpu().numpy().astype(np.int64) - 127, e)
+    z = g / np.exp2(e.astype(np.float64))[:, :, None]
+    step = np.exp2(np.maximum(np.floor(np.log2(np.maximum(np.abs(z), 2.0 ** -20))), -6) - 3)
+    t = z / step
+    far = np.abs(np.abs(t - np.floor(t)) - 0.5) > 2.0 ** -40
+    c = e4m3_decode(codes.cpu().numpy()).reshape(z.shape)
+    want = np.rint(t) * step
+    _say(f"    e4m3: {int((~far).sum())} of {t.size} on a border, {int((c != want)[far].sum())} differ")
+    assert np.array_equal(c[far], want[far])
+
+
+@pytest.mark.parametrize("T", [12, 1100])
+def test_quant_rows_next_to_every_kind_of_border(gpu, T):
+    """The bf16 pairs (x, m) whose 127 x / m lies closest to a border without
+    being on it, for each distance in binades (down to 1 / 64768: 255 2^-8 under
+    253), beside pairs that are on one."""
+    import torch
+    pairs = []
+    for j in range(9):
+        near = []
+        for X in range(128, 256):
+            for M in range(128, 256):
+                if j == 0 and X > M:
+                    continue
+                d = M << j
+                off = abs((254 * X) % (2 * d) - d)                    # |2 t - nearest odd number| in units of 1 / d
+                near.append((off / d, X, M, j))
+        near.sort()
+        pairs += [p[1:] for p in near if p[0] > 0][:24] + [p[1:] for p in near if p[0] == 0][:8]
+    x = np.zeros((len(pairs), 2 * len(pairs)))
+    for i, (X, M, j) in enumerate(pairs):
+        x[i, 0] = M
+        x[i, 1:len(pairs)] = X * 2.0 ** -j
+        x[i, len(pairs):] = -X * 2.0 ** -j
+    x *= np.exp2(np.arange(len(pairs)) % 60 - 30)[:, None]
+    if T > len(pairs):
+        x = np.concatenate([x] * (T // len(pairs) + 1))
+    xb = _bf16(x, gpu)
+    codes, scales = moe.quant_rows(xb)
+    torch.cuda.synchronize()
+    v = _f64(xb)
+    assert np.array_equal(v, x)
+    c = codes.cpu().numpy().astype(np.int64)
+    for lo in range(0, len(x), len(pairs)):                           # (the rows repeat)
+        assert np.array_equal(c[lo:lo + len(pairs)], c[:len(pairs)])
+    cols = [0, 1, 2, len(pairs) - 1, len(pairs), 2 * len(pairs) - 1]
+    want = _exact_rint(v[:len(pairs)][:, cols], np.abs(v[:len(pairs)]).max(axis=1))
+    assert np.array_equal(c[:len(pairs)][:, cols], want)
+    assert np.array_equal(c[:len(pairs), 1:len(pairs)], np.repeat(want[:, 1:2], len(pairs) - 1, axis=1))
+    assert np.array_equal(c[:len(pairs), len(pairs):], np.repeat(want[:, 4:5], len(pairs), axis=1))
+
+
+@pytest.mark.parametrize("T,H,shift", [(1, 128, 0), (70, 256, 0), (1100, 512, 0), (6, 16384, 0), (2100, 2048, 0), (5, 4096, 0),
+                                       (3, 7, 0), (1030, 333, 0), (9, 4099, 0), (9, 512, 1), (4, 2176, 4)])
+@pytest.mark.parametrize("res,w", [(True, True), (True, False), (False, True), (False, False)])
+def test_norm_in_every_mode(gpu, T, H, shift, res, w):
+    import torch
+    r = _rng(T, H, shift, res, w, 81)
+    x = _bf16(_rows_values(r, T, H), gpu, shift)
+    rs = _bf16(_rows_values(r, T, H), gpu, shift) if res else None
+    wt = _f32(1 + 0.2 * r.normal(size=H), gpu) if w else None
+    v = x.float() + rs.float() if res else x.float()
+    v64 = v.double().cpu().numpy()
+    ry, _ = dense.rms_norm(v64, None if wt is None else _f64(wt), float(np.float32(EPS)))
+    modes = [moe.Q_NONE, moe.Q_I8_ROW] + ([moe.Q_FP8_G128_POW2] if H % 128 == 0 and not shift else [])
+    for q in modes:
+        _say(f"[norm] T={T} H={H} shift={shift} res={res} w={w} q={q}")
+        y, total, codes, scales = moe.norm(x, wt, EPS, res=rs, q_mode=q)
+        torch.cuda.synchronize()
+        _close("y", _f64(y), ry, np.abs(ry) * (HB + U + 2.0 ** -40) + 2.0 ** -134)
+        if res:
+            assert torch.equal(total, v.to(torch.bfloat16))
+        if q == moe.Q_I8_ROW:
+            t, s = dense.i8_rows(ry)
+            _i8_exact("codes", codes, t)
+            _close("scales", _f64(scales), s, s * (U + 2.0 ** -40))
+        if q == moe.Q_FP8_G128_POW2:
+            _e4m3_exact(codes, scales, ry)
