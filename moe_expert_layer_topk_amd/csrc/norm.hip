@@ -12,7 +12,8 @@
 // The squares' sum, r and y are fp64, and so is every code that could depend on
 // it: a code changes where its argument passes a border, so an error of 2^-24
 // would change some ten codes in a million. int8 codes are formed in fp32
-// first, and again in fp64 where their argument lies near a border. e4m3 codes
+// first, and again in fp64 where their argument lies near a border, ties to the
+// even code. e4m3 codes
 // come from y rounded to odd, which a second rounding to fewer bits leaves
 // correctly rounded.
 // Rows of int8 read from bf16 (quant_rows): with 8-bit mantissas X and M and x
@@ -154,11 +155,15 @@ __device__ __forceinline__ void i8_scale(Peak p, double r, double* s_max, uint32
     *mul = r * (127.0 * rcp_f64(m));
     *quick = p.m >= 0x1p-100 && p.m <= 0x1p+120 ? (float)*mul : 0.f;
 }
-// the low byte of the result is the code
+// the low byte of the result is the code. u * mul is within 2^-43 of 127 y / m
+// (|.| <= 127); in rows without weights, and with weights that are powers of
+// two, r drops out of that and it can be a border exactly, so it is rounded to a
+// multiple of 2^-40 first, which puts those ties back (adding 3/2 2^12, whose
+// step that is, and taking it off again).
 template <bool NORM>
 __device__ __forceinline__ int i8_code(double u, double mul) {
     if (mul == 0.0) return 0;
-    return NORM ? (int)rint(u * mul) : (int)rintf((float)(u * mul));
+    return NORM ? (int)rint((u * mul + 0x1.8p12) - 0x1.8p12) : (int)rintf((float)(u * mul));
 }
 // y rounded to odd at 20 mantissa bits: the upper word, its last bit set where the lower is not zero
 __device__ __forceinline__ float to_odd(double y) {

@@ -104,3 +104,34 @@ def test_norm_in_every_mode(gpu, T, H, shift, res, w):
             _close("scales", _f64(scales), s, s * (U + 2.0 ** -40))
         if q == moe.Q_FP8_G128_POW2:
             _e4m3_exact(codes, scales, ry)
+
+
+@pytest.mark.parametrize("T,H,shift", [(40, 512, 0), (1100, 256, 0), (1030, 333, 0), (2100, 1032, 0), (9, 512, 1), (5, 4099, 0)])
+@pytest.mark.parametrize("res,w", [(False, False), (True, False), (False, True)])
+def test_norm_codes_with_ties(gpu, T, H, shift, res, w):
+    """127 y / m does not depend on r, so rows of small integers have it exactly
+    on a border (with weights that are powers of two as well): ties go to the
+    even code, decided here in integers."""
+    import torch
+    r = _rng(T, H, shift, res, w, 82)
+    x = r.integers(-255, 256, (T, H)).astype(np.float64)
+    tops = np.array([256, 254, 508, 2, 4, 384, 320, 255, 512, 380])[np.arange(T) % 10]
+    x = np.clip(x, -tops[:, None], tops[:, None])
+    x[np.arange(T), np.arange(T) % H] = tops
+    x *= np.exp2(r.integers(-20, 20, (T, 1)))
+    xb = _bf16(x, gpu, shift)
+    rs = _bf16(-0.5 * x, gpu, shift) if res else None                 # (the sum is x / 2)
+    wt = np.full(H, 0.25) if w else None
+    if w:
+        wt[r.random(H) < 0.3] = 0.125
+    v = x * (0.5 if res else 1.0)
+    assert np.array_equal(_f64(xb), x)
+    _, _, codes, _ = moe.norm(xb, None if wt is None else _f32(wt, gpu), EPS, res=rs, q_mode=moe.Q_I8_ROW)
+    torch.cuda.synchronize()
+    u = v * (1.0 if wt is None else wt[None, :])
+    rows = np.unique(np.concatenate([np.arange(min(T, 20)), [T - 2, T - 1]]))
+    want = _exact_rint(u[rows], np.abs(u[rows]).max(axis=1))
+    t = 127 * u[rows] / np.abs(u[rows]).max(axis=1, keepdims=True)
+    c = codes.cpu().numpy().astype(np.int64)[rows]
+    _say(f"    ties {int((np.abs(t - np.floor(t)) == 0.5).sum())} of {t.size}, {int((c != want).sum())} differ")
+    assert np.array_equal(c, want)
