@@ -135,3 +135,33 @@ def test_norm_codes_with_ties(gpu, T, H, shift, res, w):
     c = codes.cpu().numpy().astype(np.int64)[rows]
     _say(f"    ties {int((np.abs(t - np.floor(t)) == 0.5).sum())} of {t.size}, {int((c != want).sum())} differ")
     assert np.array_equal(c, want)
+
+
+@pytest.mark.parametrize("T", [40, 1100])
+@pytest.mark.parametrize("e", [-120, -124, -126, -128, -131])
+def test_norm_e4m3_codes_of_tiny_rows(gpu, T, e):
+    """y around 2^e: below 2^-126 fp32 holds fewer digits, and the scale stops at 2^-127."""
+    import torch
+    H = 1024
+    r = _rng(T, -e, 83)
+    x = _bf16(r.normal(size=(T, H)), gpu)
+    w = _f32(2.0 ** e * (1 + r.integers(0, 64, H) / 64), gpu)         # (a few digits: fp32's subnormals hold them)
+    _, _, codes, scales = moe.norm(x, w, EPS, q_mode=moe.Q_FP8_G128_POW2)
+    torch.cuda.synchronize()
+    ry, _ = dense.rms_norm(_f64(x), _f64(w), float(np.float32(EPS)))
+    _e4m3_exact(codes, scales, ry)
+
+
+@pytest.mark.parametrize("T", [5, 1100])
+def test_norm_e4m3_codes_of_tiny_groups_beside_huge_ones(gpu, T):
+    """Groups around 2^-124 and around 2^110 in one row, and in one wave."""
+    import torch
+    H = 1024
+    r = _rng(T, 84)
+    x = _bf16(r.normal(size=(T, H)), gpu)
+    e = np.repeat(np.array([-124, 110, 110, -131, 0, -118, -124, 100]), 128)
+    w = _f32(2.0 ** e * (1 + r.integers(0, 64, H) / 64), gpu)
+    _, _, codes, scales = moe.norm(x, w, EPS, q_mode=moe.Q_FP8_G128_POW2)
+    torch.cuda.synchronize()
+    ry, _ = dense.rms_norm(_f64(x), _f64(w), float(np.float32(EPS)))
+    _e4m3_exact(codes, scales, ry)
