@@ -319,7 +319,9 @@ int moe_quant_act(const uint16_t* d_x, int rows, int cols, uint8_t* d_codes, uin
  *     (ties to even); code * scale stands for y;
  *   MOE_Q_FP8_G128_POW2: d_codes u8 [rows, cols] and d_scales u8
  *     [rows, cols / 128]: the e4m3 codes and E8M0 bytes of moe_quant_act, of
- *     the unrounded y (cols % 128 == 0, every pointer 16-byte aligned);
+ *     the unrounded y (cols % 128 == 0, every pointer 16-byte aligned), for
+ *     products of the caller's own and moe_dequant_rows: moe_layer and
+ *     moe_expert_ffn take bf16 d_x and quantize it themselves;
  *   MOE_Q_NONE: neither (both NULL).
  *  d_x bf16 [rows, cols]; d_res the same or NULL; d_weight f32 [cols] or NULL
  *  (ones); d_sum and d_y may be NULL, but something has to be written.
@@ -348,8 +350,8 @@ int moe_dequant_rows(const uint8_t* d_codes, const void* d_scales, int rows, int
  * sa, times sb plus bias in one rounding, plus add; one rounding to the output
  * type.
  *  d_a i8 [M, K], d_sa f32 [M]: rows and scales as moe_norm and
- *  moe_quant_rows write them (a factor per token, such as a shared expert's
- *  gate, can be multiplied into d_sa); d_b i8 [N, K], d_sb f32 [N];
+ *  moe_quant_rows write them, which take up to 16384 columns (a factor per token,
+ *  such as a shared expert's gate, can be multiplied into d_sa); d_b i8 [N, K], d_sb f32 [N];
  *  d_bias f32 [N] or NULL; d_add [M, N] of the output's type or NULL (it may
  *  be d_out itself); d_out bf16 [M, N] (MOE_OUT_BF16) or f32 (MOE_OUT_F32), no
  *  other overlap.

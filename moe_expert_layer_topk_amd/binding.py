@@ -439,7 +439,9 @@ def quant_act(x, codes=None, exps=None, stream=None):
 # ---------------------------------------------------------------- norm, int8 products
 # Small calls of these are bound by the host: their tensors are looked at,
 # their outputs allocated and the C ABI called in _marshal.so (csrc/marshal.cpp),
-# on the current stream of the tensors' device.
+# on the current stream of the tensors' device. Outputs are allocated past
+# torch's dispatcher (its modes do not see them), and no call has a gradient:
+# an input that requires one is read, the outputs require none.
 _marshal = None
 
 
@@ -478,6 +480,8 @@ def norm(x, weight=None, eps=1e-6, res=None, q_mode=Q_NONE, with_y=True, sum=Non
     bf16 residual stream x + res (None without res, unless passed), codes and
     scales as q_mode says (Q_I8_ROW: int8 codes, fp32 scale per row;
     Q_FP8_G128_POW2: e4m3 bytes, E8M0 byte per 128 columns; Q_NONE: None).
+    The int8 rows are gemm_i8's and glu_i8's operand; layer and expert_ffn take
+    the bf16 y and quantize it themselves.
     Outputs not passed are allocated; sum and y may be x or res themselves."""
     if stream is not None:
         return _on(stream, norm, x, weight, eps, res, q_mode, with_y, sum, y, codes, scales)

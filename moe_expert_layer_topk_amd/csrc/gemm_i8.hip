@@ -159,8 +159,9 @@ __device__ __forceinline__ void store_each(const GemmArgs& p, int row, int col, 
 // with it took 14.5 us at 2048^3 instead of 12.7.
 //
 // Bound by the chip's power: on random codes the loop runs at 1.6-1.9 GHz
-// (2.4 GHz on zeros, 1.4 times as fast), with the matrix pipe busy about 80% of
-// the clocks. So what counts is energy per output: 16x16x64 instructions
+// (2.4 GHz on zeros, 1.4 times as fast), with the matrix pipe busy 75% of the
+// clocks at 4096 x 8192 x 8192, 61% at 16384 x 2048 x 2048 and 55% at gated 16384
+// x 512 x 2048, where two tiles' prologues and epilogues a CU count. So what counts is energy per output: 16x16x64 instructions
 // (registers only: 3950 TOPS on random codes; 32x32x32: 2920), tiles as large
 // as LDS allows, few instructions beside the matrix ones. 8192^3: 408 us, 2690
 // TOPS (a library product with int32 output on the same card 457-465 us); 4096
@@ -498,9 +499,11 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gemm_tile_kernel(GemmArgs p, 
 // more workgroups on a CU, beat more stages (a barrier for each step and four
 // shared stages: 333 x 1000 x 4112 9.8 us, this 8.9; 256 x 2048 x 2048 5.6 and
 // 5.0; 481 x 2496 x 1632 10.9 and 9.6; two or three stages a wave in between).
-// With one row the weights stream at HBM's rate (1 x 8192 x 8192: 10.6 us, 6.3
-// TB/s, most of it launch and first latency below 2048 x 2048: 4.0 us); with
-// more, bound by L2 to LDS loads (about 50 bytes a clock and CU). A kernel that
+// With one row the weights stream at HBM's rate: 1 x 8192 x 8192 takes 13.3 us,
+// 5.05 TB/s, with twelve weight matrices in turn (a 1 GiB copy on the same card:
+// 5.1), and 10.7 us where the one matrix of 67 MB stays in the last-level cache.
+// Below 2048 x 2048 most of it is launch and first latency (4.0 us). With more
+// rows, bound by L2 to LDS loads (about 50 bytes a clock and CU). A kernel that
 // streamed B straight into registers for up to 32 rows was no faster at one
 // row and up to 1.4 times slower at 16.
 template <int TM, int TN, int WK, bool GLU, bool F32>

@@ -5,6 +5,12 @@
 // Here a call checks its tensors, allocates the outputs that were not passed
 // and calls the C ABI on the current stream of the tensors' device: no
 // arithmetic, and the same checks and errors for every caller.
+//
+// Outputs come from torch's allocator past its dispatcher, which takes longer
+// than the allocator: dispatch modes (and the filling of new tensors that
+// torch's deterministic mode does) do not see them. Like the rest of the
+// library these calls have no gradient; an input that requires one is read, and
+// the outputs require none.
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>

@@ -165,3 +165,42 @@ def test_norm_e4m3_codes_of_tiny_groups_beside_huge_ones(gpu, T):
     torch.cuda.synchronize()
     ry, _ = dense.rms_norm(_f64(x), _f64(w), float(np.float32(EPS)))
     _e4m3_exact(codes, scales, ry)
+
+
+def test_inputs_that_require_a_gradient_are_read(gpu):
+    """No operator has a gradient: outputs require none, and are what the plain tensors give."""
+    import torch
+    r = _rng(85)
+    x = _bf16(r.normal(size=(5, 64)), gpu)
+    w = _f32(1 + 0.1 * r.normal(size=64), gpu)
+    b, sb = torch.zeros(16, 64, dtype=torch.int8, device=gpu) + 3, _f32(np.ones(16), gpu)
+    plain = moe.norm(x, w, q_mode=moe.Q_I8_ROW)
+    xg, wg, sg = x.clone().requires_grad_(), w.clone().requires_grad_(), sb.clone().requires_grad_()
+    y, _, codes, scales = moe.norm(xg, wg, q_mode=moe.Q_I8_ROW)
+    out = moe.gemm_i8(codes, scales, b, sg)
+    torch.cuda.synchronize()
+    assert not (y.requires_grad or scales.requires_grad or out.requires_grad)
+    assert torch.equal(y, plain[0]) and torch.equal(codes, plain[2]) and torch.equal(scales, plain[3])
+    assert torch.equal(out, moe.gemm_i8(plain[2], plain[3], b, sb))
+
+
+@pytest.mark.parametrize("T,H,shift,q", [(5, 256, 0, 2), (1100, 512, 0, 2), (3, 4096, 0, 2), (7, 512, 1, 1), (1030, 333, 0, 1), (3, 4099, 3, 1),
+                                         (9, 100, 5, 0)])
+def test_norm_in_place_in_every_form(gpu, T, H, shift, q):
+    """sum in x's memory and y in res's, and the other way round, on every kind of rows."""
+    import torch
+    r = _rng(T, H, shift, q, 86)
+    x, rs = _bf16(_rows_values(r, T, H), gpu, shift), _bf16(_rows_values(r, T, H), gpu, shift)
+    w = _f32(1 + 0.2 * r.normal(size=H), gpu)
+    want = moe.norm(x, w, EPS, res=rs, q_mode=q)
+    for swap in (False, True):
+        bx, br = torch.full((T * H + 16,), 7.0, dtype=torch.bfloat16, device=gpu), torch.full((T * H + 16,), 7.0, dtype=torch.bfloat16, device=gpu)
+        x2, r2 = bx[shift:shift + T * H].view(T, H), br[shift:shift + T * H].view(T, H)
+        x2.copy_(x)
+        r2.copy_(rs)
+        got = moe.norm(x2, w, EPS, res=r2, q_mode=q, sum=r2 if swap else x2, y=x2 if swap else r2)
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert (a is None and b is None) or torch.equal(a, b)
+        for buf in (bx, br):
+            assert (buf[:shift] == 7).all() and (buf[shift + T * H:] == 7).all()
