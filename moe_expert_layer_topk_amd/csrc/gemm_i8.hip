@@ -161,10 +161,10 @@ __device__ __forceinline__ void store_each(const GemmArgs& p, int row, int col, 
 // Bound by the chip's power: on random codes the loop runs at 1.6-1.9 GHz
 // (2.4 GHz on zeros, 1.4 times as fast), with the matrix pipe busy 75% of the
 // clocks at 4096 x 8192 x 8192, 61% at 16384 x 2048 x 2048 and 55% at gated 16384
-// x 512 x 2048, where two tiles' prologues and epilogues a CU count. So what counts is energy per output: 16x16x64 instructions
-// (registers only: 3950 TOPS on random codes; 32x32x32: 2920), tiles as large
-// as LDS allows, few instructions beside the matrix ones. 8192^3: 408 us, 2690
-// TOPS (a library product with int32 output on the same card 457-465 us); 4096
+// x 512 x 2048, where two tiles' prologues and epilogues a CU count. So
+// what counts is energy per output: 16x16x64 instructions (registers only: 3950
+// TOPS on random codes; 32x32x32: 2920), tiles as large as LDS allows, few
+// instructions beside the matrix ones. 8192^3: 409 us, 2690 TOPS (a library product with int32 output on the same card 457-465 us); 4096
 // x 8192 x 8192 210 us (253); 16384 x 2048 x 2048 61 us (81); gated 16384 x 512
 // x 2048 30.4 us. Measured without gain: 256 x 128 tiles with three stages, four
 // 128 x 128 waves (the compiler spills), places of the barrier and the loads

@@ -28,8 +28,9 @@ constexpr int records_from(int all, int k0) { return all - k0 > 0 ? all - k0 : 0
 // workgroup on each CU (`one`) and with all `per_cu` of them (`full`), and a
 // round's prologue and epilogue (`round`). K <= 128 counts as one step; the
 // persistent tiles run a second one there, of zeros. One `round` stands for plain
-// and gated epilogues, with and without addends, on rows of every kind. Large tiles move fewer bytes per
-// output, small ones reach more CUs. The figures are a fit to 1100 products
+// and gated epilogues, with and without addends, on rows of every
+// kind. Large tiles move fewer bytes per output, small ones reach more CUs. The
+// figures are a fit to 1100 products
 // with random sizes (1..16384 rows, 64..8192 columns, K 128..8192), each timed
 // with every shape: where the best takes 5.5 us and more, the shape picked by
 // them is 0.6% slower than it on average (below, the five differ by little more
