@@ -11,13 +11,9 @@
 // which K bytes a lane holds.
 #include "moe_common.h"
 #include "moe_kernels.h"
-#include "gemm_i8_plan.h"
-
-#include <atomic>
+#include "gemm_tile.h"
 
 namespace moe {
-
-typedef int i32x16 __attribute__((ext_vector_type(16)));
 
 struct GemmArgs {
     const int8_t* a;
@@ -31,113 +27,12 @@ struct GemmArgs {
     int lines;                // output rows are whole 128-byte lines (and add's address is 16-byte aligned)
 };
 
-__device__ const float g_no_bias = -0.0f;               // (x + -0 is x for every x, zeros of both signs too)
-
 // One output before its addend, in this order in every kernel, so that its bits
 // do not depend on the tile: the sum in fp32, the row's scale, the column's
 // scale and the bias in one rounding. Addends come after it, and the compiler
 // may not draw their addition into the product (contract(off) there).
 __device__ __forceinline__ float scaled(int sum, float sa, float sb, float bias) {
     return __builtin_fmaf((float)sum * sa, sb, bias);
-}
-
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-    typedef float f2 __attribute__((ext_vector_type(2)));
-    typedef __bf16 b2 __attribute__((ext_vector_type(2)));
-    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f2){a, b}, b2));
-}
-// silu(g) u; the hardware's base-2 exponential and reciprocal are within one
-// step of fp32 each (the correctly rounded division costs ten instructions more
-// in an epilogue that no matrix instruction hides: gated 16384 x 512 x 2048
-// 37.2 us with it)
-__device__ __forceinline__ float glu_h(float g, float u) {
-    return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269504088896341f)) * u;   // (g u first could overflow)
-}
-
-// Workgroup barrier that waits for the wave's LDS traffic only (the fence of
-// __syncthreads() would drain the direct-to-LDS loads in flight).
-static __device__ __forceinline__ void barrier_lds() {
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt(0xC07F);                // lgkmcnt(0)
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-}
-
-// NC adjacent output columns of one row, all of them inside it, in accesses of
-// up to 16 bytes. !ANY: rows are whole 128-byte lines. Outputs are written once
-// and not read here, so they are stored past the caches' order of use, and a
-// launch does not end by writing back what its last tiles left in L2 (16384 x
-// 2048 x 512 with the addend 39 -> 35 us, gated 16384 x 512 x 2048 31.4 ->
-// 30.2, others the same).
-// ANY: rows of any length that start at any element. Here such stores would
-// write parts of lines to memory one by one (15007 x 1928 x 128 32 us, stored
-// through L2 19; 10357 x 752 x 208 with the addend 11.2 and 10.2). Accesses
-// that are not aligned to their size are split by the memory pipeline, which
-// is still fewer than one for each value (5324 x 437 x 1408 with the addend
-// 24.2 us one by one, 16.3 so; 4096 x 1999 x 2048 25.1 and 21.5).
-template <int NC, bool F32, bool ANY = false>
-struct Cols {
-    typedef uint32_t word __attribute__((ext_vector_type(NC == 2 && !F32 ? 1 : NC * (F32 ? 4 : 2) / 4 < 4 ? NC * (F32 ? 4 : 2) / 4 : 4)));
-    typedef word place __attribute__((aligned(ANY ? (F32 ? 4 : 2) : sizeof(word))));
-    static constexpr int W = sizeof(word) / 4;                   // dwords of an access
-    static constexpr int NW = NC * (F32 ? 4 : 2) / (4 * W);      // accesses
-    word w[NW];
-    __device__ __forceinline__ void load(const void* p, size_t o) {
-        const place* q = (const place*)((const uint8_t*)p + o * (F32 ? 4 : 2));
-#pragma unroll
-        for (int h = 0; h < NW; ++h) w[h] = q[h];
-    }
-    __device__ __forceinline__ void add_to(float (&v)[NC]) const {
-#pragma clang fp contract(off)
-#pragma unroll
-        for (int n = 0; n < NC; ++n) {
-            if (F32) v[n] += __uint_as_float(w[n / W][n % W]);
-            else {
-                const uint32_t d = w[n / 2 / W][n / 2 % W];
-                v[n] += __uint_as_float(n & 1 ? d & 0xFFFF0000u : d << 16);
-            }
-        }
-    }
-    __device__ __forceinline__ static void store(void* p, size_t o, const float (&v)[NC]) {
-        Cols c;
-#pragma unroll
-        for (int d = 0; d < NW * W; ++d) {
-            if (F32) c.w[d / W][d % W] = __float_as_uint(v[d]);
-            else c.w[d / W][d % W] = pack_bf16(v[2 * d], v[2 * d + 1]);
-        }
-        place* q = (place*)((uint8_t*)p + o * (F32 ? 4 : 2));
-#pragma unroll
-        for (int h = 0; h < NW; ++h) {
-            if (ANY) q[h] = c.w[h];
-            else __builtin_nontemporal_store(c.w[h], q + h);
-        }
-    }
-};
-// the columns of them that exist, one by one: addends, outputs. Up to four
-// columns load without a branch (past the row's end its last addend), so that
-// no load waits in a branch of its own (10357 x 755 x 208 with the addend 18.5
-// -> 14.5 us); with eight the addresses would take registers from the step loop
-// of a 256 x 256 tile (8192 x 8191 x 8192 408 -> 452 us).
-template <int NC, bool F32>
-__device__ __forceinline__ void add_each(const GemmArgs& p, int row, int col, float (&v)[NC]) {
-#pragma clang fp contract(off)
-    const size_t o = (size_t)min(row, p.M - 1) * p.N;
-#pragma unroll
-    for (int n = 0; n < NC; ++n) {
-        if (NC > 4 && col + n >= p.N) continue;
-        const size_t i = o + min(col + n, p.N - 1);
-        v[n] += F32 ? ((const float*)p.add)[i] : bf16_to_f32(((const uint16_t*)p.add)[i]);
-    }
-}
-template <int NC, bool F32>
-__device__ __forceinline__ void store_each(const GemmArgs& p, int row, int col, const float (&v)[NC]) {
-    const size_t o = (size_t)row * p.N + col;
-#pragma unroll
-    for (int n = 0; n < NC; ++n) {
-        if (col + n >= p.N) continue;
-        if (F32) ((float*)p.out)[o + n] = v[n];
-        else ((uint16_t*)p.out)[o + n] = (uint16_t)pack_bf16(v[n], 0.f);
-    }
 }
 
 // ------------------------------------------------------------------ tiles
@@ -169,33 +64,6 @@ __device__ __forceinline__ void store_each(const GemmArgs& p, int row, int col, 
 // x 2048 30.4 us. Measured without gain: 256 x 128 tiles with three stages, four
 // 128 x 128 waves (the compiler spills), places of the barrier and the loads
 // between the matrix instructions.
-template <int V>
-struct IC {
-    static constexpr int value = V;
-};
-
-// Rows of an operand from a tile's first one on, as a buffer: accesses past its
-// end return nothing. Each K position has a descriptor of its own, based there
-// and holding the records that are left, and no scalar offset. The check that
-// drops an access then compares the lane's offset alone, which every
-// description of it agrees on; of a scalar offset the compiler's intrinsic says
-// that it is left out of the check, the MI300 instruction set that it is taken
-// off the record count, and neither what happens where it exceeds that count.
-struct Operand {
-    const uint8_t* p;
-    int bytes;
-    __device__ __forceinline__ void set(const int8_t* first, size_t n) {
-        p = (const uint8_t*)first;
-        bytes = records(n);
-    }
-    // 16 bytes a lane, from lane offset o at K position k, to dst + 16 lane
-    __device__ __forceinline__ void load_lds(uint8_t* dst, uint32_t o, int k) const {
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            __builtin_amdgcn_make_buffer_rsrc((void*)(p + k), 0, records_from(bytes, k), 0x00027000),
-            (__attribute__((address_space(3))) void*)dst, 16, (int)o, 0, 0, 0);
-    }
-};
-
 template <int TM, int TN, int WM, int WN, int R, bool GLU, bool F32, bool ANY>
 __global__ void __launch_bounds__(64 * WM * WN, 2) gemm_tile_kernel(GemmArgs p, int tiles_m, int tiles_n) {
     constexpr int WAVES = WM * WN;
@@ -658,16 +526,6 @@ __global__ void __launch_bounds__(64 * WK) gemm_split_kernel(GemmArgs p, int til
 }
 
 // ------------------------------------------------------------------ launch
-// Raises a kernel's dynamic LDS limit, once for each device (the call costs
-// more than the launch's other checks together; racing callers repeat it).
-static hipError_t allow_lds(const void* kernel, int bytes, int dev, std::atomic<uint64_t>& done) {
-    const uint64_t bit = 1ull << (dev & 63);
-    if (dev < 64 && (done.load(std::memory_order_relaxed) & bit)) return hipSuccess;
-    const hipError_t e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == hipSuccess && dev < 64) done.fetch_or(bit, std::memory_order_relaxed);
-    return e;
-}
-
 template <int TM, int TN, int WM, int WN, int R, bool GLU, bool F32, bool ANY>
 static hipError_t launch_tile(const GemmArgs& p, int dev, int kid, hipStream_t stream) {
     constexpr int OUTN = GLU ? TN / 2 : TN;
@@ -725,8 +583,6 @@ static hipError_t launch_any(const GemmArgs& p, int kid, hipStream_t stream) {
         default: return launch_split<32, 32, split_waves(S_32x32, false), GLU, F32>(p, dev, kid, stream);
     }
 }
-
-static bool whole_lines(const void* p, int cols, int size) { return ((uintptr_t)p | (uintptr_t)cols * size) % 128 == 0; }
 
 hipError_t launch_gemm_i8(const int8_t* a, const float* sa, const int8_t* b, const float* sb, const float* bias,
                           const void* add, int M, int N, int K, bool f32, void* out, bool aligned, hipStream_t stream) {
