@@ -370,6 +370,72 @@ int moe_gemm_i8(const int8_t* d_a, const float* d_sa, const int8_t* d_b, const f
 int moe_glu_i8(const int8_t* d_a, const float* d_sa, const int8_t* d_w13, const float* d_s13, int M, int I, int K,
                uint16_t* d_h, void* stream);
 
+/* ---------------------------------------------------------------- FP8 products
+ * The same dense products on e4m3 codes, with the scales of official FP8
+ * checkpoints ([VEP] introduction): an fp32 scale for every 128 x 128 block of
+ * the weights, and for the rows the power of two per 128 columns that moe_norm
+ * (MOE_Q_FP8_G128_POW2) and moe_quant_act write:
+ *    out[m][n] = sum_j sb[n / 128][j] * x_j[m][n] (+ bias[n]) (+ add[m][n]),
+ *    x_j[m][n] = 2^(sa[m][j] - 127) * sum_{128 j <= k < 128 (j + 1)} a[m][k] * b[n][k];
+ * the sum over j is fp32 (a fused multiply-add a block), then bias, then add;
+ * one rounding to the output type. x_j is fp32 where the output is; for bf16
+ * outputs it is the FP8 matrix instruction's, which drops what lies 14 bits and
+ * more below the largest product (1e-4 of the outputs' norm on normal values,
+ * where their rounding is 1.7e-3).
+ *  d_a u8 [M, K] and d_b u8 [N, K]: e4m3 codes; d_sa u8 [M, ceil(K / 128)]: E8M0
+ *  bytes (255 is NaN); d_sb f32 [ceil(N / 128), ceil(K / 128)]; the rest
+ *  as in moe_gemm_i8 (d_add may be d_out itself, no other overlap).
+ * moe_glu_fp8: moe_glu_i8's gated form; d_w13 u8 [2I, K], its gate rows first,
+ * d_s13 f32 [2 ceil(I / 128), ceil(K / 128)]: the gate rows' blocks, then the up
+ * rows', each counted from its own first row.
+ * NaN codes (0x7F, 0xFF) and NaN scales spread into the outputs that they
+ * enter, and x_j past the largest fp32 is infinite. Results repeat bit for bit; the
+ * order of the sum over j depends on M, N and K, so a row may differ in its
+ * last fp32 bits between products of different sizes.
+ * Limits and alignment as for moe_gemm_i8 (d_sa and d_sb: their types'). No
+ * workspace. */
+int moe_gemm_fp8(const uint8_t* d_a, const uint8_t* d_sa, const uint8_t* d_b, const float* d_sb, const float* d_bias,
+                 const void* d_add, int M, int N, int K, int out_type, void* d_out, void* stream);
+int moe_glu_fp8(const uint8_t* d_a, const uint8_t* d_sa, const uint8_t* d_w13, const float* d_s13, int M, int I, int K,
+                uint16_t* d_h, void* stream);
+
+/* ---------------------------------------------------------------- sampling
+ * One token per row of logits, from the caller's random numbers. Per row, with
+ * l the logits, z = l / temperature, w_i = exp(z_i - max z):
+ *  1. order: tokens by logit, largest first, ties by id, lowest first; -inf
+ *     (a masked token) is never kept;
+ *  2. top_k: the first top_k tokens of that order (top_k <= 0: all);
+ *  3. top_p: of those, the tokens whose weights before them in the order sum
+ *     to less than top_p times the weight of all of them, the first one always
+ *     (top_p >= 1: all);
+ *  4. min_p: of those, the tokens with w_i >= min_p (min_p <= 0: all);
+ *  5. the draw: the lowest id whose kept weights, summed by id up to and with
+ *     it, exceed u times the kept weight of all.
+ * temperature 0 is greedy: the first token of the order, whatever the rest
+ * say. d_ids[r] gets the id, d_p[r] its weight divided by the kept weight of
+ * all (1 if greedy).
+ * Weights are formed in fp64 and summed as integers, in multiples of 2^-42
+ * of the row's largest: sums have no order, results repeat bit for bit, and
+ * a token of less than half of that is never drawn.
+ *  d_logits f32 (MOE_OUT_F32) or bf16 (MOE_OUT_BF16) [rows, cols], rows
+ *  row_stride >= cols elements apart (a head padded to a larger vocabulary);
+ *  d_u f32 [rows] in [0, 1]; d_temperature f32 [rows], d_top_k i32 [rows],
+ *  d_top_p f32 [rows], d_min_p f32 [rows], each NULL for 1, 0, 1, 0;
+ *  d_ids i32 [rows]; d_p f32 [rows] or NULL; d_err i32 [1] or NULL.
+ * A row gets id -1 and p 0 and is counted in d_err where it has no token to
+ * draw (every logit -inf), a logit is NaN or +inf, u is NaN or outside [0, 1],
+ * the temperature negative or NaN, top_p or min_p NaN, or min_p > 1.
+ * The inputs are not written; no output overlaps another array. Limits: 1 <=
+ * rows <= MOE_SAMPLE_MAX_ROWS, 1 <= cols <= MOE_SAMPLE_MAX_COLS. Workspace:
+ * moe_sample_workspace_bytes(rows, cols) bytes (0: none), 256-byte aligned,
+ * written before it is read; calls that overlap in time need one each. */
+#define MOE_SAMPLE_MAX_ROWS 65535
+#define MOE_SAMPLE_MAX_COLS (1 << 20)
+size_t moe_sample_workspace_bytes(int rows, int cols);
+int moe_sample(const void* d_logits, int logits_type, int rows, int cols, long long row_stride, const float* d_u,
+               const float* d_temperature, const int32_t* d_top_k, const float* d_top_p, const float* d_min_p,
+               int32_t* d_ids, float* d_p, int32_t* d_err, void* d_ws, size_t ws_bytes, void* stream);
+
 /* ---------------------------------------------------------------- pool check
  * [VEP] "hierarchical paging of expert weights": slots are refilled while
  * the model runs. Every FFN call treats a slot as not resident (its pairs add

@@ -76,6 +76,10 @@ def _declare(lib):
         "moe_dequant_rows": (c_int, [P, P, c_int, c_int, c_int, P, P]),
         "moe_gemm_i8": (c_int, [P, P, P, P, P, P, c_int, c_int, c_int, c_int, P, P]),
         "moe_glu_i8": (c_int, [P, P, P, P, c_int, c_int, c_int, P, P]),
+        "moe_gemm_fp8": (c_int, [P, P, P, P, P, P, c_int, c_int, c_int, c_int, P, P]),
+        "moe_glu_fp8": (c_int, [P, P, P, P, c_int, c_int, c_int, P, P]),
+        "moe_sample_workspace_bytes": (c_size_t, [c_int, c_int]),
+        "moe_sample": (c_int, [P, c_int, c_int, c_int, ctypes.c_longlong, P, P, P, P, P, P, P, P, P, c_size_t, P]),
         "moe_pool_check": (c_int, [ctypes.POINTER(moe_slot_pool), P, P, P]),
         "moe_debug_poison": (c_int, [c_int]),
         "moe_bitwidth_plan": (c_int, [P, c_int, c_int, P]),
@@ -529,6 +533,69 @@ def shared_expert_i8(a, sa, w13, s13, w2, s2, add=None, out=None, stream=None):
         return _on(stream, shared_expert_i8, a, sa, w13, s13, w2, s2, add, out)
     hq, hs = quant_rows(glu_i8(a, sa, w13, s13))
     return gemm_i8(hq, hs, w2, s2, add=add, out=out)
+
+
+def gemm_fp8(a, sa, b, sb, bias=None, add=None, out=None, out_dtype=None, stream=None):
+    """moe_gemm_fp8: (a * sa) @ (b * sb).T (+ bias) (+ add) of e4m3 a [M, K] and
+    b [N, K] (uint8 or torch.float8_e4m3fn). sa: E8M0 bytes [M, ceil(K / 128)]
+    (uint8 or torch.float8_e8m0fnu), as norm and quant_act give them; sb: fp32
+    [ceil(N / 128), ceil(K / 128)], a scale per 128 x 128 block. out bf16
+    (default) or fp32 [M, N]; add has out's type and may be out itself."""
+    if stream is not None:
+        return _on(stream, gemm_fp8, a, sa, b, sb, bias, add, out, out_dtype)
+    return (_marshal or _load_marshal()).gemm_fp8(a, sa, b, sb, bias, add, out, out_dtype)
+
+
+def glu_fp8(a, sa, w13, s13, out=None, stream=None):
+    """moe_glu_fp8: silu(g) * u in bf16 [M, I], with g and u the FP8 products of
+    a [M, K] with rows [0, I) and [I, 2I) of w13 [2I, K]; s13 fp32
+    [2 ceil(I / 128), ceil(K / 128)]: the gate rows' block scales, then the up rows'."""
+    if stream is not None:
+        return _on(stream, glu_fp8, a, sa, w13, s13, out)
+    return (_marshal or _load_marshal()).glu_fp8(a, sa, w13, s13, out)
+
+
+def shared_expert_fp8(a, sa, w13, s13, w2, s2, add=None, out=None, stream=None):
+    """shared_expert_i8 on FP8 weights: gated product, rows back to e4m3, down
+    product (+ add, the routed experts' output; out may be add itself). a e4m3
+    [T, H] and sa as norm or quant_act give them; w13 e4m3 [2I, H], w2 e4m3
+    [H, I] with I a multiple of 128, s13 and s2 their block scales. Returns bf16 [T, H]."""
+    if stream is not None:
+        return _on(stream, shared_expert_fp8, a, sa, w13, s13, w2, s2, add, out)
+    h = glu_fp8(a, sa, w13, s13)
+    hq, hs = _marshal.quant_act(h, None, None)
+    return gemm_fp8(hq, hs, w2, s2, add=add, out=out)
+
+
+# ---------------------------------------------------------------- sampling
+def sample_workspace_bytes(rows, cols):
+    return int(lib().moe_sample_workspace_bytes(rows, cols))
+
+
+def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, ids=None, p=None, err=None, ws=None,
+           stream=None):
+    """moe_sample: one token per row of fp32 or bf16 logits [rows, cols], drawn
+    with u fp32 [rows] in [0, 1]; the rows may be parts of longer ones.
+    temperature fp32 (0: greedy), top_k int32 (0: off), top_p and min_p fp32,
+    each [rows] or None. Returns (ids int32 [rows], p fp32 [rows] (the token's
+    share of the kept weight), err): a row without a token, or with values that
+    allow none, gets id -1 and p 0 and is counted in err (int32 [1], if passed)."""
+    if stream is not None:
+        return _on(stream, sample, logits, u, temperature, top_k, top_p, min_p, ids, p, err, ws)
+    return (_marshal or _load_marshal()).sample(logits, u, temperature, top_k, top_p, min_p, ids, p, err, ws)
+
+
+def next_token(a, sa, w, s, u, bias=None, temperature=None, top_k=None, top_p=None, min_p=None, logits=None, err=None,
+               stream=None):
+    """The end of a decode step: the head's fp32 logits (gemm_fp8 of the normed
+    e4m3 rows a, sa with the head's weights w [vocabulary, H] and block scales s)
+    and a token drawn from each row. Returns (ids, p, logits)."""
+    if stream is not None:
+        return _on(stream, next_token, a, sa, w, s, u, bias, temperature, top_k, top_p, min_p, logits, err)
+    import torch
+    logits = gemm_fp8(a, sa, w, s, bias=bias, out=logits, out_dtype=torch.float32)
+    ids, p, _ = sample(logits, u, temperature, top_k, top_p, min_p, err=err)
+    return ids, p, logits
 
 
 def pool_check(pool, err=None, status=None, stream=None):

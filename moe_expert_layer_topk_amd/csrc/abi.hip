@@ -372,6 +372,41 @@ int moe_glu_i8(const int8_t* d_a, const float* d_sa, const int8_t* d_w13, const 
     return hip_status(moe::launch_glu_i8(d_a, d_sa, d_w13, d_s13, M, I, K, d_h, aligned16(d_h), (hipStream_t)stream));
 }
 
+int moe_gemm_fp8(const uint8_t* d_a, const uint8_t* d_sa, const uint8_t* d_b, const float* d_sb, const float* d_bias,
+                 const void* d_add, int M, int N, int K, int out_type, void* d_out, void* stream) {
+    if (!d_a || !d_sa || !d_b || !d_sb || !d_out || !valid_product(M, N, K) || !aligned16(d_a, d_b)) return MOE_EINVAL;
+    if (out_type != MOE_OUT_BF16 && out_type != MOE_OUT_F32) return MOE_EINVAL;
+    return hip_status(moe::launch_gemm_fp8(d_a, d_sa, d_b, d_sb, d_bias, d_add, M, N, K, out_type == MOE_OUT_F32, d_out,
+                                           aligned16(d_out, d_add), (hipStream_t)stream));
+}
+
+int moe_glu_fp8(const uint8_t* d_a, const uint8_t* d_sa, const uint8_t* d_w13, const float* d_s13, int M, int I, int K,
+                uint16_t* d_h, void* stream) {
+    if (!d_a || !d_sa || !d_w13 || !d_s13 || !d_h || !valid_product(M, I, K) || !aligned16(d_a, d_w13))
+        return MOE_EINVAL;
+    return hip_status(moe::launch_glu_fp8(d_a, d_sa, d_w13, d_s13, M, I, K, d_h, aligned16(d_h), (hipStream_t)stream));
+}
+
+size_t moe_sample_workspace_bytes(int rows, int cols) {
+    if (rows < 1 || rows > MOE_SAMPLE_MAX_ROWS || cols < 1 || cols > MOE_SAMPLE_MAX_COLS) return 0;
+    return moe::sample_workspace_bytes(rows, cols);
+}
+
+int moe_sample(const void* d_logits, int logits_type, int rows, int cols, long long row_stride, const float* d_u,
+               const float* d_temperature, const int32_t* d_top_k, const float* d_top_p, const float* d_min_p,
+               int32_t* d_ids, float* d_p, int32_t* d_err, void* d_ws, size_t ws_bytes, void* stream) {
+    if (!d_logits || !d_u || !d_ids || rows < 1 || rows > MOE_SAMPLE_MAX_ROWS || cols < 1 || cols > MOE_SAMPLE_MAX_COLS)
+        return MOE_EINVAL;
+    if (logits_type != MOE_OUT_BF16 && logits_type != MOE_OUT_F32) return MOE_EINVAL;
+    if (row_stride < cols || row_stride > (1LL << 40)) return MOE_EINVAL;
+    const int size = logits_type == MOE_OUT_F32 ? 4 : 2;
+    if ((uintptr_t)d_logits % size) return MOE_EINVAL;
+    const size_t need = moe::sample_workspace_bytes(rows, cols);
+    if (need && (!d_ws || ws_bytes < need || (uintptr_t)d_ws % 256)) return MOE_EINVAL;
+    const moe::SampleArgs a{d_logits, row_stride, rows, cols, d_u, d_temperature, d_top_k, d_top_p, d_min_p, d_ids, d_p, d_err};
+    return hip_status(moe::launch_sample(a, logits_type == MOE_OUT_F32, d_ws, (hipStream_t)stream));
+}
+
 int moe_pool_check(const moe_slot_pool* pool, int32_t* d_err, uint8_t* d_status, void* stream) {
     moe::PoolArgs pa;
     if (!pool_args(pool, &pa) || !d_err) return MOE_EINVAL;

@@ -68,6 +68,14 @@ struct Current {
     Current(const Current&) = delete;
 };
 
+constexpr auto BF16 = at::kBFloat16, F32 = at::kFloat, I32 = at::kInt, I8 = at::kChar, U8 = at::kByte;
+
+// bytes come as uint8 or as the 8-bit float type that they hold
+at::ScalarType byte_type(PyObject* o, at::ScalarType floats, const char* name) {
+    const at::Tensor& t = tensor(o, name);
+    return t.defined() && t.scalar_type() == floats ? floats : U8;
+}
+
 struct Matrix {
     const at::Tensor& t;
     int rows, cols;
@@ -156,8 +164,6 @@ PyObject* tuple(const T&... t) {
     return r;
 }
 
-constexpr auto BF16 = at::kBFloat16, F32 = at::kFloat, I8 = at::kChar, U8 = at::kByte;
-
 // (x, weight, eps, res, q_mode, with_y, sum, y, codes, scales) -> (y, sum, codes, scales)
 PyObject* py_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
@@ -223,6 +229,17 @@ PyObject* py_dequant_rows(PyObject*, PyObject* const* a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
+// out_dtype, else the type of out, else bf16
+at::ScalarType out_type(PyObject* dtype, PyObject* out) {
+    at::ScalarType ot = BF16;
+    if (dtype != Py_None) {
+        if (!THPDtype_Check(dtype)) refuse("out_dtype must be a dtype");
+        ot = reinterpret_cast<THPDtype*>(dtype)->scalar_type;
+    } else if (out != Py_None) ot = tensor(out, "out").scalar_type();
+    if (ot != BF16 && ot != F32) refuse(std::string("out must be bfloat16 or float32, got ") + c10::toString(ot));
+    return ot;
+}
+
 // a and b of a product: as many columns, on one device
 void fit(const Matrix& a, const Matrix& b, const char* name) {
     if (b.cols != a.cols || b.dev != a.dev) refuse(std::string("a ") + said(a.t) + " and " + name + " " + said(b.t) + " do not fit");
@@ -235,12 +252,7 @@ PyObject* py_gemm_i8(PyObject*, PyObject* const* v, Py_ssize_t n) {
     const Matrix a = matrix(v[0], I8, "a"), b = matrix(v[2], I8, "b");
     fit(a, b, "b");
     const Current on(a.dev);
-    at::ScalarType ot = BF16;
-    if (v[7] != Py_None) {
-        if (!THPDtype_Check(v[7])) refuse("out_dtype must be a dtype");
-        ot = reinterpret_cast<THPDtype*>(v[7])->scalar_type;
-    } else if (v[6] != Py_None) ot = tensor(v[6], "out").scalar_type();
-    if (ot != BF16 && ot != F32) refuse(std::string("out must be bfloat16 or float32, got ") + c10::toString(ot));
+    const at::ScalarType ot = out_type(v[7], v[6]);
     const int M = a.rows, N = b.rows;
     const void* sa = needed(v[1], a, M, -1, F32, "sa");
     const void* sb = needed(v[3], a, N, -1, F32, "sb");
@@ -275,6 +287,110 @@ PyObject* py_glu_i8(PyObject*, PyObject* const* v, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
+// (x, codes, exps) -> (codes, exps)
+PyObject* py_quant_act(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    count(n, 3, "quant_act");
+    const Matrix x = matrix(a[0], BF16, "x");
+    const Current on(x.dev);
+    const Out codes(a[1], x, x.rows, x.cols, U8, "codes"), exps(a[2], x, x.rows, x.cols / 128, U8, "exps");
+    run(x, [&](void* st) {
+        return moe_quant_act((const uint16_t*)x.t.data_ptr(), x.rows, x.cols, (uint8_t*)codes.p, (uint8_t*)exps.p, st);
+    });
+    return tuple(codes.t, exps.t);
+    END_HANDLE_TH_ERRORS
+}
+
+constexpr auto E4M3 = at::kFloat8_e4m3fn, E8M0 = at::kFloat8_e8m0fnu;
+int64_t blocks(int n) { return ((int64_t)n + 127) / 128; }
+
+// (a, sa, b, sb, bias, add, out, out_dtype) -> out
+PyObject* py_gemm_fp8(PyObject*, PyObject* const* v, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    count(n, 8, "gemm_fp8");
+    const Matrix a = matrix(v[0], byte_type(v[0], E4M3, "a"), "a"), b = matrix(v[2], byte_type(v[2], E4M3, "b"), "b");
+    fit(a, b, "b");
+    const Current on(a.dev);
+    const at::ScalarType ot = out_type(v[7], v[6]);
+    const int M = a.rows, N = b.rows;
+    const int64_t kb = blocks(a.cols);
+    const void* sa = needed(v[1], a, M, kb, byte_type(v[1], E8M0, "sa"), "sa");
+    const void* sb = needed(v[3], a, blocks(N), kb, F32, "sb");
+    const void* bias = given(v[4], a, N, -1, F32, "bias");
+    const void* add = given(v[5], a, M, N, ot, "add");
+    const Out out(v[6], a, M, N, ot, "out");
+    run(a, [&](void* st) {
+        return moe_gemm_fp8((const uint8_t*)a.t.data_ptr(), (const uint8_t*)sa, (const uint8_t*)b.t.data_ptr(),
+                            (const float*)sb, (const float*)bias, add, M, N, a.cols, ot == F32 ? MOE_OUT_F32 : MOE_OUT_BF16,
+                            out.p, st);
+    });
+    return wrap(out.t);
+    END_HANDLE_TH_ERRORS
+}
+
+// (a, sa, w13, s13, out) -> out
+PyObject* py_glu_fp8(PyObject*, PyObject* const* v, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    count(n, 5, "glu_fp8");
+    const Matrix a = matrix(v[0], byte_type(v[0], E4M3, "a"), "a"), w = matrix(v[2], byte_type(v[2], E4M3, "w13"), "w13");
+    fit(a, w, "w13");
+    const Current on(a.dev);
+    if (w.rows % 2) refuse("w13 holds gate and up rows, as many of each: got " + std::to_string(w.rows) + " rows");
+    const int M = a.rows, I = w.rows / 2;
+    const int64_t kb = blocks(a.cols);
+    const void* sa = needed(v[1], a, M, kb, byte_type(v[1], E8M0, "sa"), "sa");
+    const void* s13 = needed(v[3], a, 2 * blocks(I), kb, F32, "s13");
+    const Out out(v[4], a, M, I, BF16, "out");
+    run(a, [&](void* st) {
+        return moe_glu_fp8((const uint8_t*)a.t.data_ptr(), (const uint8_t*)sa, (const uint8_t*)w.t.data_ptr(),
+                           (const float*)s13, M, I, a.cols, (uint16_t*)out.p, st);
+    });
+    return wrap(out.t);
+    END_HANDLE_TH_ERRORS
+}
+
+// (logits, u, temperature, top_k, top_p, min_p, ids, p, err, ws) -> (ids, p, err)
+PyObject* py_sample(PyObject*, PyObject* const* v, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    count(n, 10, "sample");
+    const at::Tensor& t = tensor(v[0], "logits");
+    if (!t.defined()) refuse("logits must be a tensor");
+    const bool f32 = t.scalar_type() == F32;
+    // (the rows may be parts of longer ones; one row's stride says nothing)
+    if (!t.is_cuda() || (!f32 && t.scalar_type() != BF16) || t.layout() != at::kStrided || t.is_neg() || t.dim() != 2 ||
+        t.numel() == 0 || t.size(0) > INT32_MAX || t.size(1) > INT32_MAX || (t.size(1) > 1 && t.stride(1) != 1) ||
+        (t.size(0) > 1 && t.stride(0) < t.size(1)))
+        refuse("logits must be a non-empty BFloat16 or Float matrix on the device whose rows are contiguous and do not overlap, got " +
+               said(t));
+    const Matrix l{t, (int)t.size(0), (int)t.size(1), t.device()};
+    const Current on(l.dev);
+    const int B = l.rows, V = l.cols;
+    const long long stride = B > 1 ? t.stride(0) : V;
+    const void* u = needed(v[1], l, B, -1, F32, "u");
+    const void* temp = given(v[2], l, B, -1, F32, "temperature");
+    const void* top_k = given(v[3], l, B, -1, I32, "top_k");
+    const void* top_p = given(v[4], l, B, -1, F32, "top_p");
+    const void* min_p = given(v[5], l, B, -1, F32, "min_p");
+    const Out ids(v[6], l, B, -1, I32, "ids"), p(v[7], l, B, -1, F32, "p");
+    void* err = given(v[8], l, 1, -1, I32, "err");
+    const size_t need = moe_sample_workspace_bytes(B, V);
+    Out ws;
+    size_t bytes = need;
+    if (v[9] != Py_None) {
+        ws.t = tensor(v[9], "ws");
+        if (!plain(ws.t, U8) || ws.t.device() != l.dev) refuse("ws must be a contiguous Byte tensor on " + l.dev.str() + ", got " + said(ws.t));
+        bytes = (size_t)ws.t.numel();
+        ws.p = ws.t.data_ptr();
+    } else if (need) ws = Out(Py_None, l, (int64_t)need, -1, U8, "ws");
+    run(l, [&](void* st) {
+        return moe_sample(t.data_ptr(), f32 ? MOE_OUT_F32 : MOE_OUT_BF16, B, V, stride, (const float*)u, (const float*)temp,
+                          (const int32_t*)top_k, (const float*)top_p, (const float*)min_p, (int32_t*)ids.p, (float*)p.p,
+                          (int32_t*)err, ws.p, bytes, st);
+    });
+    return tuple(ids.t, p.t, tensor(v[8], "err"));
+    END_HANDLE_TH_ERRORS
+}
+
 // (MoeError,): the exception that refusals raise
 PyObject* py_set_error(PyObject*, PyObject* const* a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
@@ -293,7 +409,8 @@ PyMethodDef method(const char* name) {
 
 PyMethodDef g_methods[] = {method<py_norm>("norm"), method<py_quant_rows>("quant_rows"),
                            method<py_dequant_rows>("dequant_rows"), method<py_gemm_i8>("gemm_i8"),
-                           method<py_glu_i8>("glu_i8"), method<py_set_error>("set_error"), {nullptr, nullptr, 0, nullptr}};
+                           method<py_glu_i8>("glu_i8"), method<py_quant_act>("quant_act"),
+                           method<py_gemm_fp8>("gemm_fp8"), method<py_glu_fp8>("glu_fp8"), method<py_sample>("sample"), method<py_set_error>("set_error"), {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -14,7 +14,7 @@ int record_hip_error(int hip_error);
 // kernel ids for launch tracing (names in profile.hip)
 enum KernelId { K_ROUTE, K_ROUTE_ALIGN, K_ALIGN_SINGLE, K_ALIGN_HIST, K_ALIGN_SCAN, K_ALIGN_SCATTER, K_GEMM1_STREAM,
                 K_GEMM2_STREAM, K_QUANT_ACT, K_GEMM1_FP8, K_GEMM2_FP8, K_GEMM1_TILE, K_GEMM2_TILE, K_MFMA_PREP, K_COMBINE, K_DEQUANT, K_POOL_CHECK, K_POISON, K_ROUTER_GEMM, K_REQUANT, K_UNPACK,
-                K_NORM, K_QUANT_ROWS, K_DEQUANT_ROWS, K_GEMM_I8, K_GLU_I8, K_COUNT };
+                K_NORM, K_QUANT_ROWS, K_DEQUANT_ROWS, K_GEMM_I8, K_GLU_I8, K_GEMM_FP8, K_GLU_FP8, K_SAMPLE, K_COUNT };
 // events the next launch of kernel `kid` on `s` should stamp (false: not tracing)
 bool prof_events(int kid, hipStream_t s, hipEvent_t* start, hipEvent_t* stop);
 
@@ -147,6 +147,30 @@ hipError_t launch_gemm_i8(const int8_t* a, const float* sa, const int8_t* b, con
                           const void* add, int M, int N, int K, bool f32, void* out, bool aligned, hipStream_t stream);
 hipError_t launch_glu_i8(const int8_t* a, const float* sa, const int8_t* w13, const float* s13, int M, int I, int K,
                          uint16_t* h, bool aligned, hipStream_t stream);
+
+// e4m3 products with a scale for each block of 128 (gemm_fp8.hip); aligned: out (and add) are 16-byte aligned
+hipError_t launch_gemm_fp8(const uint8_t* a, const uint8_t* sa, const uint8_t* b, const float* sb, const float* bias,
+                           const void* add, int M, int N, int K, bool f32, void* out, bool aligned, hipStream_t stream);
+hipError_t launch_glu_fp8(const uint8_t* a, const uint8_t* sa, const uint8_t* w13, const float* s13, int M, int I, int K,
+                          uint16_t* h, bool aligned, hipStream_t stream);
+
+// one token per row of logits (sample.hip)
+int sample_max_cols();
+struct SampleArgs {
+    const void* logits;       // rows of V values, stride elements apart
+    long long stride;
+    int B, V;
+    const float* u;
+    const float* temperature; // each of these may be null
+    const int32_t* top_k;
+    const float* top_p;
+    const float* min_p;
+    int32_t* ids;
+    float* p;                 // may be null
+    int32_t* err;             // may be null
+};
+size_t sample_workspace_bytes(int B, int V);
+hipError_t launch_sample(const SampleArgs& a, bool f32, void* ws, hipStream_t stream);
 
 // pool validation (pool_check.hip): d_err += unusable slots; status[slot] optional
 hipError_t launch_pool_check(const PoolArgs& pa, int32_t* err, uint8_t* status, hipStream_t stream);
