@@ -63,17 +63,17 @@ constexpr int split_waves(int shape, bool few) {
     return shape == S_32x32 ? 8 : shape == S_64x64 || shape == S_32x64 ? (few ? 8 : 4) : 0;
 }
 
-// The shape that the costs above make the fastest for this many output rows
+// The shape that a table's costs make the fastest for this many output rows
 // and B rows. Small tiles have a workgroup each, and a launch holds fewer than
 // 2^32 threads: where theirs would hold more (2^23 tiles of eight waves, 2^24 of
 // four: some 2^29 rows on one side) they are left out; a persistent grid takes
 // any number of tiles.
-constexpr int pick_shape(int M, long long rows_b, int K, long long cus) {
+constexpr int pick_shape(const Shape (&table)[S_COUNT], int M, long long rows_b, int K, long long cus) {
     const float steps = (float)((K + 127) / 128);
     int best = 0;
     float least = 3.4e38f;
     for (int i = 0; i < S_COUNT; ++i) {
-        const Shape& c = kShapes[i];
+        const Shape& c = table[i];
         const long long tiles = shape_tiles(i, M, rows_b), slots = cus * c.per_cu;
         if (tiles * 64 * split_waves(i, tiles <= cus) >= 1LL << 32) continue;
         const long long rounds = tiles / slots, rest = tiles % slots;
@@ -86,5 +86,19 @@ constexpr int pick_shape(int M, long long rows_b, int K, long long cus) {
     }
     return best;
 }
+constexpr int pick_shape(int M, long long rows_b, int K, long long cus) { return pick_shape(kShapes, M, rows_b, K, cus); }
+
+// The e4m3 products (gemm_fp8.hip) have the same shapes at costs of their own,
+// with fp32 outputs no 256 x 256 tile.
+constexpr Shape kShapesFp8[S_COUNT] = {{256, 256, 1, 1.17f, 1.17f, 2.45f},
+                                       {128, 128, 2, 0.41f, 0.79f, 1.09f},
+                                       {64, 64, 2, 0.10f, 0.41f, 1.13f},
+                                       {32, 64, 3, 0.06f, 0.42f, 0.70f},
+                                       {32, 32, 2, 0.012f, 0.19f, 1.06f}};
+constexpr Shape kShapesFp8F32[S_COUNT] = {{256, 256, 1, 1e6f, 1e6f, 1e6f},
+                                          {128, 128, 2, 1e6f, 1e6f, 1e6f},
+                                          {64, 64, 2, 0.15f, 0.6f, 1.13f},
+                                          {32, 64, 3, 0.09f, 0.6f, 0.70f},
+                                          {32, 32, 2, 0.015f, 0.25f, 1.06f}};
 
 }  // namespace moe

@@ -126,7 +126,7 @@ struct IC {
 struct Operand {
     const uint8_t* p;
     int bytes;
-    __device__ __forceinline__ void set(const int8_t* first, size_t n) {
+    __device__ __forceinline__ void set(const void* first, size_t n) {
         p = (const uint8_t*)first;
         bytes = records(n);
     }

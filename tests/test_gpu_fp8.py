@@ -83,7 +83,7 @@ def _within(name, got, ref, tol):
 SHAPES = [(1, 1, 16), (1, 2048, 2048), (1, 17, 8192), (2, 300, 144), (7, 64, 128), (16, 129, 112), (32, 2048, 512), (31, 33, 1040),
           (33, 128, 4112), (64, 513, 256), (65, 127, 400), (100, 1000, 2064), (128, 128, 128), (130, 260, 640), (255, 257, 272),
           (256, 256, 256), (257, 511, 2048), (333, 1000, 4112), (700, 2048, 384), (1030, 770, 528), (2049, 1300, 1152),
-          (4100, 2048, 256), (5000, 2056, 16)]
+          (4100, 2048, 256), (5000, 2056, 16), (1500, 1100, 6160), (4100, 2100, 4112), (4096, 2048, 4608), (1024, 2048, 2304)]
 
 
 @pytest.mark.parametrize("M,N,K", SHAPES)
@@ -134,7 +134,8 @@ def test_gemm(gpu, M, N, K, bias, add, f32, shift):
 
 
 @pytest.mark.parametrize("M,I,K", [(1, 1, 16), (1, 512, 2048), (8, 512, 2048), (5, 100, 272), (33, 129, 128), (64, 768, 2048), (129, 200, 400),
-                                   (300, 512, 1040), (520, 130, 2048), (1025, 512, 256), (3000, 700, 144), (4099, 512, 384)])
+                                   (300, 512, 1040), (520, 130, 2048), (1025, 512, 256), (3000, 700, 144), (4099, 512, 384), (2500, 700, 2320),
+                                   (4096, 1024, 2176)])
 def test_glu(gpu, M, I, K):
     import torch
     r = np.random.default_rng([3, M, I, K])
