@@ -155,7 +155,6 @@ hipError_t launch_glu_fp8(const uint8_t* a, const uint8_t* sa, const uint8_t* w1
                           uint16_t* h, bool aligned, hipStream_t stream);
 
 // one token per row of logits (sample.hip)
-int sample_max_cols();
 struct SampleArgs {
     const void* logits;       // rows of V values, stride elements apart
     long long stride;
