@@ -5,23 +5,25 @@
 // border, a (logit, id), describes them: every token before it or equal to it,
 // with w >= min_p. The draw is a search in the sums of their weights by id.
 //
-// chunk kernel: one workgroup for each 1024 E logits, which it reads once and
-// holds in registers. It writes the chunk's largest and smallest logit, its weight and,
-// for rows with a filter, the tokens that the filter could keep, in the order of
-// their ids. A chunk can tell from itself alone, with m its largest logit, S its
-// weight (relative to m), V the row's length:
+// chunk kernel: one workgroup for each 4096 logits, which it reads once and
+// holds in registers. It writes the chunk's largest and smallest logit, its
+// weight and, for rows with a filter, the tokens that the filter could keep, in the
+// order of their ids. A chunk can tell from itself alone, with m its largest
+// logit, S its weight (relative to m), V the row's length:
 //   top_k: a token that k tokens of the chunk precede is out;
 //   min_p: the row's largest logit is m at least, so w < min_p relative to m is out;
 //   top_p: at least (1 - top_p) of the weight lies at and behind the last kept
 //     token, on at most V tokens that weigh no more than it, so w < (1 - top_p) S / V is out.
 // With top_k and top_p only the first holds: top_p's share is one of the weight
-// of all k tokens.
-// finish kernel: one workgroup a row. Few candidates (nearly always, with a
-// filter): sorted in LDS, borders from prefix sums. No filter: the chunk that
-// the draw falls into is read again. Else (a top_p that keeps thousands of
-// tokens) the row is read again: counts and weights of 2048 equal parts of
-// the logits' range, the tokens of the part that holds the border sorted, the
-// kept weight by id.
+// of all k tokens. A chunk writes no more than its share of a row's LIST; where
+// it has more candidates, it writes the first of the order and the largest
+// logit that it left out.
+// finish kernel: one workgroup a row. Candidates are sorted in LDS, borders come
+// from prefix sums, and hold if they lie before every logit that was left out
+// (nearly always, with a filter). No filter: the chunk that the draw falls into
+// is read again. Else (a top_p that keeps thousands of tokens) the row is read
+// again: counts and weights of 2048 equal parts of the logits' range, the
+// tokens of the part that holds the border sorted, the kept weight by id.
 //
 // Weights are fp64, sums of them fp64 in a fixed order; the parts' weights are
 // summed with atomics, and therefore as integers (multiples of 2^-42 of the
@@ -32,19 +34,19 @@
 
 namespace moe {
 
-constexpr int ST = 1024, SW = ST / 64;                           // threads, waves of a workgroup
-constexpr int CAP = 1536;                                        // candidates of a chunk that are written
-constexpr int LIST = 4096;                                       // candidates of a row that are sorted
+constexpr int ST = 1024;                                         // threads of a finish workgroup
+constexpr int CHUNK = 4096;                                      // logits of a chunk
+constexpr int MAX_CHUNKS = MOE_SAMPLE_MAX_COLS / CHUNK;
+constexpr int LIST = 4096;                                       // candidates of a row
 constexpr int BINS = 2048;
-constexpr int MAX_CHUNKS = 256;
 constexpr double ONE = 4398046511104.0;                          // 2^42: the sum of 2^20 weights stays below 2^63
 constexpr float INF = __builtin_inff();
 
 struct Chunk {
     double sum;               // weight relative to `top`
     float top, low;           // largest (+inf: NaN or +inf among them) and smallest logit that is not -inf
-    int n;                    // candidates, CAP + 1 for more than CAP
-    int pad;
+    float cut;                // largest candidate that is not written; -inf: all are
+    int n;                    // candidates that are
 };
 
 // larger float, larger key; zeros of both signs are one value
@@ -96,11 +98,23 @@ struct Request {
         p_on = tp < 1.f && k != 1;
         m_on = mp > 0.f && k != 1;
     }
-    // the smallest logit whose weight could reach w beside a logit of m, rounded down
+    // a logit below which the weight does not reach w beside a logit of m (the
+    // hardware's logarithm and fp32's steps are far within the 1e-5)
     __device__ __forceinline__ float least(float m, double w) const {
-        if (!(w > 0.0) || temperature == INF) return -INF;
-        const double d = log(w) * temperature;
-        return (float)((double)m + d - (fabs((double)m) + fabs(d)) * 1e-6);
+        const float f = (float)w;
+        if (!(f > 0.f) || temperature == INF) return -INF;
+        const float d = __builtin_amdgcn_logf(f) * 0.693147181f * temperature;
+        return m + d - (fabsf(m) + fabsf(d) + temperature) * 1e-5f;
+    }
+    // with `m` the largest logit and `sum` the weight of (a part of) the row:
+    // tokens below are not kept, or weigh less than 2^-46 of the largest
+    __device__ __forceinline__ float floor(float m, double sum, int V) const {
+        double w = 1.0 / 70368744177664.0;
+        if (!(k && p_on)) {
+            if (m_on) w = fmax(w, min_p);
+            if (p_on) w = fmax(w, (1.0 - top_p) * sum / V);
+        }
+        return least(m, fmin(w, 1.0));
     }
 };
 
@@ -128,79 +142,112 @@ __device__ __forceinline__ void load_logits(const void* row, int i, int V, float
     }
 }
 
-// ---- over the workgroup; `s` holds one value a wave and is free again after the next barrier
-template <typename T, typename F>
-__device__ __forceinline__ T block_reduce(T v, F f, T* s) {
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) v = f(v, (T)__shfl_xor(v, o, 64));
-    __syncthreads();
-    if (lane_id() == 0) s[threadIdx.x / 64] = v;
-    __syncthreads();
-    v = s[lane_id() & (SW - 1)];
-#pragma unroll
-    for (int o = SW / 2; o > 0; o >>= 1) v = f(v, (T)__shfl_xor(v, o, 64));
-    return v;
+// ---- over a wave by lane moves in the vector unit
+template <int CTRL, int ROWS, typename T>
+__device__ __forceinline__ T moved(T v, T none) {
+    if constexpr (sizeof(T) == 4) {
+        return __builtin_bit_cast(T, __builtin_amdgcn_update_dpp(__builtin_bit_cast(int, none), __builtin_bit_cast(int, v), CTRL, ROWS, 0xF, false));
+    } else {
+        const int2 a = __builtin_bit_cast(int2, v), b = __builtin_bit_cast(int2, none);
+        return __builtin_bit_cast(T, make_int2(__builtin_amdgcn_update_dpp(b.x, a.x, CTRL, ROWS, 0xF, false),
+                                               __builtin_amdgcn_update_dpp(b.y, a.y, CTRL, ROWS, 0xF, false)));
+    }
 }
 struct Plus {
     template <typename T>
-    __device__ __forceinline__ T operator()(T x, T y) const { return x + y; }
+    __device__ __forceinline__ static T of(T x, T y) { return x + y; }
+    template <typename T>
+    __device__ __forceinline__ static T none() { return (T)0; }
 };
 struct Most {
     template <typename T>
-    __device__ __forceinline__ T operator()(T x, T y) const { return x > y ? x : y; }
+    __device__ __forceinline__ static T of(T x, T y) { return x > y ? x : y; }
+    template <typename T>
+    __device__ __forceinline__ static T none() { return __is_same(T, float) ? (T)-INF : (T)(__is_same(T, int) ? -0x7FFFFFFF - 1 : 0); }
 };
 struct Least {
     template <typename T>
-    __device__ __forceinline__ T operator()(T x, T y) const { return x < y ? x : y; }
+    __device__ __forceinline__ static T of(T x, T y) { return x < y ? x : y; }
+    template <typename T>
+    __device__ __forceinline__ static T none() { return __is_same(T, float) ? (T)INF : __is_same(T, int) ? (T)0x7FFFFFFF : (T)~0ull; }
 };
-// sum over the threads up to and with this one
+// over the lanes up to and with this one
+template <typename F, typename T>
+__device__ __forceinline__ T wave_scan(T v) {
+    const T none = F::template none<T>();
+    v = F::of(moved<0x111, 0xF>(v, none), v);                    // from 1, 2, 4, 8 lanes below in the row of 16
+    v = F::of(moved<0x112, 0xF>(v, none), v);
+    v = F::of(moved<0x114, 0xF>(v, none), v);
+    v = F::of(moved<0x118, 0xF>(v, none), v);
+    v = F::of(moved<0x142, 0xA>(v, none), v);                    // rows 0 and 2 into 1 and 3
+    v = F::of(moved<0x143, 0xC>(v, none), v);                    // the lower half's into the upper
+    return v;
+}
 template <typename T>
-__device__ __forceinline__ T block_sums(T v, T* s) {
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const T y = __shfl_up(v, o, 64);
-        if (lane_id() >= o) v += y;
+__device__ __forceinline__ T of_lane(T v, int lane) {
+    if constexpr (sizeof(T) == 4) return __builtin_bit_cast(T, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
+    else {
+        const int2 a = __builtin_bit_cast(int2, v);
+        return __builtin_bit_cast(T, make_int2(__builtin_amdgcn_readlane(a.x, lane), __builtin_amdgcn_readlane(a.y, lane)));
     }
+}
+template <typename F, typename T>
+__device__ __forceinline__ T wave_all(T v) { return of_lane(wave_scan<F>(v), 63); }
+
+// ---- over a workgroup of NT threads. A value a wave goes through `s`, which no
+// call may use that is less than one barrier away.
+template <int NT, typename F, typename T>
+__device__ __forceinline__ T block_all(T v, void* s) {
+    v = wave_scan<F>(v);
+    if (lane_id() == 63) ((T*)s)[threadIdx.x / 64] = v;
     __syncthreads();
-    if (lane_id() == 63) s[threadIdx.x / 64] = v;
+    const int l = lane_id() & 15;
+    return of_lane(wave_scan<F>(l < NT / 64 ? ((const T*)s)[l] : F::template none<T>()), 15);
+}
+// sum over the threads up to and with this one; that of all
+template <int NT, typename T>
+__device__ __forceinline__ T block_sums(T v, T& all, void* s) {
+    v = wave_scan<Plus>(v);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    if (lane_id() == 63) ((T*)s)[wave] = v;
     __syncthreads();
-    T w = s[lane_id() & (SW - 1)];
-#pragma unroll
-    for (int o = 1; o < SW; o <<= 1) {
-        const T y = __shfl_up(w, o, SW);
-        if ((lane_id() & (SW - 1)) >= o) w += y;
-    }
-    const int wave = threadIdx.x / 64;
-    const T before = __shfl(w, max(wave - 1, 0), 64);
-    return wave ? before + v : v;
+    const int l = lane_id() & 15;
+    const T w = wave_scan<Plus>(l < NT / 64 ? ((const T*)s)[l] : (T)0);
+    all = of_lane(w, 15);
+    return wave ? of_lane(w, wave - 1) + v : v;
 }
 
 // equal parts of [low, top], the largest logits first (part: monotone in x)
+template <int N>
 struct Parts {
     float top, scale;
-    __device__ __forceinline__ Parts(float t, float low) : top(t), scale(t > low ? (float)BINS / (t - low) : 0.f) {}
-    __device__ __forceinline__ int of(float x) const { return (int)fminf((top - x) * scale, (float)(BINS - 1)); }
+    __device__ __forceinline__ Parts(float t, float low) : top(t), scale(t > low ? (float)N / (t - low) : 0.f) {}
+    __device__ __forceinline__ int of(float x) const { return (int)fminf((top - x) * scale, (float)(N - 1)); }
 };
-// the first part up to and with which the counts reach `want`, -1 if they never do; how many lie before it
-__device__ __forceinline__ int part_of_count(const uint32_t* cnt, uint32_t want, uint32_t& before, uint32_t* s, int* s_at) {
-    const uint32_t a = cnt[2 * threadIdx.x], b = cnt[2 * threadIdx.x + 1];
-    const uint32_t end = block_sums(a + b, s);
-    if (threadIdx.x == 0) s_at[0] = -1;
-    __syncthreads();
-    const uint32_t start = end - a - b;
-    if (start < want && want <= end) {
-        const bool second = start + a < want;
-        s_at[0] = 2 * threadIdx.x + second;
-        s_at[1] = (int)(second ? start + a : start);
+// The first part up to and with which the counts reach `want` (-1: they never do), and how many lie before it.
+// A barrier before the call; s: two places for block_sums, at: two for the result.
+template <int NT, int N>
+__device__ __forceinline__ int part_of_count(const uint32_t* cnt, uint32_t want, uint32_t& before, void* s, int* at) {
+    constexpr int R = N / NT;
+    uint32_t c[R], own = 0, all;
+#pragma unroll
+    for (int i = 0; i < R; ++i) own += c[i] = cnt[R * threadIdx.x + i];
+    uint32_t start = block_sums<NT>(own, all, s) - own;
+    if (all < want) return -1;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        if (start < want && want <= start + c[i]) {
+            at[0] = R * threadIdx.x + i;
+            at[1] = (int)start;
+        }
+        start += c[i];
     }
     __syncthreads();
-    before = (uint32_t)s_at[1];
-    const int at = s_at[0];
-    __syncthreads();
-    return at;
+    before = (uint32_t)at[1];
+    return at[0];
 }
 
-// n <= LIST places in LDS, largest first; n rounded up to a power of two with zeros
+// n <= LIST places in LDS, largest first; n rounded up to a power of two with zeros. Barriers before and behind.
 __device__ __forceinline__ void sort_places(uint64_t* p, int n) {
     int size = 64;
     while (size < n) size <<= 1;
@@ -221,25 +268,26 @@ __device__ __forceinline__ void sort_places(uint64_t* p, int n) {
 }
 
 // ------------------------------------------------------------------ a chunk
+constexpr int CHUNK_BINS = 1024;
 struct ChunkShared {
-    uint32_t cnt[BINS];
-    double sum[SW];
-    uint64_t best[SW];
-    float f[SW];
-    uint32_t u[SW];
+    uint32_t cnt[CHUNK_BINS];
+    uint64_t s[8][16];
     int at[2];
-    int part[16][SW];
+    int part[4][16];
 };
 
-template <bool F32, int E>
-__device__ void sample_chunk(const SampleArgs& a, int r, int c, Chunk* info, uint2* list, ChunkShared& s) {
-    constexpr int NV = E / 4;
+// NT threads with E logits each; `share`: how many candidates may be written
+template <bool F32, int NT, int E>
+__device__ void sample_chunk(const SampleArgs& a, int r, int c, int share, Chunk* info, uint64_t* list, ChunkShared& s) {
+    constexpr int NV = E / 4, SW = NT / 64;
+    static_assert(NT * E == CHUNK && NV <= 4, "chunk");
     const void* row = (const uint8_t*)a.logits + (size_t)r * a.stride * (F32 ? 4 : 2);
-    const int V = a.V, c0 = c * ST * E, t = threadIdx.x, wave = t / 64;
-    const Request q(a, r);
+    const int V = a.V, c0 = c * CHUNK, t = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(t / 64);
     float x[NV][4];
 #pragma unroll
-    for (int j = 0; j < NV; ++j) load_logits<F32>(row, c0 + (j * ST + t) * 4, V, x[j]);
+    for (int j = 0; j < NV; ++j) load_logits<F32>(row, c0 + (j * NT + t) * 4, V, x[j]);
+    const Request q(a, r);
+    for (int i = t; i < CHUNK_BINS; i += NT) s.cnt[i] = 0;
     float top = -INF, low = INF;
 #pragma unroll
     for (int j = 0; j < NV; ++j)
@@ -249,9 +297,18 @@ __device__ void sample_chunk(const SampleArgs& a, int r, int c, Chunk* info, uin
             top = fmaxf(top, y);
             if (y > -INF) low = fminf(low, y);
         }
-    const float own = top;                                       // the thread's largest
-    top = block_reduce(top, Most(), s.f);
-    Chunk out{0.0, top, 0.f, 0, 0};
+    {
+        const float wt = wave_scan<Most>(top), wl = wave_scan<Least>(low);
+        if (lane_id() == 63) {
+            ((float*)s.s[0])[wave] = wt;
+            ((float*)s.s[1])[wave] = wl;
+        }
+        __syncthreads();
+        const int l = lane_id() & 15;
+        top = of_lane(wave_scan<Most>(l < SW ? ((const float*)s.s[0])[l] : -INF), 15);
+        low = of_lane(wave_scan<Least>(l < SW ? ((const float*)s.s[1])[l] : INF), 15);
+    }
+    Chunk out{0.0, top, low, -INF, 0};
     if (q.bad || !(top < INF) || top == -INF) {
         if (t == 0) *info = out;
         return;
@@ -261,16 +318,15 @@ __device__ void sample_chunk(const SampleArgs& a, int r, int c, Chunk* info, uin
 #pragma unroll
         for (int j = 0; j < NV; ++j)
 #pragma unroll
-            for (int v = 0; v < 4; ++v) best = Most()(best, place_of(x[j][v], c0 + (j * ST + t) * 4 + v));
-        best = block_reduce(best, Most(), s.best);
+            for (int v = 0; v < 4; ++v) best = Most::of(best, place_of(x[j][v], c0 + (j * NT + t) * 4 + v));
+        best = block_all<NT, Most>(best, s.s[2]);
         if (t == 0) {
-            list[0] = make_uint2((uint32_t)best, (uint32_t)(best >> 32));
+            list[0] = best;
             out.n = 1;
             *info = out;
         }
         return;
     }
-    out.low = low = block_reduce(low, Least(), s.f);
     // the chunk's weight, where the row's is needed (with top_k its candidates have it; min_p alone: likewise)
     if (q.k == 0 && (q.p_on || !q.m_on)) {
         double sum = 0.0;
@@ -278,86 +334,85 @@ __device__ void sample_chunk(const SampleArgs& a, int r, int c, Chunk* info, uin
         for (int j = 0; j < NV; ++j)
 #pragma unroll
             for (int v = 0; v < 4; ++v) sum += x[j][v] == -INF ? 0.0 : exp_neg(((double)x[j][v] - (double)top) * q.inv);
-        out.sum = block_reduce(sum, Plus(), s.sum);
+        out.sum = block_all<NT, Plus>(sum, s.s[2]);
     }
     if (q.k == 0 && !q.p_on && !q.m_on) {
         if (t == 0) *info = out;
         return;
     }
-    float floor = -INF;
-    if (!(q.k && q.p_on)) {
-        if (q.m_on) floor = q.least(top, q.min_p);
-        if (q.p_on) floor = fmaxf(floor, q.least(top, (1.0 - q.top_p) * out.sum / V));
-    }
-    bool in[NV][4];
-    int n = 0;
+    const float floor = fmaxf(q.floor(top, out.sum, V), low);
+    // Candidates: from `least` on. More than the share, or than a few times k:
+    // those of the parts up to the k-th (what is left out then is out), or of as
+    // many parts as fit the share.
+    auto count = [&](auto f) __attribute__((always_inline)) {
+        int n = 0;
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
+        for (int j = 0; j < NV; ++j)
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-            in[j][v] = x[j][v] > -INF && x[j][v] >= floor;
-            n += in[j][v];
-        }
-    if (q.k) {
-        // more of them than a few times k: those of the parts up to the k-th. (1024
-        // threads' largest bound the first 1024 tokens from below.)
-        const int all = block_reduce(n, Plus(), (int*)s.u);
-        if (all > 2 * q.k + 64) {
-            const float least = block_reduce(own, Least(), s.f);
-            const Parts part(top, fmaxf(floor, q.k <= ST && least > -INF ? least : low));
-            for (int i = t; i < BINS; i += ST) s.cnt[i] = 0;
-            __syncthreads();
+            for (int v = 0; v < 4; ++v) n += f(x[j][v]);
+        return n;
+    };
+    const int all = block_all<NT, Plus>(count([&](float y) { return y >= floor; }), s.s[3]);
+    const Parts<CHUNK_BINS> part(top, floor);
+    int last = CHUNK_BINS;
+    if (all > share || (q.k && all > 2 * q.k + 64)) {
 #pragma unroll
-            for (int j = 0; j < NV; ++j)
+        for (int j = 0; j < NV; ++j)
 #pragma unroll
-                for (int v = 0; v < 4; ++v)
-                    if (in[j][v] && (q.k > ST || x[j][v] >= least)) atomicAdd(&s.cnt[part.of(x[j][v])], 1u);
-            __syncthreads();
-            uint32_t before;
-            const int last = part_of_count(s.cnt, (uint32_t)q.k, before, s.u, s.at);
-            if (last >= 0) {
+            for (int v = 0; v < 4; ++v)
+                if (x[j][v] >= floor) atomicAdd(&s.cnt[part.of(x[j][v])], 1u);
+        __syncthreads();
+        uint32_t before;
+        const int want = q.k ? min(q.k, share) : share;
+        last = part_of_count<NT, CHUNK_BINS>(s.cnt, (uint32_t)want, before, s.s[4], s.at);
+        if (last < 0) last = CHUNK_BINS;
+        else {
+            const bool fits = (int)(before + s.cnt[last]) <= share;
+            if (!fits) --last;
+            if (!fits || !q.k || q.k > share) {
+                float cut = -INF;
 #pragma unroll
                 for (int j = 0; j < NV; ++j)
 #pragma unroll
-                    for (int v = 0; v < 4; ++v) in[j][v] = in[j][v] && (q.k > ST || x[j][v] >= least) && part.of(x[j][v]) <= last;
+                    for (int v = 0; v < 4; ++v)
+                        if (x[j][v] >= floor && part.of(x[j][v]) > last) cut = fmaxf(cut, x[j][v]);
+                out.cut = block_all<NT, Most>(cut, s.s[5]);
             }
         }
     }
-    // candidates in the order of their ids: [vector][wave][lane][element]
+    // in the order of their ids: [vector][wave][lane][element]
+    auto in = [&](float y) { return y >= floor && part.of(y) <= last; };
     int at[NV];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-        int before = 0, count = 0;
+        int before = 0, n = 0;
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
-            const uint64_t b = __ballot(in[j][v]);
+            const uint64_t b = __ballot(in(x[j][v]));
             before += __popcll(b & lanemask_lt());
-            count += __popcll(b);
+            n += __popcll(b);
         }
         at[j] = before;
-        if (lane_id() == 0) s.part[j][wave] = count;
+        if (lane_id() == 0) s.part[j][wave] = n;
     }
     __syncthreads();
-    int total = 0, start[NV];
+    int total = 0;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
 #pragma unroll
         for (int w = 0; w < SW; ++w) {
-            if (w == wave) start[j] = total;
+            if (w == wave) at[j] += total;
             total += s.part[j][w];
         }
     }
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-        int to = start[j] + at[j];
+        int to = at[j];
 #pragma unroll
         for (int v = 0; v < 4; ++v)
-            if (in[j][v]) {
-                if (to < CAP) list[to] = make_uint2(~(uint32_t)(c0 + (j * ST + t) * 4 + v), logit_key(x[j][v]));
-                ++to;
-            }
+            if (in(x[j][v])) list[to++] = place_of(x[j][v], c0 + (j * NT + t) * 4 + v);
     }
-    out.n = min(total, CAP + 1);
+    out.n = total;
     if (t == 0) *info = out;
 }
 
@@ -368,48 +423,41 @@ struct RowShared {
     uint32_t cnt[BINS];
     uint64_t mass[BINS];
     double ends[MAX_CHUNKS];  // weight up to and with a chunk
-    int first[MAX_CHUNKS + 1];
-    double sum[SW];
-    uint64_t best[SW];
-    float f[SW];
-    uint32_t u[SW];
-    int at[2];
+    uint64_t s[16][16];
+    double got[2];
+    uint64_t border[2];
+    int at[2], hit[2];
     int n;
-    double d;
 };
 
 // The lowest id in [lo, hi) (lo a multiple of four) up to and with which the
 // weights exceed `aim` (past their sum: the last id with a weight), -1 if there
-// is no weight. aim(sum) gives it. Returned in s.at[0], the sum in s.d and the
-// id's weight in s.sum[0], to all threads.
+// is no weight. aim(sum) gives it. The id is left in s.hit[0], the sum in
+// s.got[1] and the id's weight in s.got[0].
 template <bool F32, typename W, typename A>
 __device__ void draw(const void* row, int lo, int hi, W weight, A aim, RowShared& s) {
-    double* sums = (double*)s.sorted;                            // of 256 ids each, LIST of them
-    const int t = threadIdx.x, lane = lane_id(), wave = t / 64;
+    double* sums = (double*)s.sorted;                            // of 256 ids each, LIST of them at most
+    const int t = threadIdx.x, lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(t / 64);
     const int groups = (hi - lo + 255) / 256;
     __syncthreads();
-    for (int g = wave; g < groups; g += SW) {
+    for (int g = wave; g < groups; g += ST / 64) {
         float x[4];
         const int id = lo + g * 256 + lane * 4;
         load_logits<F32>(row, id, hi, x);
         double w = 0.0;
 #pragma unroll
         for (int v = 0; v < 4; ++v) w += weight(x[v], id + v);
-#pragma unroll
-        for (int o = 32; o > 0; o >>= 1) w += __shfl_xor(w, o, 64);
-        if (lane == 0) sums[g] = w;
+        w = wave_scan<Plus>(w);
+        if (lane == 63) sums[g] = w;
     }
+    if (t == 0) s.hit[0] = s.hit[1] = -1;
     __syncthreads();
     // a run of groups for each thread
     const int run = (groups + ST - 1) / ST, g0 = min(t * run, groups), g1 = min(g0 + run, groups);
-    double own = 0.0;
+    double own = 0.0, total;
     for (int g = g0; g < g1; ++g) own += sums[g];
-    const double end = block_sums(own, s.sum);
-    __syncthreads();
-    if (t == ST - 1) s.d = end;
-    if (t == 0) s.at[0] = s.at[1] = -1;
-    __syncthreads();
-    const double total = s.d, want = aim(total);
+    const double end = block_sums<ST>(own, total, s.s[0]);
+    const double want = aim(total);
     // the group: the first one whose end exceeds the aim, else the last one with a weight
     {
         double e = end - own;
@@ -417,37 +465,31 @@ __device__ void draw(const void* row, int lo, int hi, W weight, A aim, RowShared
             const double before = e;
             e += sums[g];
             if (sums[g] > 0.0) {
-                atomicMax(&s.at[1], g);
-                if (e > want && before <= want) atomicMax(&s.at[0], g);
+                atomicMax(&s.hit[1], g);
+                if (e > want && before <= want) atomicMax(&s.hit[0], g);
             }
         }
     }
     __syncthreads();
-    const int found = s.at[0], last = s.at[1], g = found >= 0 ? found : last;
+    const int found = s.hit[0], last = s.hit[1], g = found >= 0 ? found : last;
     if (g >= g0 && g < g1) {
         double e = end - own;
         for (int i = g0; i < g; ++i) e += sums[i];
-        s.sum[1] = e;
+        s.got[0] = e;
     }
+    if (t == 0) s.got[1] = total;
     __syncthreads();
-    const double start = s.sum[1];
-    __syncthreads();
-    if (g < 0) return;                                           // (s.at[0] is -1)
+    if (g < 0) return;                                           // (s.hit[0] is -1)
     if (wave == 0) {
+        const double start = s.got[0];
         float x[4];
         const int id = lo + g * 256 + lane * 4;
         load_logits<F32>(row, id, hi, x);
         double w[4], sum = 0.0;
 #pragma unroll
         for (int v = 0; v < 4; ++v) sum += w[v] = weight(x[v], id + v);
-        double e = sum;
-#pragma unroll
-        for (int o = 1; o < 64; o <<= 1) {
-            const double y = __shfl_up(e, o, 64);
-            if (lane >= o) e += y;
-        }
-        e = start + (e - sum);
-        int at = 0x7FFFFFFF, any = -1;
+        double e = start + (wave_scan<Plus>(sum) - sum);
+        int at = -1, any = -1;
         double wa = 0.0, wy = 0.0;
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
@@ -455,26 +497,37 @@ __device__ void draw(const void* row, int lo, int hi, W weight, A aim, RowShared
             if (w[v] > 0.0) {
                 any = id + v;
                 wy = w[v];
-                if (e > want && at == 0x7FFFFFFF) {
+                if (e > want && at < 0) {
                     at = id + v;
                     wa = w[v];
                 }
             }
         }
-        const uint64_t hit = __ballot(at != 0x7FFFFFFF), some = __ballot(any >= 0);
+        const uint64_t hit = __ballot(at >= 0), some = __ballot(any >= 0);
         const int from = hit ? __ffsll((long long)hit) - 1 : 63 - __clzll((long long)some);
         if (lane == from) {
-            s.at[0] = hit ? at : any;
-            s.sum[0] = hit ? wa : wy;
+            s.hit[0] = hit ? at : any;
+            s.got[0] = hit ? wa : wy;
         }
     }
     __syncthreads();
 }
 
 template <bool F32>
-__device__ void sample_finish(const SampleArgs& a, int r, int chunks, int chunk_size, const Chunk* info, const uint2* lists, RowShared& s) {
+__device__ void sample_finish(const SampleArgs& a, int r, int chunks, int share, const Chunk* info, const uint64_t* lists, RowShared& s) {
     const void* row = (const uint8_t*)a.logits + (size_t)r * a.stride * (F32 ? 4 : 2);
-    const int V = a.V, t = threadIdx.x;
+    const int V = a.V, t = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(t / 64);
+    // four candidates of a chunk for each thread (memory behind the last one is the lists' own)
+    const int c4 = min(4 * t / share, chunks - 1), i4 = 4 * t - c4 * share;
+    uint64_t e[4];
+    int n4 = 0;
+    if (4 * t < chunks * share) {
+        n4 = info[c4].n;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) e[i] = lists[(size_t)c4 * share + i4 + i];
+    }
+    Chunk mine{0.0, -INF, INF, -INF, 0};
+    if (t < chunks) mine = info[t];
     const Request q(a, r);
     const double u = a.u[r];
     auto give = [&](int id, double p) {
@@ -484,184 +537,154 @@ __device__ void sample_finish(const SampleArgs& a, int r, int chunks, int chunk_
             if (id < 0 && a.err) atomicAdd(a.err, 1);
         }
     };
-    Chunk mine{0.0, -INF, INF, 0, 0};
-    if (t < chunks) mine = info[t];
-    const float top = block_reduce(mine.top, Most(), s.f);
+    for (int i = t; i < BINS; i += ST) s.cnt[i] = 0;
+    float top, low, cut;
+    {
+        const float wt = wave_scan<Most>(mine.top), wl = wave_scan<Least>(mine.low), wc = wave_scan<Most>(mine.cut);
+        if (lane_id() == 63) {
+            ((float*)s.s[1])[wave] = wt;
+            ((float*)s.s[2])[wave] = wl;
+            ((float*)s.s[3])[wave] = wc;
+        }
+        __syncthreads();
+        const int l = lane_id() & 15;
+        top = of_lane(wave_scan<Most>(((const float*)s.s[1])[l]), 15);
+        low = of_lane(wave_scan<Least>(((const float*)s.s[2])[l]), 15);
+        cut = of_lane(wave_scan<Most>(((const float*)s.s[3])[l]), 15);
+    }
     if (q.bad || !(top < INF) || top == -INF) return give(-1, 0.0);
-    if (mine.top == -INF) mine.low = INF;                        // (a chunk without a token)
-    const int n_all = block_reduce(mine.n, Plus(), (int*)s.u);
-    const bool over = block_reduce(mine.n, Most(), (int*)s.u) > CAP;
     const double zmax = top;
     auto weight = [&](float x) { return x == -INF ? 0.0 : exp_neg(((double)x - zmax) * q.inv); };
 
     if (q.k == 1) {
         uint64_t best = 0;
-        if (t < chunks && mine.n) {
-            const uint2 e = lists[(size_t)t * CAP];
-            best = (uint64_t)e.y << 32 | e.x;
-        }
-        best = block_reduce(best, Most(), s.best);
-        return give(place_id(best), 1.0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i4 + i < n4) best = Most::of(best, e[i]);
+        return give(place_id(block_all<ST, Most>(best, s.s[4])), 1.0);
     }
     // the row's weight from the chunks'
+    double all;
     const double part = t < chunks && mine.sum > 0.0 ? mine.sum * exp_neg(((double)mine.top - zmax) * q.inv) : 0.0;
-    const double end = block_sums(part, s.sum);
-    __syncthreads();
-    if (t < chunks) s.ends[t] = end;
-    if (t == ST - 1) s.d = end;
-    __syncthreads();
-    const double all = s.d;
+    const double end = block_sums<ST>(part, all, s.s[5]);
     if (q.k == 0 && !q.p_on && !q.m_on) {
         // no filter: the chunk that the aim falls into (past the sum: the last with a weight)
-        const double aim = u * all;
+        if (t < chunks) s.ends[t] = end;
         if (t == 0) s.at[0] = s.at[1] = -1;
         __syncthreads();
-        if (t < chunks && part > 0.0) {
+        const double aim = u * all;
+        if (part > 0.0) {
             atomicMax(&s.at[1], t);
             if (s.ends[t] > aim && (t == 0 || s.ends[t - 1] <= aim)) atomicMax(&s.at[0], t);
         }
         __syncthreads();
         const int c = s.at[0] >= 0 ? s.at[0] : s.at[1];
         const double before = c ? s.ends[c - 1] : 0.0;
-        draw<F32>(row, c * chunk_size, min((c + 1) * chunk_size, V), [&](float x, int) { return weight(x); },
+        draw<F32>(row, c * CHUNK, min((c + 1) * CHUNK, V), [&](float x, int) { return weight(x); },
                   [&](double) { return aim - before; }, s);
-        return give(s.at[0], s.sum[0] / all);
+        return give(s.hit[0], s.got[0] / all);
     }
 
     // ---- few candidates
-    // where candidate i of the row lies: chunk c with first[c] <= i < first[c + 1]
-    bool listed = !over;
-    int n = 0;
-    if (listed) {
-        const int fe = block_sums(mine.n, (int*)s.u);
-        if (t < chunks) s.first[t + 1] = fe;
-        if (t == 0) s.first[0] = 0;
-        __syncthreads();
-        auto candidate = [&](int i) {
-            int lo = 0, hi = chunks;
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) / 2;
-                if (s.first[mid] <= i) lo = mid;
-                else hi = mid;
-            }
-            const uint2 e = lists[(size_t)lo * CAP + i - s.first[lo]];
-            return (uint64_t)e.y << 32 | e.x;
-        };
-        float floor = -INF;
-        if (!(q.k && q.p_on)) {
-            if (q.m_on) floor = q.least(top, q.min_p);
-            if (q.p_on) floor = fmaxf(floor, q.least(top, (1.0 - q.top_p) * all / V));
-        }
-        // top_k of several chunks' firsts: the parts up to the k-th
-        int last = BINS;
-        float low = INF;
-        for (int i = t; i < n_all; i += ST) low = fminf(low, place_logit(candidate(i)));
-        const Parts cut(top, block_reduce(low, Least(), s.f));
-        if (q.k && n_all > 2 * q.k + 64) {
-            for (int i = t; i < BINS; i += ST) s.cnt[i] = 0;
-            __syncthreads();
-            for (int i = t; i < n_all; i += ST) {
-                const float x = place_logit(candidate(i));
-                if (x >= floor) atomicAdd(&s.cnt[cut.of(x)], 1u);
-            }
+    const float least = q.floor(top, all, V), floor = fmaxf(least, low);
+    const Parts<BINS> parts(top, floor);
+    uint64_t border = 0;                                         // the last kept place (before min_p)
+    {
+        bool in[4];
+        int own = 0, n;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) own += in[i] = i4 + i < n4 && place_logit(e[i]) >= floor;
+        int to = block_sums<ST>(own, n, s.s[6]);
+        if (q.k && n > 2 * q.k + 64) {                           // those of the parts up to the k-th
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (in[i]) atomicAdd(&s.cnt[parts.of(place_logit(e[i]))], 1u);
             __syncthreads();
             uint32_t before;
-            last = part_of_count(s.cnt, (uint32_t)q.k, before, s.u, s.at);
-            if (last < 0) last = BINS;
-        }
-        for (int i0 = 0; i0 < n_all; i0 += ST) {                 // in the order of the ids
-            uint64_t e = 0;
-            bool in = false;
-            if (i0 + t < n_all) {
-                e = candidate(i0 + t);
-                const float x = place_logit(e);
-                in = x >= floor && cut.of(x) <= last;
-            }
-            const int to = block_sums((int)in, (int*)s.u);
-            if (in && n + to <= LIST) s.list[n + to - 1] = e;
-            if (t == ST - 1) s.n = to;
-            __syncthreads();
-            n += s.n;
-        }
-        listed = n <= LIST;
-    }
-    uint64_t border = 0;                                         // the last kept place (before min_p)
-    if (listed) {
-        __syncthreads();
-        for (int i = t; i < n; i += ST) s.sorted[i] = s.list[i];
-        __syncthreads();
-        sort_places(s.sorted, n);
-        int keep = q.k ? min(n, q.k) : n;
-        // a run of the order for each thread
-        constexpr int RUN = LIST / ST;
-        if (q.p_on) {
-            const int run = (n + ST - 1) / ST, i0 = min(t * run, keep), i1 = min(i0 + run, keep);
-            double w[RUN], own = 0.0;
+            const int last = part_of_count<ST, BINS>(s.cnt, (uint32_t)q.k, before, s.s[7], s.at);
+            own = 0;
 #pragma unroll
-            for (int i = 0; i < RUN; ++i) {
-                w[i] = i0 + i < i1 ? weight(place_logit(s.sorted[i0 + i])) : 0.0;
-                own += w[i];
+            for (int i = 0; i < 4; ++i) own += in[i] = in[i] && parts.of(place_logit(e[i])) <= last;
+            to = block_sums<ST>(own, n, s.s[8]);
+        }
+        to -= own;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (in[i]) {
+                s.list[to] = e[i];
+                s.sorted[to++] = e[i];
             }
-            const double e = block_sums(own, s.sum);
-            __syncthreads();
-            if (t == ST - 1) s.d = e;
-            __syncthreads();
-            const double want = q.top_p * (q.k ? s.d : all);
-            double before = e - own;
+        __syncthreads();
+        if (n) sort_places(s.sorted, n);
+        // a run of four of the order for each thread
+        int keep = q.k ? min(n, q.k) : n;
+        bool sure = !(cut >= least);                             // nothing that counts was left out
+        if (q.k && !sure) sure = n >= q.k && place_logit(s.sorted[q.k - 1]) > cut;
+        const bool reach = sure;
+        if (q.p_on && n) {
+            double w[4], sum = 0.0, total;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                w[i] = 4 * t + i < keep ? weight(place_logit(s.sorted[4 * t + i])) : 0.0;
+                sum += w[i];
+            }
+            double before = block_sums<ST>(sum, total, s.s[9]) - sum;
+            const double want = q.top_p * (q.k ? total : all);
             int m = 0;
 #pragma unroll
-            for (int i = 0; i < RUN; ++i) {
-                if (i0 + i < i1 && (before < want || i0 + i == 0)) m = i0 + i + 1;
+            for (int i = 0; i < 4; ++i) {
+                if (4 * t + i < keep && (before < want || 4 * t + i == 0)) m = 4 * t + i + 1;
                 before += w[i];
             }
-            keep = block_reduce(m, Most(), (int*)s.u);
+            m = block_all<ST, Most>(m, s.s[10]);
+            // (k off, candidates left out: the border has to lie among those that are here, before all of the others)
+            if (!q.k && !reach) sure = total >= want && place_logit(s.sorted[m - 1]) > cut;
+            keep = m;
         }
-        border = s.sorted[keep - 1];
-        // the draw by id
-        const int run = (n + ST - 1) / ST, i0 = min(t * run, n), i1 = min(i0 + run, n);
-        double w[RUN], own = 0.0;
+        if (sure) {
+            border = s.sorted[keep - 1];
+            // the draw by id
+            double w[4], sum = 0.0, total;
 #pragma unroll
-        for (int i = 0; i < RUN; ++i) {
-            w[i] = 0.0;
-            if (i0 + i < i1 && s.list[i0 + i] >= border) {
-                w[i] = weight(place_logit(s.list[i0 + i]));
-                if (w[i] < q.min_p) w[i] = 0.0;
+            for (int i = 0; i < 4; ++i) {
+                w[i] = 0.0;
+                if (4 * t + i < n && s.list[4 * t + i] >= border) {
+                    w[i] = weight(place_logit(s.list[4 * t + i]));
+                    if (w[i] < q.min_p) w[i] = 0.0;
+                }
+                sum += w[i];
             }
-            own += w[i];
-        }
-        const double e = block_sums(own, s.sum);
-        __syncthreads();
-        if (t == ST - 1) s.d = e;
-        if (t == 0) s.at[0] = 0x7FFFFFFF, s.at[1] = -1;
-        __syncthreads();
-        const double total = s.d, aim = u * total;
-        double sum = e - own;
+            if (t == 0) s.hit[0] = 0x7FFFFFFF, s.hit[1] = -1;
+            double x = block_sums<ST>(sum, total, s.s[11]) - sum;
+            const double aim = u * total;
+            int first = 0x7FFFFFFF, last = -1;
 #pragma unroll
-        for (int i = 0; i < RUN; ++i) {
-            sum += w[i];
-            if (w[i] > 0.0) {
-                atomicMax(&s.at[1], i0 + i);
-                if (sum > aim) atomicMin(&s.at[0], i0 + i);
+            for (int i = 0; i < 4; ++i) {
+                x += w[i];
+                if (w[i] > 0.0) {
+                    last = 4 * t + i;
+                    if (x > aim) first = min(first, 4 * t + i);
+                }
             }
+            if (last >= 0) atomicMax(&s.hit[1], last);
+            if (first != 0x7FFFFFFF) atomicMin(&s.hit[0], first);
+            __syncthreads();
+            const uint64_t chosen = s.list[s.hit[0] != 0x7FFFFFFF ? s.hit[0] : s.hit[1]];
+            return give(place_id(chosen), weight(place_logit(chosen)) / total);
         }
-        __syncthreads();
-        const int at = s.at[0] != 0x7FFFFFFF ? s.at[0] : s.at[1];
-        const uint64_t chosen = s.list[at];
-        return give(place_id(chosen), weight(place_logit(chosen)) / total);
     }
 
     // ---- many: over the row again. Logits 2^-46 of the largest weight and less do not count.
-    const float lowest = block_reduce(mine.low, Least(), s.f);
-    const float floor = fmaxf(lowest, q.least(top, 1.0 / 70368744177664.0));
-    const Parts parts(top, floor);
     auto mass = [&](float x) { return (uint64_t)__builtin_rint(weight(x) * ONE); };
+    const float bottom = fmaxf(q.least(top, 1.0 / 70368744177664.0), low);
+    const Parts<BINS> every(top, bottom);
     auto each = [&](auto f) {
         for (int i = t * 4; i < V; i += ST * 4) {
             float x[4];
             load_logits<F32>(row, i, V, x);
 #pragma unroll
             for (int v = 0; v < 4; ++v)
-                if (x[v] >= floor) f(x[v], i + v);
+                if (x[v] >= bottom) f(x[v], i + v);
         }
     };
     if (q.k || q.p_on) {
@@ -672,7 +695,7 @@ __device__ void sample_finish(const SampleArgs& a, int r, int chunks, int chunk_
         }
         __syncthreads();
         each([&](float x, int) {
-            const int b = parts.of(x);
+            const int b = every.of(x);
             atomicAdd(&s.cnt[b], 1u);
             atomicAdd((unsigned long long*)&s.mass[b], (unsigned long long)mass(x));
         });
@@ -685,48 +708,48 @@ __device__ void sample_finish(const SampleArgs& a, int r, int chunks, int chunk_
             __syncthreads();
             if (m <= LIST) {
                 each([&](float x, int id) {
-                    if (parts.of(x) == b) s.sorted[atomicAdd(&s.n, 1)] = place_of(x, id);
+                    if (every.of(x) == b) s.sorted[atomicAdd(&s.n, 1)] = place_of(x, id);
                 });
                 __syncthreads();
                 sort_places(s.sorted, m);
-                constexpr int RUN = LIST / ST;
-                const int run = (m + ST - 1) / ST, i0 = min(t * run, m), i1 = min(i0 + run, m);
-                uint64_t w[RUN], own = 0;
+                uint64_t w[4], own = 0, all_of;
 #pragma unroll
-                for (int i = 0; i < RUN; ++i) {
-                    w[i] = i0 + i < i1 ? mass(place_logit(s.sorted[i0 + i])) : 0;
+                for (int i = 0; i < 4; ++i) {
+                    w[i] = 4 * t + i < m ? mass(place_logit(s.sorted[4 * t + i])) : 0;
                     own += w[i];
                 }
-                uint64_t before = block_sums(own, s.best) - own, in = 0;
+                uint64_t before = block_sums<ST>(own, all_of, s.s[1]) - own, in = 0;
                 int keep = 0;
 #pragma unroll
-                for (int i = 0; i < RUN; ++i) {
-                    if (i0 + i < i1 && ((by_mass ? before : (uint64_t)(i0 + i)) < want || i0 + i == 0)) {
-                        keep = i0 + i + 1;
+                for (int i = 0; i < 4; ++i) {
+                    const int at = 4 * t + i;
+                    if (at < m && ((by_mass ? before : (uint64_t)at) < want || at == 0)) {
+                        keep = at + 1;
                         in += w[i];
                     }
                     before += w[i];
                 }
-                keep = block_reduce(keep, Most(), (int*)s.u);
-                kept = block_reduce(in, Plus(), s.best);
+                keep = block_all<ST, Most>(keep, s.s[2]);
+                kept = block_all<ST, Plus>(in, s.s[3]);
                 return s.sorted[keep - 1];
             }
             // more than can be sorted: halve the range of keys until one is left
             uint32_t lo = ~0u, hi = 0;
             each([&](float x, int) {
-                if (parts.of(x) == b) {
+                if (every.of(x) == b) {
                     lo = min(lo, logit_key(x));
                     hi = max(hi, logit_key(x));
                 }
             });
-            lo = block_reduce(lo, Least(), s.u);
-            hi = block_reduce(hi, Most(), s.u);
+            lo = block_all<ST, Least>(lo, s.s[1]);
+            hi = block_all<ST, Most>(hi, s.s[2]);
             auto above = [&](uint32_t key, bool masses) {
                 uint64_t v = 0;
                 each([&](float x, int) {
-                    if (parts.of(x) == b && logit_key(x) > key) v += masses ? mass(x) : 1;
+                    if (every.of(x) == b && logit_key(x) > key) v += masses ? mass(x) : 1;
                 });
-                return block_reduce(v, Plus(), s.best);
+                __syncthreads();
+                return block_all<ST, Plus>(v, s.s[3]);
             };
             if (want == 0) want = 1;
             while (lo < hi) {                                    // the smallest key with less than `want` above it
@@ -741,123 +764,108 @@ __device__ void sample_finish(const SampleArgs& a, int r, int chunks, int chunk_
             kept = above(lo, true);
             draw<F32>(row, 0, V, [&](float x, int) { return x > -INF && logit_key(x) == key ? 1.0 : 0.0; },
                       [&](double sum) { return fmin((double)ties, sum) - 1.0; }, s);
-            kept += (uint64_t)fmin((double)ties, s.d) * mass(key_logit(key));
-            return (uint64_t)key << 32 | (uint32_t)~s.at[0];
+            kept += (uint64_t)fmin((double)ties, s.got[1]) * mass(key_logit(key));
+            return (uint64_t)key << 32 | (uint32_t)~s.hit[0];
         };
-        // masses up to and with each part
-        auto mass_end = [&](uint64_t& first) {
-            first = s.mass[2 * t];
-            return block_sums(first + s.mass[2 * t + 1], s.best);
-        };
-        uint64_t first, whole;
-        const uint64_t ends = mass_end(first);
-        __syncthreads();
-        if (t == ST - 1) s.best[0] = ends;
-        __syncthreads();
-        whole = s.best[0];
-        __syncthreads();
+        // masses of this thread's two parts, and up to and with them
+        const uint64_t first = s.mass[2 * t], second = s.mass[2 * t + 1];
+        uint64_t whole;
+        const uint64_t ends = block_sums<ST>(first + second, whole, s.s[4]);
         if (q.k) {
             uint32_t before;
-            const int b = part_of_count(s.cnt, (uint32_t)q.k, before, s.u, s.at);
+            const int b = part_of_count<ST, BINS>(s.cnt, (uint32_t)q.k, before, s.s[5], s.at);
             if (b >= 0) {
-                if (t == b / 2) s.best[0] = ends - s.mass[b] - (b & 1 ? 0 : s.mass[b + 1]);
-                __syncthreads();
-                const uint64_t over_b = s.best[0];
+                if (t == b / 2) s.border[0] = ends - (b & 1 ? second : first + second);
                 __syncthreads();
                 uint64_t kept;
                 border = border_in(b, q.k - before, false, kept);
-                whole = over_b + kept;
+                whole = s.border[0] + kept;
             }
         }
         if (q.p_on) {
             const double x = __builtin_ceil(q.top_p * (double)whole);
             const uint64_t want = x < 1.0 ? 1 : (uint64_t)x;
+            const uint64_t start = ends - first - second;
+            __syncthreads();
             if (t == 0) s.at[0] = 0;
             __syncthreads();
-            const uint64_t start = ends - first - s.mass[2 * t + 1];
             if (start < want && want <= ends) {
-                const bool second = start + first < want;
-                s.at[0] = 2 * t + second;
-                s.best[0] = second ? start + first : start;
+                const bool later = start + first < want;
+                s.at[0] = 2 * t + later;
+                s.border[1] = later ? start + first : start;
             }
             __syncthreads();
-            const int b = s.at[0];
-            const uint64_t before = s.best[0];
-            __syncthreads();
             uint64_t kept;
-            const uint64_t p = border_in(b, want - before, true, kept);
-            border = Most()(border, p);
+            const int b = s.at[0];
+            const uint64_t p = border_in(b, want - s.border[1], true, kept);
+            border = Most::of(border, p);
         }
     }
     draw<F32>(row, 0, V, [&](float x, int id) {
-                  if (!(x >= floor) || place_of(x, id) < border) return 0.0;
+                  if (!(x >= bottom) || place_of(x, id) < border) return 0.0;
                   const double w = weight(x);
                   return w >= q.min_p ? w : 0.0;
               }, [&](double sum) { return u * sum; }, s);
-    give(s.at[0], s.sum[0] / s.d);
+    give(s.hit[0], s.got[0] / s.got[1]);
 }
 
-template <bool F32, int E>
-__global__ void __launch_bounds__(ST) sample_chunk_kernel(SampleArgs a, int chunks, Chunk* info, uint2* lists) {
+constexpr int CHUNK_THREADS = 256;
+template <bool F32>
+__global__ void __launch_bounds__(CHUNK_THREADS) sample_chunk_kernel(SampleArgs a, int chunks, int share, Chunk* info, uint64_t* lists) {
     __shared__ ChunkShared s;
     const long long n = (long long)a.B * chunks;
     for (long long i = blockIdx.x; i < n; i += gridDim.x) {
-        sample_chunk<F32, E>(a, (int)(i / chunks), (int)(i % chunks), info + i, lists + i * CAP, s);
+        sample_chunk<F32, CHUNK_THREADS, CHUNK / CHUNK_THREADS>(a, (int)(i / chunks), (int)(i % chunks), share, info + i, lists + i * share, s);
         __syncthreads();
     }
 }
 template <bool F32>
-__global__ void __launch_bounds__(ST) sample_finish_kernel(SampleArgs a, int chunks, int chunk_size, const Chunk* info, const uint2* lists) {
+__global__ void __launch_bounds__(ST) sample_finish_kernel(SampleArgs a, int chunks, int share, const Chunk* info, const uint64_t* lists) {
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
     const size_t i = (size_t)blockIdx.x * chunks;
-    sample_finish<F32>(a, blockIdx.x, chunks, chunk_size, info + i, lists + i * CAP, *(RowShared*)smem);
+    sample_finish<F32>(a, blockIdx.x, chunks, share, info + i, lists + i * share, *(RowShared*)smem);
 }
 // rows of one chunk
-template <bool F32, int E>
-__global__ void __launch_bounds__(ST) sample_row_kernel(SampleArgs a, Chunk* info, uint2* lists) {
+template <bool F32>
+__global__ void __launch_bounds__(ST) sample_row_kernel(SampleArgs a, int share, Chunk* info, uint64_t* lists) {
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
     const size_t i = blockIdx.x;
-    sample_chunk<F32, E>(a, (int)i, 0, info + i, lists + i * CAP, *(ChunkShared*)smem);
+    sample_chunk<F32, ST, CHUNK / ST>(a, (int)i, 0, share, info + i, lists + i * share, *(ChunkShared*)smem);
     __syncthreads();
-    sample_finish<F32>(a, (int)i, 1, ST * E, info + i, lists + i * CAP, *(RowShared*)smem);
+    sample_finish<F32>(a, (int)i, 1, share, info + i, lists + i * share, *(RowShared*)smem);
 }
 
-// Logits of a thread of the chunk kernel: 4 where 16 would leave CUs without a chunk.
-static int chunk_elems(int B, int V) { return (long long)B * ((V + ST * 16 - 1) / (ST * 16)) >= 256 || V > ST * 4 * MAX_CHUNKS ? 16 : 4; }
-static int chunks_of(int B, int V) {
-    const int e = chunk_elems(B, V);
-    return (V + ST * e - 1) / (ST * e);
-}
+static int chunks_of(int V) { return (V + CHUNK - 1) / CHUNK; }
+static int share_of(int chunks) { return LIST / chunks / 4 * 4; }
+static size_t info_bytes(int B, int V) { return ((size_t)B * chunks_of(V) * sizeof(Chunk) + 255) / 256 * 256; }
 size_t sample_workspace_bytes(int B, int V) {
-    const size_t n = (size_t)B * chunks_of(B, V);
-    return (n * sizeof(Chunk) + 255) / 256 * 256 + n * CAP * sizeof(uint2);
+    const int chunks = chunks_of(V);
+    return info_bytes(B, V) + (size_t)B * chunks * share_of(chunks) * 8;
 }
 
 template <bool F32>
 static hipError_t launch(const SampleArgs& a, void* ws, hipStream_t stream) {
-    const int e = chunk_elems(a.B, a.V), chunks = chunks_of(a.B, a.V);
-    const size_t n = (size_t)a.B * chunks;
+    const int chunks = chunks_of(a.V), share = share_of(chunks);
     Chunk* info = (Chunk*)ws;
-    uint2* lists = (uint2*)((uint8_t*)ws + (n * sizeof(Chunk) + 255) / 256 * 256);
+    uint64_t* lists = (uint64_t*)((uint8_t*)ws + info_bytes(a.B, a.V));
     static_assert(sizeof(RowShared) <= 163840 && sizeof(ChunkShared) <= sizeof(RowShared), "LDS");
     int dev = 0;
-    hipError_t st = hipGetDevice(&dev);
-    if (st != hipSuccess) return st;
+    hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess) return e;
+    static std::atomic<uint64_t> done[2];
     if (chunks == 1) {
-        static std::atomic<uint64_t> done[2];
-        const auto kernel = e == 16 ? sample_row_kernel<F32, 16> : sample_row_kernel<F32, 4>;
-        st = allow_lds((const void*)kernel, sizeof(RowShared), dev, done[e == 16]);
-        if (st != hipSuccess) return st;
-        return launch_kernel(K_SAMPLE, stream, kernel, dim3((unsigned)a.B), dim3(ST), sizeof(RowShared), a, info, lists);
+        e = allow_lds((const void*)sample_row_kernel<F32>, sizeof(RowShared), dev, done[0]);
+        if (e != hipSuccess) return e;
+        return launch_kernel(K_SAMPLE, stream, sample_row_kernel<F32>, dim3((unsigned)a.B), dim3(ST), sizeof(RowShared), a, share, info, lists);
     }
-    const auto kernel = e == 16 ? sample_chunk_kernel<F32, 16> : sample_chunk_kernel<F32, 4>;
-    st = launch_kernel(K_SAMPLE, stream, kernel, dim3((unsigned)(n < (1u << 21) ? n : 1u << 21)), dim3(ST), 0, a, chunks, info, lists);
-    if (st != hipSuccess) return st;
-    static std::atomic<uint64_t> done{0};
-    st = allow_lds((const void*)sample_finish_kernel<F32>, sizeof(RowShared), dev, done);
-    if (st != hipSuccess) return st;
-    return launch_kernel(K_SAMPLE, stream, sample_finish_kernel<F32>, dim3((unsigned)a.B), dim3(ST), sizeof(RowShared), a, chunks, ST * e,
-                         (const Chunk*)info, (const uint2*)lists);
+    e = allow_lds((const void*)sample_finish_kernel<F32>, sizeof(RowShared), dev, done[1]);
+    if (e != hipSuccess) return e;
+    const long long n = (long long)a.B * chunks;
+    e = launch_kernel(K_SAMPLE, stream, sample_chunk_kernel<F32>, dim3((unsigned)(n < (1 << 20) ? n : 1 << 20)), dim3(CHUNK_THREADS), 0, a,
+                      chunks, share, info, lists);
+    if (e != hipSuccess) return e;
+    return launch_kernel(K_SAMPLE, stream, sample_finish_kernel<F32>, dim3((unsigned)a.B), dim3(ST), sizeof(RowShared), a, chunks, share,
+                         (const Chunk*)info, (const uint64_t*)lists);
 }
 hipError_t launch_sample(const SampleArgs& a, bool f32, void* ws, hipStream_t stream) {
     return f32 ? launch<true>(a, ws, stream) : launch<false>(a, ws, stream);

@@ -13,7 +13,9 @@ import numpy as np
 def sample_row(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
     """Returns (id, p, kept ids by order, margin): margin is how far, in parts of
     the largest weight, the nearest decision (top_p's border, min_p's border,
-    the draw) is from going the other way. (-1, 0, [], inf) without a token."""
+    the draw) is from going the other way; min_p's, which one weight decides and no
+    sum of V of them, counts 8 V times (2^-45 of it like V 2^-42 of the others).
+    (-1, 0, [], inf) without a token."""
     l = np.asarray(logits, dtype=np.float64)
     none = (-1, 0.0, np.zeros(0, dtype=np.int64), np.inf)
     if np.isnan(l).any() or np.any(l == np.inf) or not np.any(l > -np.inf):
@@ -33,7 +35,7 @@ def sample_row(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
         margin = min(margin, np.abs(before[1:] - want).min(initial=np.inf))
         n = max(1, int(np.sum(before < want)))
     if min_p > 0:
-        margin = min(margin, np.abs(w[1:n] - min_p).min(initial=np.inf))
+        margin = min(margin, np.abs(w[1:n] - min_p).min(initial=np.inf) * 8 * len(l))
         n = int(np.sum(w[:n] >= min_p))
     kept = order[:n]
     by_id = np.argsort(kept)

@@ -3,7 +3,9 @@
 Each weight is off by half of 2^-42 of the largest, and fp64's exponential by
 far less, so no sum of V weights is off by more than V 2^-43, and a decision
 (a border, the draw) by twice that: where the oracle's decisions are more than
-V 2^-42 away from going the other way, the ids are equal. p is a quotient of
+V 2^-42 away from going the other way, the ids are equal. (w >= min_p is one
+weight's decision: the exponential is off by less than 1e-14 = 2^-46.5 of it, so
+2^-45 is enough there.) p is a quotient of
 fp64 values, off by the sums' V 2^-43 (of a sum of at least 1) and one rounding
 to fp32: p (2^-24 + V 2^-42).
 """
@@ -90,6 +92,29 @@ def test_kinds_of_rows(gpu, name, B, V):
         assert np.array_equal(ids.cpu().numpy()[sure], rid[sure]), (ids, rid, margin)
         assert np.all(np.abs(p.double().cpu().numpy() - rp)[sure] <= rp[sure] * (2.0 ** -24 + V * 2.0 ** -42))
         assert sure.any() or name == "two values"
+
+
+@pytest.mark.parametrize("V", [9000, 131072])
+@pytest.mark.parametrize("bf16", [False, True])
+def test_many_kept_tokens(gpu, V, bf16):
+    """top_k of thousands, top_p of flat rows, ordered logits (one chunk has all of the firsts), soft masks: borders among more
+    tokens than are kept as candidates."""
+    import torch
+    r = np.random.default_rng([7, V])
+    B = 12
+    l = r.normal(size=(B, V)) * np.array([0.01, 0.3, 1, 3] * 3)[:, None]
+    l[4:8] = -np.sort(-l[4:8], axis=1)
+    l[8:] = np.where(r.random((4, V)) < 0.9, np.array([-1e4, -65504.0, -3e38, -30.0])[:, None], l[8:])
+    l = torch.from_numpy(l.astype(np.float32)).to(torch.bfloat16 if bf16 else torch.float32)
+    for k, pp, mp in ((2000, None, None), (5000, 0.9, None), (V - 7, 0.5, 0.001), (0, 0.99, None), (0, 0.3, None), (300, None, None), (0, None, 1e-4),
+                      (V + 5, None, None), (700, 0.999, None)):
+        u = r.random(B).astype(np.float32)
+        t = (0.2 + 2 * r.random(B)).astype(np.float32)
+        par = [t, np.full(B, k, np.int32), None if pp is None else np.full(B, pp, np.float32), None if mp is None else np.full(B, mp, np.float32)]
+        _say(f"[many] V={V} bf16={bf16} k={k} p={pp} m={mp}")
+        ids, p, _ = moe.sample(l.to(gpu), _dev(u, gpu), *(_dev(v, gpu) for v in par))
+        torch.cuda.synchronize()
+        _check(ids, p, oracle_sample(l.double().numpy(), u.astype(np.float64), *(None if v is None else v.astype(np.float64) for v in par)), V)
 
 
 def test_equal_logits_take_the_lowest_ids(gpu):
