@@ -18,12 +18,12 @@
 // of all k tokens. A chunk writes no more than its share of a row's LIST; where
 // it has more candidates, it writes the first of the order and the largest
 // logit that it left out.
-// finish kernel: one workgroup a row. Candidates are sorted in LDS, borders come
-// from prefix sums, and hold if they lie before every logit that was left out
-// (nearly always, with a filter). No filter: the chunk that the draw falls into
-// is read again. Else (a top_p that keeps thousands of tokens) the row is read
-// again: counts and weights of 2048 equal parts of the logits' range, the
-// tokens of the part that holds the border sorted, the kept weight by id.
+// finish kernel: one workgroup a row. Counts and weights of 2048 equal parts of
+// the candidates' range say which part holds a border, and its tokens, put in
+// order, where. It holds if it lies before every logit that was left out
+// (nearly always, with a filter); else (a top_p that keeps thousands of tokens)
+// the same is done with all of the row's logits, read again. No filter: the
+// chunk that the draw falls into is read again.
 //
 // Weights are fp64, sums of them fp64 in a fixed order; the parts' weights are
 // summed with atomics, and therefore as integers (multiples of 2^-42 of the
@@ -38,6 +38,7 @@ constexpr int ST = 1024;                                         // threads of a
 constexpr int CHUNK = 4096;                                      // logits of a chunk
 constexpr int MAX_CHUNKS = MOE_SAMPLE_MAX_COLS / CHUNK;
 constexpr int LIST = 4096;                                       // candidates of a row
+constexpr int RUN = LIST / ST;                                   // of a thread
 constexpr int BINS = 2048;
 constexpr double ONE = 4398046511104.0;                          // 2^42: the sum of 2^20 weights stays below 2^63
 constexpr float INF = __builtin_inff();
@@ -60,30 +61,44 @@ __device__ __forceinline__ uint64_t place_of(float x, int id) { return (uint64_t
 __device__ __forceinline__ float place_logit(uint64_t p) { return key_logit((uint32_t)(p >> 32)); }
 __device__ __forceinline__ int place_id(uint64_t p) { return (int)~(uint32_t)p; }
 
-// e^x for x <= 0: 2^n e^r with |r| <= ln 2 / 2 and Taylor's polynomial of e^r to
-// r^11 (the rest is below 7e-15); 1 for 0, 0 below 2^-1022
-__device__ __forceinline__ double exp_neg(double x) {
-    const double n = __builtin_rint(x * 1.4426950408889634074);
-    const double r = __builtin_fma(n, -0.693147180559945309417, x);
-    double y = 1.0 / 39916800.0;
-    y = __builtin_fma(y, r, 1.0 / 3628800.0);
-    y = __builtin_fma(y, r, 1.0 / 362880.0);
-    y = __builtin_fma(y, r, 1.0 / 40320.0);
-    y = __builtin_fma(y, r, 1.0 / 5040.0);
-    y = __builtin_fma(y, r, 1.0 / 720.0);
-    y = __builtin_fma(y, r, 1.0 / 120.0);
-    y = __builtin_fma(y, r, 1.0 / 24.0);
-    y = __builtin_fma(y, r, 1.0 / 6.0);
-    y = __builtin_fma(y, r, 0.5);
-    y = __builtin_fma(y, r, 1.0);
-    y = __builtin_fma(y, r, 1.0);
-    const int e = n < -1022.0 ? 0 : (int)n + 1023;
-    return e ? y * __longlong_as_double((long long)e << 52) : 0.0;
+// 2^(i / 32)
+__device__ const double g_two[32] = {
+    1.0, 1.0218971486541166, 1.0442737824274138, 1.0671404006768237,
+    1.0905077326652577, 1.1143867425958924, 1.1387886347566916, 1.1637248587775775,
+    1.189207115002721, 1.215247359980469, 1.241857812073484, 1.2690509571917332,
+    1.2968395546510096, 1.3252366431597413, 1.3542555469368927, 1.383909881963832,
+    1.4142135623730951, 1.4451808069770467, 1.4768261459394993, 1.5091644275934228,
+    1.5422108254079407, 1.5759808451078865, 1.6104903319492543, 1.645755478153965,
+    1.681792830507429, 1.718619298122478, 1.7562521603732995, 1.7947090750031072,
+    1.8340080864093424, 1.8741676341103, 1.9152065613971474, 1.9571441241754002};
+// e^(d inv) for d <= 0, scale = 32 inv / ln 2: 2^(n / 32) e^r with |r| <= ln 2 / 64
+// and Taylor's polynomial of e^r to r^5 (the rest is below 3e-15); 1 for 0, 0
+// far below 2^-1022. `two`: the table in LDS (32 entries, 64 banks), where it saves
+// six of the eleven steps that a whole power of two would leave to the polynomial.
+__device__ __forceinline__ double exp_neg(double d, double scale, const double* two) {
+    const double y = d * scale, n = __builtin_rint(y);
+    const double r = (y - n) * 0.0216608493924982909;            // ln 2 / 32
+    double f = 1.0 / 120.0;
+    f = __builtin_fma(f, r, 1.0 / 24.0);
+    f = __builtin_fma(f, r, 1.0 / 6.0);
+    f = __builtin_fma(f, r, 0.5);
+    f = __builtin_fma(f, r, 1.0);
+    f = __builtin_fma(f, r, 1.0);
+    const int e = (int)fmax(n, -40000.0);
+    return __builtin_ldexp(f * two[e & 31], e >> 5);
+}
+
+// e^((x - top) inv), 0 for -inf. (Without a branch: in one for each element the
+// chains of a thread's elements wait for themselves; 16 of them 5600 -> 3100 clocks.)
+__device__ __forceinline__ double weight_of(float x, double top, double scale, const double* two) {
+    const bool none = x == -INF;
+    const double w = exp_neg(none ? 0.0 : (double)x - top, scale, two);
+    return none ? 0.0 : w;
 }
 
 // a row's parameters
 struct Request {
-    double inv, top_p, min_p;  // 1 / temperature (0 for infinity)
+    double scale, top_p, min_p;// 32 / (ln 2 temperature), 0 for infinity
     float temperature;
     int k;                     // 0: off
     bool bad, p_on, m_on;
@@ -91,7 +106,7 @@ struct Request {
         temperature = a.temperature ? a.temperature[r] : 1.f;
         const float u = a.u[r], tp = a.top_p ? a.top_p[r] : 1.f, mp = a.min_p ? a.min_p[r] : 0.f;
         bad = !(u >= 0.f && u <= 1.f) || !(temperature >= 0.f) || tp != tp || !(mp <= 1.f);
-        inv = temperature > 0.f ? 1.0 / (double)temperature : 0.0;
+        scale = temperature > 0.f ? 46.16624130844682903552 / (double)temperature : 0.0;
         k = temperature == 0.f ? 1 : a.top_k ? max(a.top_k[r], 0) : 0;
         top_p = tp > 0.f ? tp : 0.f;
         min_p = mp > 0.f ? mp : 0.f;
@@ -118,27 +133,39 @@ struct Request {
     }
 };
 
-// N consecutive logits from element i on, -inf past the row's end
-template <bool F32, int N>
-__device__ __forceinline__ void load_logits(const void* row, int i, int V, float (&x)[N]) {
-    typedef uint32_t w4 __attribute__((ext_vector_type(N)));
-    typedef uint32_t w2 __attribute__((ext_vector_type(N / 2)));
+// four consecutive logits from element i on, which the row has
+template <bool F32>
+__device__ __forceinline__ void load_four(const void* row, int i, float (&x)[4]) {
+    typedef uint32_t w4 __attribute__((ext_vector_type(4)));
+    typedef uint32_t w2 __attribute__((ext_vector_type(2)));
     typedef w4 place4 __attribute__((aligned(4)));
     typedef w2 place2 __attribute__((aligned(2)));
-    if (i + N <= V) {
-        if (F32) {
-            const w4 v = *(const place4*)((const float*)row + i);
+    if (F32) {
+        const w4 v = *(const place4*)((const float*)row + i);
 #pragma unroll
-            for (int j = 0; j < N; ++j) x[j] = __uint_as_float(v[j]);
-        } else {
-            const w2 v = *(const place2*)((const uint16_t*)row + i);
+        for (int j = 0; j < 4; ++j) x[j] = __uint_as_float(v[j]);
+    } else {
+        const w2 v = *(const place2*)((const uint16_t*)row + i);
 #pragma unroll
-            for (int j = 0; j < N; ++j) x[j] = __uint_as_float(j & 1 ? v[j / 2] & 0xFFFF0000u : v[j / 2] << 16);
-        }
+        for (int j = 0; j < 4; ++j) x[j] = __uint_as_float(j & 1 ? v[j / 2] & 0xFFFF0000u : v[j / 2] << 16);
+    }
+}
+// N fours, `step` elements apart, -inf from element V on. Where all of `all`
+// elements from `base` on are there (the same for a wave), the loads go out
+// together, without a branch for each.
+template <bool F32, int N>
+__device__ __forceinline__ void load_fours(const void* row, int i, int step, int base, int all, int V, float (&x)[N][4]) {
+    if (base + all <= V) {
+#pragma unroll
+        for (int n = 0; n < N; ++n) load_four<F32>(row, i + n * step, x[n]);
     } else {
 #pragma unroll
-        for (int j = 0; j < N; ++j)
-            x[j] = i + j < V ? (F32 ? ((const float*)row)[i + j] : bf16_to_f32(((const uint16_t*)row)[i + j])) : -INF;
+        for (int n = 0; n < N; ++n)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int e = i + n * step + j;
+                x[n][j] = e < V ? (F32 ? ((const float*)row)[e] : bf16_to_f32(((const uint16_t*)row)[e])) : -INF;
+            }
     }
 }
 
@@ -270,6 +297,7 @@ __device__ __forceinline__ void sort_places(uint64_t* p, int n) {
 // ------------------------------------------------------------------ a chunk
 constexpr int CHUNK_BINS = 1024;
 struct ChunkShared {
+    double two[32];
     uint32_t cnt[CHUNK_BINS];
     uint64_t s[8][16];
     int at[2];
@@ -278,16 +306,16 @@ struct ChunkShared {
 
 // NT threads with E logits each; `share`: how many candidates may be written
 template <bool F32, int NT, int E>
-__device__ void sample_chunk(const SampleArgs& a, int r, int c, int share, Chunk* info, uint64_t* list, ChunkShared& s) {
+__device__ __forceinline__ void sample_chunk(const SampleArgs& a, int r, int c, int share, Chunk* info, uint64_t* list, ChunkShared& s) {
     constexpr int NV = E / 4, SW = NT / 64;
     static_assert(NT * E == CHUNK && NV <= 4, "chunk");
     const void* row = (const uint8_t*)a.logits + (size_t)r * a.stride * (F32 ? 4 : 2);
     const int V = a.V, c0 = c * CHUNK, t = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(t / 64);
     float x[NV][4];
-#pragma unroll
-    for (int j = 0; j < NV; ++j) load_logits<F32>(row, c0 + (j * NT + t) * 4, V, x[j]);
+    load_fours<F32>(row, c0 + 4 * t, 4 * NT, c0, CHUNK, V, x);
     const Request q(a, r);
     for (int i = t; i < CHUNK_BINS; i += NT) s.cnt[i] = 0;
+    if (t < 32) s.two[t] = g_two[t];
     float top = -INF, low = INF;
 #pragma unroll
     for (int j = 0; j < NV; ++j)
@@ -332,8 +360,9 @@ __device__ void sample_chunk(const SampleArgs& a, int r, int c, int share, Chunk
         double sum = 0.0;
 #pragma unroll
         for (int j = 0; j < NV; ++j)
+            if (__ballot(x[j][0] > -INF || x[j][1] > -INF || x[j][2] > -INF || x[j][3] > -INF))
 #pragma unroll
-            for (int v = 0; v < 4; ++v) sum += x[j][v] == -INF ? 0.0 : exp_neg(((double)x[j][v] - (double)top) * q.inv);
+            for (int v = 0; v < 4; ++v) sum += weight_of(x[j][v], top, q.scale, s.two);
         out.sum = block_all<NT, Plus>(sum, s.s[2]);
     }
     if (q.k == 0 && !q.p_on && !q.m_on) {
@@ -381,7 +410,7 @@ __device__ void sample_chunk(const SampleArgs& a, int r, int c, int share, Chunk
         }
     }
     // in the order of their ids: [vector][wave][lane][element]
-    auto in = [&](float y) { return y >= floor && part.of(y) <= last; };
+    auto in = [&](float y) __attribute__((always_inline)) { return y >= floor && part.of(y) <= last; };
     int at[NV];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -418,39 +447,61 @@ __device__ void sample_chunk(const SampleArgs& a, int r, int c, int share, Chunk
 
 // ------------------------------------------------------------------ a row
 struct RowShared {
+    double two[32];
     uint64_t list[LIST];      // candidates by id
-    uint64_t sorted[LIST];    // ... by place; wave sums of a draw
+    uint64_t sorted[LIST];    // a part's tokens; the groups' sums of a draw
     uint32_t cnt[BINS];
     uint64_t mass[BINS];
-    double ends[MAX_CHUNKS];  // weight up to and with a chunk
     uint64_t s[16][16];
     double got[2];
-    uint64_t border[2];
-    int at[2], hit[2];
+    uint64_t before[2];
+    int at[2], hit[1], part[16];
     int n;
 };
+
+// the least `first` of the workgroup's threads, if there is none (0x7FFFFFFF) the largest `last`
+__device__ __forceinline__ int choose(int first, int last, RowShared& s) {
+    first = wave_all<Least>(first);
+    last = wave_all<Most>(last);
+    const int wave = threadIdx.x / 64;
+    if (lane_id() == 0) {
+        ((int*)s.s[8])[wave] = first;
+        ((int*)s.s[9])[wave] = last;
+    }
+    __syncthreads();
+    const int l = lane_id() & 15;
+    first = of_lane(wave_scan<Least>(l < ST / 64 ? ((const int*)s.s[8])[l] : 0x7FFFFFFF), 15);
+    last = of_lane(wave_scan<Most>(l < ST / 64 ? ((const int*)s.s[9])[l] : -1), 15);
+    return first != 0x7FFFFFFF ? first : last;
+}
 
 // The lowest id in [lo, hi) (lo a multiple of four) up to and with which the
 // weights exceed `aim` (past their sum: the last id with a weight), -1 if there
 // is no weight. aim(sum) gives it. The id is left in s.hit[0], the sum in
 // s.got[1] and the id's weight in s.got[0].
 template <bool F32, typename W, typename A>
-__device__ void draw(const void* row, int lo, int hi, W weight, A aim, RowShared& s) {
+__device__ __forceinline__ void draw(const void* row, int lo, int hi, W weight, A aim, RowShared& s) {
     double* sums = (double*)s.sorted;                            // of 256 ids each, LIST of them at most
     const int t = threadIdx.x, lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(t / 64);
     const int groups = (hi - lo + 255) / 256;
     __syncthreads();
-    for (int g = wave; g < groups; g += ST / 64) {
-        float x[4];
-        const int id = lo + g * 256 + lane * 4;
-        load_logits<F32>(row, id, hi, x);
-        double w = 0.0;
+    constexpr int D = 8;                                         // loads in flight
+    for (int g0 = wave; g0 < groups; g0 += D * (ST / 64)) {
+        float x[D][4];
+        const int base = lo + g0 * 256;
+        load_fours<F32>(row, base + 4 * lane, 256 * (ST / 64), base, 256 * (ST / 64) * (D - 1) + 256, hi, x);
 #pragma unroll
-        for (int v = 0; v < 4; ++v) w += weight(x[v], id + v);
-        w = wave_scan<Plus>(w);
-        if (lane == 63) sums[g] = w;
+        for (int d = 0; d < D; ++d) {
+            const int g = g0 + d * (ST / 64), id = lo + g * 256 + lane * 4;
+            if (g >= groups) break;
+            double w = 0.0;
+#pragma unroll
+            for (int v = 0; v < 4; ++v) w += weight(x[d][v], id + v);
+            w = wave_scan<Plus>(w);
+            if (lane == 63) sums[g] = w;
+        }
     }
-    if (t == 0) s.hit[0] = s.hit[1] = -1;
+    if (t == 0) s.hit[0] = -1;
     __syncthreads();
     // a run of groups for each thread
     const int run = (groups + ST - 1) / ST, g0 = min(t * run, groups), g1 = min(g0 + run, groups);
@@ -459,19 +510,18 @@ __device__ void draw(const void* row, int lo, int hi, W weight, A aim, RowShared
     const double end = block_sums<ST>(own, total, s.s[0]);
     const double want = aim(total);
     // the group: the first one whose end exceeds the aim, else the last one with a weight
+    int first = 0x7FFFFFFF, last = -1;
     {
         double e = end - own;
         for (int g = g0; g < g1; ++g) {
-            const double before = e;
             e += sums[g];
             if (sums[g] > 0.0) {
-                atomicMax(&s.hit[1], g);
-                if (e > want && before <= want) atomicMax(&s.hit[0], g);
+                last = g;
+                if (e > want) first = min(first, g);
             }
         }
     }
-    __syncthreads();
-    const int found = s.hit[0], last = s.hit[1], g = found >= 0 ? found : last;
+    const int g = choose(first, last, s);
     if (g >= g0 && g < g1) {
         double e = end - own;
         for (int i = g0; i < g; ++i) e += sums[i];
@@ -482,12 +532,12 @@ __device__ void draw(const void* row, int lo, int hi, W weight, A aim, RowShared
     if (g < 0) return;                                           // (s.hit[0] is -1)
     if (wave == 0) {
         const double start = s.got[0];
-        float x[4];
+        float x[1][4];
         const int id = lo + g * 256 + lane * 4;
-        load_logits<F32>(row, id, hi, x);
+        load_fours<F32>(row, id, 0, lo + g * 256, 256, hi, x);
         double w[4], sum = 0.0;
 #pragma unroll
-        for (int v = 0; v < 4; ++v) sum += w[v] = weight(x[v], id + v);
+        for (int v = 0; v < 4; ++v) sum += w[v] = weight(x[0][v], id + v);
         double e = start + (wave_scan<Plus>(sum) - sum);
         int at = -1, any = -1;
         double wa = 0.0, wy = 0.0;
@@ -513,217 +563,331 @@ __device__ void draw(const void* row, int lo, int hi, W weight, A aim, RowShared
     __syncthreads();
 }
 
+// A lane's chunks of a row: lane, 64 + lane, ...
+template <typename F>
+__device__ __forceinline__ void each_chunk(int chunks, F f) {
+    for (int c0 = 0; c0 < chunks; c0 += 64) f(c0 + lane_id(), c0 + lane_id() < chunks);
+}
+
+// `listed`: the row's one chunk has left its candidates in s.list
 template <bool F32>
-__device__ void sample_finish(const SampleArgs& a, int r, int chunks, int share, const Chunk* info, const uint64_t* lists, RowShared& s) {
+__device__ __forceinline__ void sample_finish(const SampleArgs& a, int r, int chunks, int share, const Chunk* info, const uint64_t* lists, bool listed, RowShared& s) {
     const void* row = (const uint8_t*)a.logits + (size_t)r * a.stride * (F32 ? 4 : 2);
-    const int V = a.V, t = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(t / 64);
-    // four candidates of a chunk for each thread (memory behind the last one is the lists' own)
-    const int c4 = min(4 * t / share, chunks - 1), i4 = 4 * t - c4 * share;
-    uint64_t e[4];
-    int n4 = 0;
-    if (4 * t < chunks * share) {
-        n4 = info[c4].n;
+    const int V = a.V, t = threadIdx.x, lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(t / 64);
+    // candidates, four of a chunk in a row for each thread (memory behind the last one is the lists' own)
+    uint64_t e[RUN];
+    int n4[RUN / 4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) e[i] = lists[(size_t)c4 * share + i4 + i];
+    for (int g = 0; g < RUN / 4; ++g) {
+        const int slot = 4 * (g * ST + t), c = min(slot / share, chunks - 1), i = slot - c * share;
+        n4[g] = 0;
+        if (slot < chunks * share) {
+            n4[g] = info[c].n - i;
+#pragma unroll
+            for (int v = 0; v < 4; ++v) e[4 * g + v] = listed ? s.list[i + v] : lists[(size_t)c * share + i + v];
+        }
     }
-    Chunk mine{0.0, -INF, INF, -INF, 0};
-    if (t < chunks) mine = info[t];
+    // every wave puts the chunks together for itself
+    float top = -INF, low = INF, cut = -INF;
+    each_chunk(chunks, [&](int c, bool in) __attribute__((always_inline)) {
+        if (!in) return;
+        const Chunk k = info[c];
+        top = fmaxf(top, k.top);
+        low = fminf(low, k.low);
+        cut = fmaxf(cut, k.cut);
+    });
     const Request q(a, r);
     const double u = a.u[r];
-    auto give = [&](int id, double p) {
+    for (int i = t; i < BINS; i += ST) {
+        s.cnt[i] = 0;
+        s.mass[i] = 0;
+    }
+    if (t < 32) s.two[t] = g_two[t];
+    __syncthreads();
+    top = wave_all<Most>(top);
+    low = wave_all<Least>(low);
+    cut = wave_all<Most>(cut);
+    auto give = [&](int id, double p) __attribute__((always_inline)) {
         if (t == 0) {
             a.ids[r] = id;
             if (a.p) a.p[r] = (float)p;
             if (id < 0 && a.err) atomicAdd(a.err, 1);
         }
     };
-    for (int i = t; i < BINS; i += ST) s.cnt[i] = 0;
-    float top, low, cut;
-    {
-        const float wt = wave_scan<Most>(mine.top), wl = wave_scan<Least>(mine.low), wc = wave_scan<Most>(mine.cut);
-        if (lane_id() == 63) {
-            ((float*)s.s[1])[wave] = wt;
-            ((float*)s.s[2])[wave] = wl;
-            ((float*)s.s[3])[wave] = wc;
-        }
-        __syncthreads();
-        const int l = lane_id() & 15;
-        top = of_lane(wave_scan<Most>(((const float*)s.s[1])[l]), 15);
-        low = of_lane(wave_scan<Least>(((const float*)s.s[2])[l]), 15);
-        cut = of_lane(wave_scan<Most>(((const float*)s.s[3])[l]), 15);
-    }
     if (q.bad || !(top < INF) || top == -INF) return give(-1, 0.0);
     const double zmax = top;
-    auto weight = [&](float x) { return x == -INF ? 0.0 : exp_neg(((double)x - zmax) * q.inv); };
+    auto weight = [&](float x) __attribute__((always_inline)) { return weight_of(x, zmax, q.scale, s.two); };
+    auto mass = [&](float x) __attribute__((always_inline)) { return (uint64_t)__builtin_rint(weight(x) * ONE); };
 
     if (q.k == 1) {
         uint64_t best = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (i4 + i < n4) best = Most::of(best, e[i]);
+        for (int i = 0; i < RUN; ++i)
+            if (i % 4 < n4[i / 4]) best = Most::of(best, e[i]);
         return give(place_id(block_all<ST, Most>(best, s.s[4])), 1.0);
     }
-    // the row's weight from the chunks'
-    double all;
-    const double part = t < chunks && mine.sum > 0.0 ? mine.sum * exp_neg(((double)mine.top - zmax) * q.inv) : 0.0;
-    const double end = block_sums<ST>(part, all, s.s[5]);
-    if (q.k == 0 && !q.p_on && !q.m_on) {
-        // no filter: the chunk that the aim falls into (past the sum: the last with a weight)
-        if (t < chunks) s.ends[t] = end;
-        if (t == 0) s.at[0] = s.at[1] = -1;
-        __syncthreads();
+    // the row's weight from the chunks', where they have it
+    double all = 0.0;
+    const bool pure = q.k == 0 && !q.p_on && !q.m_on;
+    auto scaled = [&](int c, bool in) __attribute__((always_inline)) {
+        if (!in || !(info[c].sum > 0.0)) return 0.0;
+        return info[c].sum * exp_neg((double)info[c].top - zmax, q.scale, s.two);
+    };
+    if (q.k == 0 && (q.p_on || pure)) each_chunk(chunks, [&](int c, bool in) __attribute__((always_inline)) { all += wave_all<Plus>(scaled(c, in)); });
+    if (pure) {
+        // no filter: the chunk that the aim falls into (past the sum: the last with a weight), read again
         const double aim = u * all;
-        if (part > 0.0) {
-            atomicMax(&s.at[1], t);
-            if (s.ends[t] > aim && (t == 0 || s.ends[t - 1] <= aim)) atomicMax(&s.at[0], t);
+        double sum = 0.0, before = 0.0;
+        int at = -1;
+        each_chunk(chunks, [&](int c, bool in) __attribute__((always_inline)) {
+            const double w = scaled(c, in), end = sum + wave_scan<Plus>(w);
+            const uint64_t some = __ballot(w > 0.0), hit = some & __ballot(end > aim);
+            if (at < 0 || !(sum > aim)) {
+                const int l = hit ? __ffsll((long long)hit) - 1 : some ? 63 - __clzll((long long)some) : -1;
+                if (l >= 0) {
+                    at = c - lane + l;
+                    before = l ? of_lane(end, l - 1) : sum;
+                }
+            }
+            sum = of_lane(end, 63);
+        });
+        constexpr int NV = CHUNK / (4 * ST);
+        const int id0 = at * CHUNK;
+        float x[NV][4];
+        load_fours<F32>(row, id0 + 4 * t, 4 * ST, id0, CHUNK, V, x);
+        // sums up to and with each lane's four, of each [vector][wave]
+        double w[NV][4], ends[NV];
+#pragma unroll
+        for (int g = 0; g < NV; ++g) {
+            double own = 0.0;
+#pragma unroll
+            for (int v = 0; v < 4; ++v) w[g][v] = 0.0;
+            if (__ballot(x[g][0] > -INF || x[g][1] > -INF || x[g][2] > -INF || x[g][3] > -INF)) {
+#pragma unroll
+                for (int v = 0; v < 4; ++v) own += w[g][v] = weight(x[g][v]);
+            }
+            ends[g] = wave_scan<Plus>(own);
+            if (lane == 63) ((double*)s.s[4])[g * (ST / 64) + wave] = ends[g];
+            ends[g] -= own;
         }
         __syncthreads();
-        const int c = s.at[0] >= 0 ? s.at[0] : s.at[1];
-        const double before = c ? s.ends[c - 1] : 0.0;
-        draw<F32>(row, c * CHUNK, min((c + 1) * CHUNK, V), [&](float x, int) { return weight(x); },
-                  [&](double) { return aim - before; }, s);
-        return give(s.hit[0], s.got[0] / all);
+        static_assert(NV * (ST / 64) == 16, "a lane each");
+        const double part = ((const double*)s.s[4])[lane & 15], upto = before + wave_scan<Plus>(lane < 16 ? part : 0.0);
+        int first = 0x7FFFFFFF, last = -1;
+        double pf = 0.0, pl = 0.0;
+#pragma unroll
+        for (int g = 0; g < NV; ++g) {
+            const int i = g * (ST / 64) + wave;
+            double y = (i ? of_lane(upto, i - 1) : before) + ends[g];
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                const int id = 4 * (g * ST + t) + v;
+                y += w[g][v];
+                if (w[g][v] > 0.0) {
+                    last = id;
+                    pl = w[g][v];
+                    if (y > aim && id < first) {
+                        first = id;
+                        pf = w[g][v];
+                    }
+                }
+            }
+        }
+        const int chosen = choose(first, last, s);
+        if (chosen == first || (chosen == last && first == 0x7FFFFFFF)) {            // (the token's thread)
+            a.ids[r] = id0 + chosen;
+            if (a.p) a.p[r] = (float)((chosen == first ? pf : pl) / all);
+        }
+        return;
     }
 
     // ---- few candidates
     const float least = q.floor(top, all, V), floor = fmaxf(least, low);
-    const Parts<BINS> parts(top, floor);
-    uint64_t border = 0;                                         // the last kept place (before min_p)
-    {
-        bool in[4];
-        int own = 0, n;
+    bool in[RUN];
+    int n;
+    // those that f(i) names of the thread's, into s.list in the order of their ids (barriers before and behind)
+    auto collect = [&](auto f) __attribute__((always_inline)) {
+        int to[RUN / 4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) own += in[i] = i4 + i < n4 && place_logit(e[i]) >= floor;
-        int to = block_sums<ST>(own, n, s.s[6]);
-        if (q.k && n > 2 * q.k + 64) {                           // those of the parts up to the k-th
+        for (int g = 0; g < RUN / 4; ++g) {
+            int before = 0, count = 0;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (in[i]) atomicAdd(&s.cnt[parts.of(place_logit(e[i]))], 1u);
-            __syncthreads();
-            uint32_t before;
-            const int last = part_of_count<ST, BINS>(s.cnt, (uint32_t)q.k, before, s.s[7], s.at);
-            own = 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) own += in[i] = in[i] && parts.of(place_logit(e[i])) <= last;
-            to = block_sums<ST>(own, n, s.s[8]);
-        }
-        to -= own;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (in[i]) {
-                s.list[to] = e[i];
-                s.sorted[to++] = e[i];
+            for (int v = 0; v < 4; ++v) {
+                in[4 * g + v] = f(4 * g + v);
+                const uint64_t b = __ballot(in[4 * g + v]);
+                before += __popcll(b & lanemask_lt());
+                count += __popcll(b);
             }
+            to[g] = before;
+            if (lane == 0) s.part[g * (ST / 64) + wave] = count;
+        }
         __syncthreads();
-        if (n) sort_places(s.sorted, n);
-        // a run of four of the order for each thread
-        int keep = q.k ? min(n, q.k) : n;
-        bool sure = !(cut >= least);                             // nothing that counts was left out
-        if (q.k && !sure) sure = n >= q.k && place_logit(s.sorted[q.k - 1]) > cut;
-        const bool reach = sure;
-        if (q.p_on && n) {
-            double w[4], sum = 0.0, total;
+        static_assert(RUN / 4 * (ST / 64) == 16, "a lane each");
+        const int end = wave_scan<Plus>(lane < 16 ? s.part[lane] : 0);
+        n = of_lane(end, 15);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                w[i] = 4 * t + i < keep ? weight(place_logit(s.sorted[4 * t + i])) : 0.0;
-                sum += w[i];
-            }
-            double before = block_sums<ST>(sum, total, s.s[9]) - sum;
-            const double want = q.top_p * (q.k ? total : all);
-            int m = 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (4 * t + i < keep && (before < want || 4 * t + i == 0)) m = 4 * t + i + 1;
-                before += w[i];
-            }
-            m = block_all<ST, Most>(m, s.s[10]);
-            // (k off, candidates left out: the border has to lie among those that are here, before all of the others)
-            if (!q.k && !reach) sure = total >= want && place_logit(s.sorted[m - 1]) > cut;
-            keep = m;
-        }
-        if (sure) {
-            border = s.sorted[keep - 1];
-            // the draw by id
-            double w[4], sum = 0.0, total;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                w[i] = 0.0;
-                if (4 * t + i < n && s.list[4 * t + i] >= border) {
-                    w[i] = weight(place_logit(s.list[4 * t + i]));
-                    if (w[i] < q.min_p) w[i] = 0.0;
-                }
-                sum += w[i];
-            }
-            if (t == 0) s.hit[0] = 0x7FFFFFFF, s.hit[1] = -1;
-            double x = block_sums<ST>(sum, total, s.s[11]) - sum;
-            const double aim = u * total;
-            int first = 0x7FFFFFFF, last = -1;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                x += w[i];
-                if (w[i] > 0.0) {
-                    last = 4 * t + i;
-                    if (x > aim) first = min(first, 4 * t + i);
-                }
-            }
-            if (last >= 0) atomicMax(&s.hit[1], last);
-            if (first != 0x7FFFFFFF) atomicMin(&s.hit[0], first);
-            __syncthreads();
-            const uint64_t chosen = s.list[s.hit[0] != 0x7FFFFFFF ? s.hit[0] : s.hit[1]];
-            return give(place_id(chosen), weight(place_logit(chosen)) / total);
-        }
-    }
-
-    // ---- many: over the row again. Logits 2^-46 of the largest weight and less do not count.
-    auto mass = [&](float x) { return (uint64_t)__builtin_rint(weight(x) * ONE); };
-    const float bottom = fmaxf(q.least(top, 1.0 / 70368744177664.0), low);
-    const Parts<BINS> every(top, bottom);
-    auto each = [&](auto f) {
-        for (int i = t * 4; i < V; i += ST * 4) {
-            float x[4];
-            load_logits<F32>(row, i, V, x);
+        for (int g = 0; g < RUN / 4; ++g) {
+            const int i = g * (ST / 64) + wave;
+            int at = to[g] + (i ? of_lane(end, i - 1) : 0);
 #pragma unroll
             for (int v = 0; v < 4; ++v)
-                if (x[v] >= bottom) f(x[v], i + v);
+                if (in[4 * g + v]) s.list[at++] = e[4 * g + v];
         }
     };
-    if (q.k || q.p_on) {
+    collect([&](int i) __attribute__((always_inline)) { return i % 4 < n4[i / 4] && place_logit(e[i]) >= floor; });
+    // more than one wave can put in order: the parts up to the k-th first
+    auto candidates = [&](auto f) __attribute__((always_inline)) {
+#pragma unroll
+        for (int v = 0; v < RUN; ++v)
+            if (in[v]) f(place_logit(e[v]), place_id(e[v]));
+    };
+    if (q.k && n > 64 && n > q.k) {
+        const Parts<BINS> parts(top, floor);
+        candidates([&](float x, int) __attribute__((always_inline)) { atomicAdd(&s.cnt[parts.of(x)], 1u); });
         __syncthreads();
-        for (int i = t; i < BINS; i += ST) {
-            s.cnt[i] = 0;
-            s.mass[i] = 0;
+        uint32_t before;
+        const int last = part_of_count<ST, BINS>(s.cnt, (uint32_t)q.k, before, s.s[10], s.at);
+        collect([&](int v) __attribute__((always_inline)) { return in[v] && parts.of(place_logit(e[v])) <= last; });
+        for (int i = t; i < BINS; i += ST) s.cnt[i] = 0;
+    }
+    __syncthreads();
+    if (n <= 64 && !(cut >= least)) {
+        if (wave) return;
+        // a candidate a lane: how many, and what weight, the others have that lie before it
+        const uint64_t mine = lane < n ? s.list[lane] : 0;
+        const double w = lane < n ? weight(place_logit(mine)) : 0.0;
+        double before = 0.0;
+        int rank = 0;
+        for (int i = 0; i < n; ++i) {
+            const bool first = of_lane(mine, i) > mine;
+            rank += first;
+            before += first ? of_lane(w, i) : 0.0;
+        }
+        bool keep = lane < n && (!q.k || rank < q.k);
+        const double whole = q.k ? wave_all<Plus>(keep ? w : 0.0) : all;
+        keep = keep && (!q.p_on || before < q.top_p * whole || rank == 0) && w >= q.min_p;
+        const double end = wave_scan<Plus>(keep ? w : 0.0), total = of_lane(end, 63), aim = u * total;
+        const uint64_t some = __ballot(keep && w > 0.0), hit = some & __ballot(end > aim);
+        const int l = hit ? __ffsll((long long)hit) - 1 : 63 - __clzll((long long)some);
+        return give(place_id(of_lane(mine, l)), of_lane(w, l) / total);
+    }
+    // ---- the border, among the candidates; where it may lie behind one that was
+    // left out, among the row's logits (but those of 2^-46 of the largest weight and less)
+    uint64_t border = 0;                                         // the last kept place (before min_p)
+    const float bottom = fmaxf(q.least(top, 1.0 / 70368744177664.0), low);
+    bool many = false;
+    for (;;) {
+        const float from = many ? bottom : floor, left_out = many || !(cut >= least) ? -INF : cut;
+        const Parts<BINS> parts(top, from);
+        auto each = [&](auto f) __attribute__((always_inline)) {
+            if (!many) {
+                candidates(f);
+                return;
+            }
+            constexpr int D = 4;                                 // loads in flight
+            for (int i = t * 4; i < V; i += D * ST * 4) {
+                float x[D][4];
+                load_fours<F32>(row, i, ST * 4, i - 4 * t, D * ST * 4, V, x);
+#pragma unroll
+                for (int d = 0; d < D; ++d)
+#pragma unroll
+                    for (int v = 0; v < 4; ++v)
+                        if (x[d][v] >= from) f(x[d][v], i + d * ST * 4 + v);
+            }
+        };
+        // counts and masses of the parts
+        const bool both = q.p_on;
+        if (q.k || both) {
+            each([&](float x, int) __attribute__((always_inline)) {
+                const int b = parts.of(x);
+                if (q.k) atomicAdd(&s.cnt[b], 1u);
+                if (both) atomicAdd((unsigned long long*)&s.mass[b], (unsigned long long)mass(x));
+            });
         }
         __syncthreads();
-        each([&](float x, int) {
-            const int b = every.of(x);
-            atomicAdd(&s.cnt[b], 1u);
-            atomicAdd((unsigned long long*)&s.mass[b], (unsigned long long)mass(x));
-        });
-        __syncthreads();
-        // the tokens of part b that lie before (mass: whose masses before them stay below) `want`, the first one always:
-        // the last of them, and all their mass
-        auto border_in = [&](int b, uint64_t want, bool by_mass, uint64_t& kept) -> uint64_t {
-            const int m = (int)s.cnt[b];
+        constexpr int R = BINS / ST;
+        uint64_t own = 0, ends = 0, whole = 0;                   // masses of this thread's parts, up to and with them, of all
+        if (both) {
+#pragma unroll
+            for (int i = 0; i < R; ++i) own += s.mass[R * t + i];
+            ends = block_sums<ST>(own, whole, s.s[5]);
+            if (q.k == 0 && !many) whole = (uint64_t)__builtin_ceil(all * ONE);
+        }
+        bool found = q.k || both || !(left_out > -INF);
+        for (int stage = 0; stage < 2 && found; ++stage) {       // top_k, then top_p
+            if (stage == 0 ? !q.k : !both) continue;
+            // The part, and what lies before it: tokens; masses.
+            int b = -1;
+            uint64_t want;
+            if (stage == 0) {
+                uint32_t before;
+                b = part_of_count<ST, BINS>(s.cnt, (uint32_t)q.k, before, s.s[6], s.at);
+                want = q.k - before;
+                if (b >= 0 && t == b / R) {
+                    uint64_t x = ends - own;
+                    for (int i = R * t; i < b; ++i) x += s.mass[i];
+                    s.before[0] = x;
+                }
+            } else {
+                const double share_of = __builtin_ceil(q.top_p * (double)whole);
+                want = share_of < 1.0 ? 1 : (uint64_t)share_of;
+                __syncthreads();
+                if (t == 0) s.at[0] = -1;
+                __syncthreads();
+                if (ends - own < want && want <= ends) {
+                    uint64_t start = ends - own;
+                    int i = R * t;
+                    while (start + s.mass[i] < want) start += s.mass[i++];
+                    s.at[0] = i;
+                    s.before[1] = start;
+                }
+                __syncthreads();
+                b = s.at[0];
+                if (b >= 0) want -= s.before[1];
+            }
+            if (b < 0) {                                         // never reached: all of them, or candidates left out
+                found = !(left_out > -INF);
+                continue;
+            }
+            // In that part: the last token that lies before `want` tokens (the last
+            // one whose masses before it stay below `want`; the first one always),
+            // and the mass up to and with it.
+            uint64_t place, kept;
             if (t == 0) s.n = 0;
             __syncthreads();
-            if (m <= LIST) {
-                each([&](float x, int id) {
-                    if (every.of(x) == b) s.sorted[atomicAdd(&s.n, 1)] = place_of(x, id);
-                });
-                __syncthreads();
-                sort_places(s.sorted, m);
-                uint64_t w[4], own = 0, all_of;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    w[i] = 4 * t + i < m ? mass(place_logit(s.sorted[4 * t + i])) : 0;
-                    own += w[i];
+            each([&](float x, int id) __attribute__((always_inline)) {
+                if (parts.of(x) == b) {
+                    const int at = atomicAdd(&s.n, 1);
+                    if (at < LIST) s.sorted[at] = place_of(x, id);
                 }
-                uint64_t before = block_sums<ST>(own, all_of, s.s[1]) - own, in = 0;
+            });
+            __syncthreads();
+            const int m = s.n;
+            if (m <= 64) {                                       // every wave for itself: each token against all
+                const uint64_t mine = lane < m ? s.sorted[lane] : 0;
+                const uint64_t w = lane < m ? mass(place_logit(mine)) : 0;
+                uint64_t before = 0;
+                for (int i = 0; i < m; ++i) {
+                    const uint64_t wo = stage ? of_lane(w, i) : 1;
+                    before += of_lane(mine, i) > mine ? wo : 0;
+                }
+                const bool in = lane < m && (before < want || before == 0);      // (the first, and others behind masses of zero)
+                kept = wave_all<Plus>(in ? w : 0);
+                place = wave_all<Least>(in ? mine : ~0ull);
+            } else if (m <= LIST) {
+                sort_places(s.sorted, m);
+                uint64_t w[RUN], sum = 0, all_of;
+#pragma unroll
+                for (int i = 0; i < RUN; ++i) {
+                    w[i] = RUN * t + i < m ? mass(place_logit(s.sorted[RUN * t + i])) : 0;
+                    sum += w[i];
+                }
+                uint64_t before = block_sums<ST>(sum, all_of, s.s[1]) - sum, in = 0;
                 int keep = 0;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int at = 4 * t + i;
-                    if (at < m && ((by_mass ? before : (uint64_t)at) < want || at == 0)) {
+                for (int i = 0; i < RUN; ++i) {
+                    const int at = RUN * t + i;
+                    if (at < m && ((stage ? before : (uint64_t)at) < want || at == 0)) {
                         keep = at + 1;
                         in += w[i];
                     }
@@ -731,82 +895,92 @@ __device__ void sample_finish(const SampleArgs& a, int r, int chunks, int share,
                 }
                 keep = block_all<ST, Most>(keep, s.s[2]);
                 kept = block_all<ST, Plus>(in, s.s[3]);
-                return s.sorted[keep - 1];
-            }
-            // more than can be sorted: halve the range of keys until one is left
-            uint32_t lo = ~0u, hi = 0;
-            each([&](float x, int) {
-                if (every.of(x) == b) {
-                    lo = min(lo, logit_key(x));
-                    hi = max(hi, logit_key(x));
-                }
-            });
-            lo = block_all<ST, Least>(lo, s.s[1]);
-            hi = block_all<ST, Most>(hi, s.s[2]);
-            auto above = [&](uint32_t key, bool masses) {
-                uint64_t v = 0;
-                each([&](float x, int) {
-                    if (every.of(x) == b && logit_key(x) > key) v += masses ? mass(x) : 1;
+                place = s.sorted[keep - 1];
+            } else {
+                // more than can be sorted (the row's logits, then): halve the range of keys until one is left
+                uint32_t lo = ~0u, hi = 0;
+                each([&](float x, int) __attribute__((always_inline)) {
+                    if (parts.of(x) == b) {
+                        lo = min(lo, logit_key(x));
+                        hi = max(hi, logit_key(x));
+                    }
                 });
-                __syncthreads();
-                return block_all<ST, Plus>(v, s.s[3]);
-            };
-            if (want == 0) want = 1;
-            while (lo < hi) {                                    // the smallest key with less than `want` above it
-                const uint32_t mid = lo + (hi - lo) / 2;
-                if (above(mid, by_mass) < want) hi = mid;
-                else lo = mid + 1;
+                lo = block_all<ST, Least>(lo, s.s[1]);
+                hi = block_all<ST, Most>(hi, s.s[2]);
+                // the smallest key with less than `want` above it; last of all what lies above that, and its mass
+                uint64_t above, above_mass;
+                if (want == 0) want = 1;
+                for (bool last = false;;) {
+                    last = lo >= hi;
+                    const uint32_t mid = last ? lo : lo + (hi - lo) / 2;
+                    uint64_t n_above = 0, m_above = 0;
+                    each([&](float x, int) __attribute__((always_inline)) {
+                        if (parts.of(x) == b && logit_key(x) > mid) {
+                            ++n_above;
+                            m_above += mass(x);
+                        }
+                    });
+                    __syncthreads();
+                    above = block_all<ST, Plus>(n_above, s.s[3]);
+                    above_mass = block_all<ST, Plus>(m_above, s.s[4]);
+                    if (last) break;
+                    if ((stage ? above_mass : above) < want) hi = mid;
+                    else lo = mid + 1;
+                }
+                // of the tokens with that key the first by id
+                const uint32_t key = lo;
+                const uint64_t each_one = mass(key_logit(key)), left = want - (stage ? above_mass : above);
+                const double ties = !stage ? (double)left : each_one ? (double)((left + each_one - 1) / each_one) : (double)V;
+                draw<F32>(row, 0, V, [&](float x, int) __attribute__((always_inline)) { return x > -INF && logit_key(x) == key ? 1.0 : 0.0; },
+                          [&](double sum) { return fmin(ties, sum) - 1.0; }, s);
+                kept = above_mass + (uint64_t)fmin(ties, s.got[1]) * each_one;
+                place = (uint64_t)key << 32 | (uint32_t)~s.hit[0];
             }
-            // of the tokens with that key the first by id
-            const uint64_t each_one = by_mass ? mass(key_logit(lo)) : 1, left = want - above(lo, by_mass);
-            const uint64_t ties = each_one ? (left + each_one - 1) / each_one : (uint64_t)V;
-            const uint32_t key = lo;
-            kept = above(lo, true);
-            draw<F32>(row, 0, V, [&](float x, int) { return x > -INF && logit_key(x) == key ? 1.0 : 0.0; },
-                      [&](double sum) { return fmin((double)ties, sum) - 1.0; }, s);
-            kept += (uint64_t)fmin((double)ties, s.got[1]) * mass(key_logit(key));
-            return (uint64_t)key << 32 | (uint32_t)~s.hit[0];
-        };
-        // masses of this thread's two parts, and up to and with them
-        const uint64_t first = s.mass[2 * t], second = s.mass[2 * t + 1];
-        uint64_t whole;
-        const uint64_t ends = block_sums<ST>(first + second, whole, s.s[4]);
-        if (q.k) {
-            uint32_t before;
-            const int b = part_of_count<ST, BINS>(s.cnt, (uint32_t)q.k, before, s.s[5], s.at);
-            if (b >= 0) {
-                if (t == b / 2) s.border[0] = ends - (b & 1 ? second : first + second);
-                __syncthreads();
-                uint64_t kept;
-                border = border_in(b, q.k - before, false, kept);
-                whole = s.border[0] + kept;
-            }
+            border = Most::of(border, place);
+            found = place_logit(place) > left_out;
+            if (stage == 0) whole = s.before[0] + kept;
         }
-        if (q.p_on) {
-            const double x = __builtin_ceil(q.top_p * (double)whole);
-            const uint64_t want = x < 1.0 ? 1 : (uint64_t)x;
-            const uint64_t start = ends - first - second;
-            __syncthreads();
-            if (t == 0) s.at[0] = 0;
-            __syncthreads();
-            if (start < want && want <= ends) {
-                const bool later = start + first < want;
-                s.at[0] = 2 * t + later;
-                s.border[1] = later ? start + first : start;
-            }
-            __syncthreads();
-            uint64_t kept;
-            const int b = s.at[0];
-            const uint64_t p = border_in(b, want - s.border[1], true, kept);
-            border = Most::of(border, p);
+        if (found) break;
+        many = true;
+        border = 0;
+        __syncthreads();
+        for (int i = t; i < BINS; i += ST) {
+            s.cnt[i] = 0;
+            s.mass[i] = 0;
         }
+        __syncthreads();
     }
-    draw<F32>(row, 0, V, [&](float x, int id) {
-                  if (!(x >= bottom) || place_of(x, id) < border) return 0.0;
-                  const double w = weight(x);
-                  return w >= q.min_p ? w : 0.0;
-              }, [&](double sum) { return u * sum; }, s);
-    give(s.hit[0], s.got[0] / s.got[1]);
+    if (many) {
+        draw<F32>(row, 0, V, [&](float x, int id) __attribute__((always_inline)) {
+                      const double w = weight(x);
+                      return x >= bottom && place_of(x, id) >= border && w >= q.min_p ? w : 0.0;
+                  }, [&](double sum) { return u * sum; }, s);
+        return give(s.hit[0], s.got[0] / s.got[1]);
+    }
+    // the draw by id: a run of the list for each thread
+    __syncthreads();
+    const int run = (n + ST - 1) / ST, i0 = min(t * run, n), i1 = min(i0 + run, n);
+    auto kept = [&](int i) __attribute__((always_inline)) {
+        const uint64_t at = s.list[i];
+        const double w = weight(place_logit(at));
+        return at >= border && w >= q.min_p ? w : 0.0;
+    };
+    double sum = 0.0, total;
+    for (int i = i0; i < i1; ++i) sum += kept(i);
+    double x = block_sums<ST>(sum, total, s.s[7]) - sum;
+    const double aim = u * total;
+    int first = 0x7FFFFFFF, last = -1;
+    if (sum > 0.0)
+        for (int i = i0; i < i1; ++i) {
+            const double w = kept(i);
+            x += w;
+            if (w > 0.0) {
+                last = i;
+                if (x > aim) first = min(first, i);
+            }
+        }
+    const uint64_t chosen = s.list[choose(first, last, s)];
+    give(place_id(chosen), weight(place_logit(chosen)) / total);
 }
 
 constexpr int CHUNK_THREADS = 256;
@@ -823,16 +997,21 @@ template <bool F32>
 __global__ void __launch_bounds__(ST) sample_finish_kernel(SampleArgs a, int chunks, int share, const Chunk* info, const uint64_t* lists) {
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
     const size_t i = (size_t)blockIdx.x * chunks;
-    sample_finish<F32>(a, blockIdx.x, chunks, share, info + i, lists + i * share, *(RowShared*)smem);
+    sample_finish<F32>(a, blockIdx.x, chunks, share, info + i, lists + i * share, false, *(RowShared*)smem);
 }
 // rows of one chunk
+struct OneShared {
+    RowShared row;
+    ChunkShared chunk;
+    Chunk info;
+};
 template <bool F32>
-__global__ void __launch_bounds__(ST) sample_row_kernel(SampleArgs a, int share, Chunk* info, uint64_t* lists) {
+__global__ void __launch_bounds__(ST) sample_row_kernel(SampleArgs a) {
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-    const size_t i = blockIdx.x;
-    sample_chunk<F32, ST, CHUNK / ST>(a, (int)i, 0, share, info + i, lists + i * share, *(ChunkShared*)smem);
+    OneShared& s = *(OneShared*)smem;
+    sample_chunk<F32, ST, CHUNK / ST>(a, blockIdx.x, 0, LIST, &s.info, s.row.list, s.chunk);
     __syncthreads();
-    sample_finish<F32>(a, (int)i, 1, share, info + i, lists + i * share, *(RowShared*)smem);
+    sample_finish<F32>(a, blockIdx.x, 1, LIST, &s.info, nullptr, true, s.row);
 }
 
 static int chunks_of(int V) { return (V + CHUNK - 1) / CHUNK; }
@@ -840,6 +1019,7 @@ static int share_of(int chunks) { return LIST / chunks / 4 * 4; }
 static size_t info_bytes(int B, int V) { return ((size_t)B * chunks_of(V) * sizeof(Chunk) + 255) / 256 * 256; }
 size_t sample_workspace_bytes(int B, int V) {
     const int chunks = chunks_of(V);
+    if (chunks == 1) return 0;
     return info_bytes(B, V) + (size_t)B * chunks * share_of(chunks) * 8;
 }
 
@@ -848,15 +1028,15 @@ static hipError_t launch(const SampleArgs& a, void* ws, hipStream_t stream) {
     const int chunks = chunks_of(a.V), share = share_of(chunks);
     Chunk* info = (Chunk*)ws;
     uint64_t* lists = (uint64_t*)((uint8_t*)ws + info_bytes(a.B, a.V));
-    static_assert(sizeof(RowShared) <= 163840 && sizeof(ChunkShared) <= sizeof(RowShared), "LDS");
+    static_assert(sizeof(OneShared) <= 163840, "LDS");
     int dev = 0;
     hipError_t e = hipGetDevice(&dev);
     if (e != hipSuccess) return e;
     static std::atomic<uint64_t> done[2];
     if (chunks == 1) {
-        e = allow_lds((const void*)sample_row_kernel<F32>, sizeof(RowShared), dev, done[0]);
+        e = allow_lds((const void*)sample_row_kernel<F32>, sizeof(OneShared), dev, done[0]);
         if (e != hipSuccess) return e;
-        return launch_kernel(K_SAMPLE, stream, sample_row_kernel<F32>, dim3((unsigned)a.B), dim3(ST), sizeof(RowShared), a, share, info, lists);
+        return launch_kernel(K_SAMPLE, stream, sample_row_kernel<F32>, dim3((unsigned)a.B), dim3(ST), sizeof(OneShared), a);
     }
     e = allow_lds((const void*)sample_finish_kernel<F32>, sizeof(RowShared), dev, done[1]);
     if (e != hipSuccess) return e;
