@@ -83,7 +83,7 @@ __device__ __forceinline__ f32x4 mfma_block(const i32x8& a, const i32x8& b, int 
 // (zero times a NaN code from the next row would be NaN).
 constexpr int SCALE_STEPS = 16;
 
-template <int TM, int TN, int WM, int WN, int R, bool GLU, bool ANY>
+template <int TM, int TN, int WM, int WN, int R, bool GLU, bool F32, bool ANY>
 __global__ void __launch_bounds__(64 * WM * WN, 2) gemm_fp8_tile_kernel(Fp8Args p, int tiles_m, int tiles_n) {
     constexpr int WAVES = WM * WN;
     constexpr int MF = TM / WM / 16, NF = TN / WN / 16;
@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gemm_fp8_tile_kernel(Fp8Args 
     };
     auto scales_store = [&](int slot) __attribute__((always_inline)) {
         const int t = wv * 64 + opaque_lane(), row = t >> 1;
-        uint8_t* to = s_scale + slot * SCALES + (8 * (t & 1) * (TM / 64) + row / 64) * 64 + (row & 15) * 4 + ((row >> 4) & 3);
+        uint8_t* to = s_scale + slot * SCALES + (8 * (t & 1) * (TM / 64) + row / 64) * 64 + (F32 ? row & 63 : (row & 15) * 4 + ((row >> 4) & 3));
 #pragma unroll
         for (int i = 0; i < 8; ++i) to[i * TM] = (uint8_t)(sc[i / 4] >> (8 * (i % 4)));
         if (t < 2 * SCALE_STEPS) *(float*)(s_scale + slot * SCALES + SCALE_STEPS * TM + 4 * t) = sf;
@@ -222,13 +222,16 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gemm_fp8_tile_kernel(Fp8Args 
     auto read_b = [&](int off, int n) __attribute__((always_inline)) {
         fb[n % 2] = join(*(const i32x4*)(smem + loB + off + n * 2048), *(const i32x4*)(smem + (loB ^ 64) + off + n * 2048));
     };
-    int e = 0;
+    int e[F32 ? MF : 1];                                         // scales of row m of each fragment; F32: of rows 4 q .. of one
     float f0 = 0.f, f1 = 0.f;
     // this wave's scales of step s (slot: of its 16 steps)
     auto read_scales = [&](int s, int slot) __attribute__((always_inline)) {
         const uint8_t* at = s_scale + slot * SCALES;
         const int i = s % SCALE_STEPS;
-        e = *(const int*)(at + (i * (TM / 64) + mw) * 64 + 4 * (lane & 15));
+        if constexpr (F32) {
+#pragma unroll
+            for (int a = 0; a < MF; ++a) e[a] = *(const int*)(at + (i * (TM / 64) + mw) * 64 + 16 * a + 4 * (lane >> 4));
+        } else e[0] = *(const int*)(at + (i * (TM / 64) + mw) * 64 + 4 * (lane & 15));
         const float* f = (const float*)(at + SCALE_STEPS * TM);
         f0 = f[(!GLU && TN > 128 ? nw * NF * 16 / 128 * SCALE_STEPS : 0) + i];
         if (GLU) f1 = f[SCALE_STEPS + i];
@@ -244,29 +247,61 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gemm_fp8_tile_kernel(Fp8Args 
     // loaded. nstep, nslot: the next step and its scales' slot.
     auto step = [&](int st, int nstep, int nslot, int k0, bool pending, int put, int fetch) __attribute__((always_inline)) {
         const int cur = opaque_stage(st), nxt_st = R == 2 ? st ^ 1 : (st + 1) % R, nxt = opaque_stage(nxt_st);
-        const int e0 = e;
+        int e0[F32 ? MF : 1];
+#pragma unroll
+        for (int a = 0; a < (F32 ? MF : 1); ++a) e0[a] = e[a];
         const float g0 = f0, g1 = f1;
         f32x4 x[DEPTH + 1];
+        bf16x8 wa[F32 ? MF : 1][4], wb[4];
+        if constexpr (F32) {
+#pragma unroll
+            for (int a = 0; a < MF; ++a)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) wa[a][i] = widen(fa[a], i);
+        }
         auto fma = [&](int k) __attribute__((always_inline)) {
             const int n = k / MF, a = k % MF;
             const float s = GLU && n >= NC ? g1 : g0;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[a][n][i] = __builtin_fmaf(x[k % (DEPTH + 1)][i], s, acc[a][n][i]);
-            asm volatile("" : "+v"(acc[a][n]));          // (here: the compiler would move it, and its matrix instruction, past the step's branches)
+            for (int i = 0; i < 4; ++i) {
+                float y = x[k % (DEPTH + 1)][i];
+                if constexpr (F32) y *= e8m0_f32((uint32_t)e0[a] >> (8 * i) & 255);
+                acc[a][n][i] = __builtin_fmaf(y, s, acc[a][n][i]);
+            }
+            asm volatile("" : "+v"(acc[a][n]));
+        };
+        // the instructions up to k stay before the branch that follows (the
+        // compiler would move them past it, to their multiply-adds, and hold the
+        // fragments of two steps)
+        auto issued = [&](int k) __attribute__((always_inline)) {
+#pragma unroll
+            for (int i = 0; i < DEPTH; ++i) asm volatile("" : "+v"(x[(k - i) % (DEPTH + 1)]));
         };
         if (TM == 128) __builtin_amdgcn_s_setprio(1);
 #pragma unroll
         for (int k = 0; k < NK; ++k) {
             const int n = k / MF, a = k % MF;
             f32x4& y = x[k % (DEPTH + 1)];
-            if (a == 0) y = mfma_block<0>(fa[a], fb[n % 2], e0);
-            if (a == 1) y = mfma_block<1>(fa[a], fb[n % 2], e0);
-            if (a == 2) y = mfma_block<2>(fa[a], fb[n % 2], e0);
-            if (a == 3) y = mfma_block<3>(fa[a], fb[n % 2], e0);
+            if constexpr (F32) {
+                if (a == 0) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) wb[i] = widen(fb[n % 2], i);
+                }
+                y = f32x4{0, 0, 0, 0};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) y = mfma_bf16_16x16x32(wa[a][i], wb[i], y);
+            } else {
+                if (a == 0) y = mfma_block<0>(fa[a], fb[n % 2], e0[0]);
+                if (a == 1) y = mfma_block<1>(fa[a], fb[n % 2], e0[0]);
+                if (a == 2) y = mfma_block<2>(fa[a], fb[n % 2], e0[0]);
+                if (a == 3) y = mfma_block<3>(fa[a], fb[n % 2], e0[0]);
+            }
+            __builtin_amdgcn_sched_barrier(0);
             if (k >= DEPTH) fma(k - DEPTH);
             if (k == BAR) {
                 if (TM == 128) __builtin_amdgcn_s_setprio(0);
                 wait_vmcnt<(R - 2) * NL>();
+                issued(k);
                 if (pending) scales_store(put);
                 end_of_k(nstep, nxt_st);
                 barrier_lds();
@@ -282,6 +317,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gemm_fp8_tile_kernel(Fp8Args 
                 if (BAR + 1 + l * (NK - 1 - BAR) / NL == k) dma(k0, st, l);
             __builtin_amdgcn_sched_barrier(0);
         }
+        issued(NK - 1);
         if (fetch >= 0) scales_load(fetch);
 #pragma unroll
         for (int k = NK - DEPTH; k < NK; ++k) fma(k);
@@ -306,8 +342,8 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gemm_fp8_tile_kernel(Fp8Args 
         for (int a = 0; a < MF; ++a) {
             // the addends of NB rows are loaded together (rows and columns past
             // the output: from inside it, and dropped)
-            constexpr int AB = 4;
-            Cols<NC, false, ANY> plus[ADD ? AB : 1];
+            constexpr int AB = F32 ? 2 : 4;
+            Cols<NC, F32, ANY> plus[ADD ? AB : 1];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 if constexpr (ADD) {
@@ -332,7 +368,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gemm_fp8_tile_kernel(Fp8Args 
 #pragma unroll
                     for (int n = 0; n < NC; ++n) asm volatile("" : "+v"(v[n]));
                 }
-                if (row < p.M && full) Cols<NC, false, ANY>::store(p.out, (size_t)row * p.N + col, v);
+                if (row < p.M && full) Cols<NC, F32, ANY>::store(p.out, (size_t)row * p.N + col, v);
             }
         }
         // a wave in which the output's rows end inside a lane: that lane's columns
@@ -352,11 +388,11 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gemm_fp8_tile_kernel(Fp8Args 
                 if (full) continue;
                 if constexpr (ADD) {
 #pragma unroll
-                    for (int i = 0; i < RB; ++i) add_each<NC, false>(p, row + i, col, v[i]);
+                    for (int i = 0; i < RB; ++i) add_each<NC, F32>(p, row + i, col, v[i]);
                 }
 #pragma unroll
                 for (int i = 0; i < RB; ++i)
-                    if (row + i < p.M) store_each<NC, false>(p, row + i, col, v[i]);
+                    if (row + i < p.M) store_each<NC, F32>(p, row + i, col, v[i]);
             }
         }
     };
@@ -383,6 +419,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gemm_fp8_tile_kernel(Fp8Args 
     for (int a = 0; a < MF; ++a) read_a(opaque_stage(0), a);
     read_b(opaque_stage(0), 0);
     read_b(opaque_stage(0), 1);
+    __builtin_amdgcn_s_waitcnt(0xC07F);                          // (lgkmcnt(0): left open, it would be waited for in every step)
     int st = 0, slot = 0;                                        // slot: of the scales of the step being multiplied
     bool pending = false;
     if constexpr (R > 2) {                                       // (one tile a workgroup)
@@ -601,17 +638,17 @@ __global__ void __launch_bounds__(64 * WK) gemm_fp8_split_kernel(Fp8Args p, int 
 }
 
 // ------------------------------------------------------------------ launch
-template <int TM, int TN, int WM, int WN, int R, bool GLU, bool ANY>
+template <int TM, int TN, int WM, int WN, int R, bool GLU, bool F32, bool ANY>
 static hipError_t launch_tile(const Fp8Args& p, int dev, int kid, hipStream_t stream) {
     constexpr int OUTN = GLU ? TN / 2 : TN;
     constexpr int SMEM = R * (TM + TN) * 128 + 2 * SCALE_STEPS * (TM + 8) + 8 * TN;
     constexpr int PER_CU = 163840 / SMEM < 8 / (WM * WN) ? 163840 / SMEM : 8 / (WM * WN);
     static std::atomic<uint64_t> done{0};
-    const hipError_t e = allow_lds((const void*)gemm_fp8_tile_kernel<TM, TN, WM, WN, R, GLU, ANY>, SMEM, dev, done);
+    const hipError_t e = allow_lds((const void*)gemm_fp8_tile_kernel<TM, TN, WM, WN, R, GLU, F32, ANY>, SMEM, dev, done);
     if (e != hipSuccess) return e;
     const int tm = (p.M + TM - 1) / TM, tn = (p.N + OUTN - 1) / OUTN;
     const int slots = (device_cus(dev) * PER_CU + 7) / 8 * 8, grid = min(slots, (tm * tn + 7) / 8 * 8);
-    return launch_kernel(kid, stream, gemm_fp8_tile_kernel<TM, TN, WM, WN, R, GLU, ANY>, dim3((unsigned)grid),
+    return launch_kernel(kid, stream, gemm_fp8_tile_kernel<TM, TN, WM, WN, R, GLU, F32, ANY>, dim3((unsigned)grid),
                          dim3(64 * WM * WN), SMEM, p, tm, tn);
 }
 
@@ -640,15 +677,15 @@ static hipError_t launch_any(const Fp8Args& p, int kid, hipStream_t stream) {
     const bool few = shape_tiles(shape, p.M, rows_b) <= cus;             // at most one tile a CU
     if constexpr (!F32) {
         if (shape == S_256x256)
-            return p.lines ? launch_tile<256, 256, 4, 2, 2, GLU, false>(p, dev, kid, stream)
-                           : launch_tile<256, 256, 4, 2, 2, GLU, true>(p, dev, kid, stream);
-        if (shape == S_128x128) {
-            if (few)
-                return p.lines ? launch_tile<128, 128, 2, 2, 4, GLU, false>(p, dev, kid, stream)
-                               : launch_tile<128, 128, 2, 2, 4, GLU, true>(p, dev, kid, stream);
-            return p.lines ? launch_tile<128, 128, 2, 2, 2, GLU, false>(p, dev, kid, stream)
-                           : launch_tile<128, 128, 2, 2, 2, GLU, true>(p, dev, kid, stream);
-        }
+            return p.lines ? launch_tile<256, 256, 4, 2, 2, GLU, false, false>(p, dev, kid, stream)
+                           : launch_tile<256, 256, 4, 2, 2, GLU, false, true>(p, dev, kid, stream);
+    }
+    if (shape == S_128x128) {
+        if (few)
+            return p.lines ? launch_tile<128, 128, 2, 2, 4, GLU, F32, false>(p, dev, kid, stream)
+                           : launch_tile<128, 128, 2, 2, 4, GLU, F32, true>(p, dev, kid, stream);
+        return p.lines ? launch_tile<128, 128, 2, 2, 2, GLU, F32, false>(p, dev, kid, stream)
+                       : launch_tile<128, 128, 2, 2, 2, GLU, F32, true>(p, dev, kid, stream);
     }
     switch (shape) {
         case S_32x64:
