@@ -90,22 +90,22 @@ constexpr int pick_shape(int M, long long rows_b, int K, long long cus) { return
 
 // The e4m3 products (gemm_fp8.hip) have the same shapes at costs of their own;
 // with fp32 outputs, whose codes are widened to bf16 in registers, no 256 x 256
-// tile. Fits to 2800 products with bf16 outputs, plain and gated, and 3600 with
-// fp32 outputs (1..16384 rows, 64..8192 columns, fp32 to 32768, K 128..8192), each
-// timed with every shape: where the best takes 5.5 us and more, the picked one is
-// 0.3% (fp32 0.6%) slower on average, 1.04 (1.07) times in the worst hundredth.
-// E.g. 328 x 7213 x 2560: 32x64 17.4 us, 128x128 19.8, 256x256 36.5; 767 x 2816 x
-// 3968 (fp32) 32x64 30.8, 64x64 34.3, 128x128 52; 784 x 9216 x 512 (fp32)
-// 128x128 15.2, 64x64 20.6.
-constexpr Shape kShapesFp8[S_COUNT] = {{256, 256, 1, 1.104f, 0.952f, 3.589f},
-                                       {128, 128, 2, 0.472f, 0.669f, 1.687f},
-                                       {64, 64, 2, 0.249f, 0.320f, 1.098f},
-                                       {32, 64, 3, 0.210f, 0.284f, 0.502f},
-                                       {32, 32, 2, 0.105f, 0.216f, 0.583f}};
+// tile. Fits to 4300 products with bf16 outputs, plain and gated, and 5300 with
+// fp32 outputs (1..16384 rows, 64..16384 columns, fp32 to 32768, K 128..8192),
+// timed with every shape that could pay: where the best takes 5.5 us and more, the
+// picked one is 0.5% slower on average, 1.08 times in the worst hundredth. E.g.
+// 328 x 7213 x 2560: 32x64 17.4 us, 128x128 19.8, 256x256 36.5; 778 x 11393 x
+// 6784: 256x256 90 us, 128x128 97, 64x64 124; 767 x 2816 x 3968 (fp32) 32x64
+// 30.8, 64x64 34.3, 128x128 52; 784 x 9216 x 512 (fp32) 128x128 15.2, 64x64 20.6.
+constexpr Shape kShapesFp8[S_COUNT] = {{256, 256, 1, 1.129f, 1.241f, 2.323f},
+                                       {128, 128, 2, 0.506f, 0.774f, 1.387f},
+                                       {64, 64, 2, 0.223f, 0.358f, 1.212f},
+                                       {32, 64, 3, 0.202f, 0.260f, 0.596f},
+                                       {32, 32, 2, 0.100f, 0.221f, 0.669f}};
 constexpr Shape kShapesFp8F32[S_COUNT] = {{256, 256, 1, 1e6f, 1e6f, 1e6f},
-                                          {128, 128, 2, 0.715f, 1.135f, 1.570f},
-                                          {64, 64, 2, 0.159f, 0.340f, 1.031f},
-                                          {32, 64, 3, 0.017f, 0.167f, 0.752f},
-                                          {32, 32, 2, 0.005f, 0.100f, 0.593f}};
+                                          {128, 128, 2, 0.671f, 0.897f, 1.617f},
+                                          {64, 64, 2, 0.153f, 0.263f, 1.288f},
+                                          {32, 64, 3, 0.055f, 0.232f, 0.688f},
+                                          {32, 32, 2, 0.026f, 0.140f, 0.522f}};
 
 }  // namespace moe
