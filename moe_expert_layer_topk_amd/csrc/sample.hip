@@ -42,6 +42,7 @@ constexpr int RUN = LIST / ST;                                   // of a thread
 constexpr int BINS = 2048;
 constexpr double ONE = 4398046511104.0;                          // 2^42: the sum of 2^20 weights stays below 2^63
 constexpr float INF = __builtin_inff();
+constexpr int STEPS = 256;                                       // a chunk's steps of an eighth of the temperature
 
 struct Chunk {
     double sum;               // weight relative to `top`
@@ -112,6 +113,11 @@ struct Request {
         min_p = mp > 0.f ? mp : 0.f;
         p_on = tp < 1.f && k != 1;
         m_on = mp > 0.f && k != 1;
+    }
+    // The step that a logit is in: they are an eighth of the temperature wide and the
+    // same for every chunk. Monotone in x; clamped where an int would not hold it.
+    __device__ __forceinline__ int step(float x) const {
+        return (int)floorf(fminf(fmaxf(x * (8.f / temperature), -1e9f), 1e9f));
     }
     // a logit below which the weight does not reach w beside a logit of m (the
     // hardware's logarithm and fp32's steps are far within the 1e-5)
@@ -298,6 +304,7 @@ __device__ __forceinline__ void sort_places(uint64_t* p, int n) {
 constexpr int CHUNK_BINS = 1024;
 struct ChunkShared {
     double two[32];
+    uint64_t mass[STEPS];
     uint32_t cnt[CHUNK_BINS];
     uint64_t s[8][16];
     int at[2];
@@ -306,7 +313,7 @@ struct ChunkShared {
 
 // NT threads with E logits each; `share`: how many candidates may be written
 template <bool F32, int NT, int E>
-__device__ __forceinline__ void sample_chunk(const SampleArgs& a, int r, int c, int share, Chunk* info, uint64_t* list, ChunkShared& s) {
+__device__ __forceinline__ void sample_chunk(const SampleArgs& a, int r, int c, int share, Chunk* info, uint64_t* list, uint64_t* steps, ChunkShared& s) {
     constexpr int NV = E / 4, SW = NT / 64;
     static_assert(NT * E == CHUNK && NV <= 4, "chunk");
     const void* row = (const uint8_t*)a.logits + (size_t)r * a.stride * (F32 ? 4 : 2);
@@ -315,6 +322,7 @@ __device__ __forceinline__ void sample_chunk(const SampleArgs& a, int r, int c, 
     load_fours<F32>(row, c0 + 4 * t, 4 * NT, c0, CHUNK, V, x);
     const Request q(a, r);
     for (int i = t; i < CHUNK_BINS; i += NT) s.cnt[i] = 0;
+    for (int i = t; i < STEPS; i += NT) s.mass[i] = 0;
     if (t < 32) s.two[t] = g_two[t];
     float top = -INF, low = INF;
 #pragma unroll
@@ -357,13 +365,27 @@ __device__ __forceinline__ void sample_chunk(const SampleArgs& a, int r, int c, 
     }
     // the chunk's weight, where the row's is needed (with top_k its candidates have it; min_p alone: likewise)
     if (q.k == 0 && (q.p_on || !q.m_on)) {
+        // (top_p: by steps below the largest logit's too, for a border among many tokens)
+        const int first = q.step(top);
         double sum = 0.0;
 #pragma unroll
         for (int j = 0; j < NV; ++j)
-            if (__ballot(x[j][0] > -INF || x[j][1] > -INF || x[j][2] > -INF || x[j][3] > -INF))
+            if (__ballot(x[j][0] > -INF || x[j][1] > -INF || x[j][2] > -INF || x[j][3] > -INF)) {
+                double w[4];
 #pragma unroll
-            for (int v = 0; v < 4; ++v) sum += weight_of(x[j][v], top, q.scale, s.two);
+                for (int v = 0; v < 4; ++v) sum += w[v] = weight_of(x[j][v], top, q.scale, s.two);
+                if (q.p_on) {
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) {
+                        const int i = first - q.step(x[j][v]);
+                        if (x[j][v] > -INF && i < STEPS)
+                            atomicAdd((unsigned long long*)&s.mass[i], (unsigned long long)__builtin_rint(w[v] * ONE));
+                    }
+                }
+            }
         out.sum = block_all<NT, Plus>(sum, s.s[2]);
+        if (q.p_on && steps)
+            for (int i = t; i < STEPS; i += NT) steps[i] = s.mass[i];
     }
     if (q.k == 0 && !q.p_on && !q.m_on) {
         if (t == 0) *info = out;
@@ -452,6 +474,9 @@ struct RowShared {
     uint64_t sorted[LIST];    // a part's tokens; the groups' sums of a draw
     uint32_t cnt[BINS];
     uint64_t mass[BINS];
+    double share[MAX_CHUNKS], above[MAX_CHUNKS];                 // a chunk's weights' unit in the row's; its kept weight in whole steps
+    uint64_t kept[MAX_CHUNKS];                                   // ... in the border's step, as a mass
+    int shift[MAX_CHUNKS];
     uint64_t s[16][16];
     double got[2];
     uint64_t before[2];
@@ -569,9 +594,465 @@ __device__ __forceinline__ void each_chunk(int chunks, F f) {
     for (int c0 = 0; c0 < chunks; c0 += 64) f(c0 + lane_id(), c0 + lane_id() < chunks);
 }
 
+// The draw from the kept tokens, those from place `least` on, whose weight in chunk
+// c is kept(c, in): the chunk that the aim falls into (past the sum: the last with
+// a weight), read again.
+template <bool F32, typename K, typename W>
+__device__ __forceinline__ void draw_by_chunks(const SampleArgs& a, int r, const void* row, int chunks, K kept, W weight, double total, uint64_t least,
+                                               RowShared& s) {
+    const int V = a.V, t = threadIdx.x, lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(t / 64);
+    const double u = a.u[r];
+        const double aim = u * total;
+    double sum = 0.0, before = 0.0;
+    int at = -1;
+    each_chunk(chunks, [&](int c, bool in) __attribute__((always_inline)) {
+        const double w = kept(c, in), end = sum + wave_scan<Plus>(w);
+        const uint64_t some = __ballot(w > 0.0), hit = some & __ballot(end > aim);
+        if (at < 0 || !(sum > aim)) {
+            const int l = hit ? __ffsll((long long)hit) - 1 : some ? 63 - __clzll((long long)some) : -1;
+            if (l >= 0) {
+                at = c - lane + l;
+                before = l ? of_lane(end, l - 1) : sum;
+            }
+        }
+        sum = of_lane(end, 63);
+    });
+    constexpr int NV = CHUNK / (4 * ST);
+    const int id0 = at * CHUNK;
+    float x[NV][4];
+    load_fours<F32>(row, id0 + 4 * t, 4 * ST, id0, CHUNK, V, x);
+    // sums up to each lane's four, of each [vector][wave]
+    double w[NV][4], ends[NV];
+#pragma unroll
+    for (int g = 0; g < NV; ++g) {
+        double own = 0.0;
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+            w[g][v] = 0.0;
+            if (place_of(x[g][v], id0 + 4 * (g * ST + t) + v) < least) x[g][v] = -INF;
+        }
+        if (__ballot(x[g][0] > -INF || x[g][1] > -INF || x[g][2] > -INF || x[g][3] > -INF)) {
+#pragma unroll
+            for (int v = 0; v < 4; ++v) own += w[g][v] = weight(x[g][v]);
+        }
+        ends[g] = wave_scan<Plus>(own);
+        if (lane == 63) ((double*)s.s[4])[g * (ST / 64) + wave] = ends[g];
+        ends[g] -= own;
+    }
+    __syncthreads();
+    static_assert(NV * (ST / 64) == 16, "a lane each");
+    const double part = ((const double*)s.s[4])[lane & 15], upto = before + wave_scan<Plus>(lane < 16 ? part : 0.0);
+    int first = 0x7FFFFFFF, last = -1;
+    double pf = 0.0, pl = 0.0;
+#pragma unroll
+    for (int g = 0; g < NV; ++g) {
+        const int i = g * (ST / 64) + wave;
+        double y = (i ? of_lane(upto, i - 1) : before) + ends[g];
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+            const int id = 4 * (g * ST + t) + v;
+            y += w[g][v];
+            if (w[g][v] > 0.0) {
+                last = id;
+                pl = w[g][v];
+                if (y > aim && id < first) {
+                    first = id;
+                    pf = w[g][v];
+                }
+            }
+        }
+    }
+    const int chosen = choose(first, last, s);
+    if (chosen == first || (chosen == last && first == 0x7FFFFFFF)) {            // (the token's thread)
+        a.ids[r] = id0 + chosen;
+        if (a.p) a.p[r] = (float)((chosen == first ? pf : pl) / total);
+    }
+}
+
+// The border of the tokens that each(f) calls f(logit, id) for, by counts and masses
+// of equal parts of [from, top], which fill(parts) adds up. share_of: the weight that
+// top_p is a share of (0: that of these tokens, or of those that top_k leaves).
+// False if the border may lie behind left_out. ALL: there may be more tokens in a
+// part than can be sorted; nth(key, n) then finds the n-th id (the last, of fewer)
+// with a logit's key. A barrier before; s.cnt and s.mass are zero.
+template <bool ALL, typename M, typename E, typename F, typename N>
+__device__ __forceinline__ bool find_border(const Request& q, float top, float from, double share_of, float left_out, M mass, E each, F fill, N nth,
+                                            uint64_t& border, RowShared& s) {
+    const int t = threadIdx.x, lane = lane_id();
+    const Parts<BINS> parts(top, from);
+    border = 0;
+    // counts and masses of the parts
+    const bool both = q.p_on;
+    fill(parts);
+    __syncthreads();
+    constexpr int R = BINS / ST;
+    uint64_t own = 0, ends = 0, whole = 0;                   // masses of this thread's parts, up to and with them, of all
+    if (both) {
+#pragma unroll
+        for (int i = 0; i < R; ++i) own += s.mass[R * t + i];
+        ends = block_sums<ST>(own, whole, s.s[5]);
+        if (share_of > 0.0) whole = (uint64_t)__builtin_ceil(share_of * ONE);
+    }
+    bool found = q.k || both || !(left_out > -INF);
+    for (int stage = 0; stage < 2 && found; ++stage) {       // top_k, then top_p
+        if (stage == 0 ? !q.k : !both) continue;
+        // The part, and what lies before it: tokens; masses.
+        int b = -1;
+        uint64_t want;
+        if (stage == 0) {
+            uint32_t before;
+            b = part_of_count<ST, BINS>(s.cnt, (uint32_t)q.k, before, s.s[6], s.at);
+            want = q.k - before;
+            if (b >= 0 && t == b / R) {
+                uint64_t x = ends - own;
+                for (int i = R * t; i < b; ++i) x += s.mass[i];
+                s.before[0] = x;
+            }
+        } else {
+            const double part = __builtin_ceil(q.top_p * (double)whole);
+            want = part < 1.0 ? 1 : (uint64_t)part;
+            __syncthreads();
+            if (t == 0) s.at[0] = -1;
+            __syncthreads();
+            if (ends - own < want && want <= ends) {
+                uint64_t start = ends - own;
+                int i = R * t;
+                while (start + s.mass[i] < want) start += s.mass[i++];
+                s.at[0] = i;
+                s.before[1] = start;
+            }
+            __syncthreads();
+            b = s.at[0];
+            if (b >= 0) want -= s.before[1];
+        }
+        if (b < 0) {                                         // never reached: all of them, or candidates left out
+            found = !(left_out > -INF);
+            continue;
+        }
+        // In that part: the last token that lies before `want` tokens (the last
+        // one whose masses before it stay below `want`; the first one always),
+        // and the mass up to and with it.
+        uint64_t place, kept;
+        if (t == 0) s.n = 0;
+        __syncthreads();
+        each([&](float x, int id) __attribute__((always_inline)) {
+            if (parts.of(x) == b) {
+                const int at = atomicAdd(&s.n, 1);
+                if (at < LIST) s.sorted[at] = place_of(x, id);
+            }
+        });
+        __syncthreads();
+        const int m = s.n;
+        if (m <= 64) {                                       // every wave for itself: each token against all
+            const uint64_t mine = lane < m ? s.sorted[lane] : 0;
+            const uint64_t w = lane < m ? mass(place_logit(mine)) : 0;
+            uint64_t before = 0;
+            for (int i = 0; i < m; ++i) {
+                const uint64_t wo = stage ? of_lane(w, i) : 1;
+                before += of_lane(mine, i) > mine ? wo : 0;
+            }
+            const bool in = lane < m && (before < want || before == 0);      // (the first, and others behind masses of zero)
+            kept = wave_all<Plus>(in ? w : 0);
+            place = wave_all<Least>(in ? mine : ~0ull);
+        } else if (m <= LIST) {
+            sort_places(s.sorted, m);
+            uint64_t w[RUN], sum = 0, all_of;
+#pragma unroll
+            for (int i = 0; i < RUN; ++i) {
+                w[i] = RUN * t + i < m ? mass(place_logit(s.sorted[RUN * t + i])) : 0;
+                sum += w[i];
+            }
+            uint64_t before = block_sums<ST>(sum, all_of, s.s[1]) - sum, in = 0;
+            int keep = 0;
+#pragma unroll
+            for (int i = 0; i < RUN; ++i) {
+                const int at = RUN * t + i;
+                if (at < m && ((stage ? before : (uint64_t)at) < want || at == 0)) {
+                    keep = at + 1;
+                    in += w[i];
+                }
+                before += w[i];
+            }
+            keep = block_all<ST, Most>(keep, s.s[2]);
+            kept = block_all<ST, Plus>(in, s.s[3]);
+            place = s.sorted[keep - 1];
+        } else if constexpr (ALL) {
+            // more than can be sorted (the row's logits, then): halve the range of keys until one is left
+            uint32_t lo = ~0u, hi = 0;
+            each([&](float x, int) __attribute__((always_inline)) {
+                if (parts.of(x) == b) {
+                    lo = min(lo, logit_key(x));
+                    hi = max(hi, logit_key(x));
+                }
+            });
+            lo = block_all<ST, Least>(lo, s.s[1]);
+            hi = block_all<ST, Most>(hi, s.s[2]);
+            // the smallest key with less than `want` above it; last of all what lies above that, and its mass
+            uint64_t above, above_mass;
+            if (want == 0) want = 1;
+            for (bool last = false;;) {
+                last = lo >= hi;
+                const uint32_t mid = last ? lo : lo + (hi - lo) / 2;
+                uint64_t n_above = 0, m_above = 0;
+                each([&](float x, int) __attribute__((always_inline)) {
+                    if (parts.of(x) == b && logit_key(x) > mid) {
+                        ++n_above;
+                        m_above += mass(x);
+                    }
+                });
+                __syncthreads();
+                above = block_all<ST, Plus>(n_above, s.s[3]);
+                above_mass = block_all<ST, Plus>(m_above, s.s[4]);
+                if (last) break;
+                if ((stage ? above_mass : above) < want) hi = mid;
+                else lo = mid + 1;
+            }
+            // of the tokens with that key the first by id
+            const uint32_t key = lo;
+            const uint64_t each_one = mass(key_logit(key)), left = want - (stage ? above_mass : above);
+            const double ties = !stage ? (double)left : each_one ? (double)((left + each_one - 1) / each_one) : (double)MOE_SAMPLE_MAX_COLS;
+            nth(key, ties);
+            kept = above_mass + (uint64_t)fmin(ties, s.got[1]) * each_one;
+            place = (uint64_t)key << 32 | (uint32_t)~s.hit[0];
+        } else {                                             // (LIST candidates are sorted)
+            place = kept = 0;
+        }
+        border = Most::of(border, place);
+        found = place_logit(place) > left_out;
+        if (stage == 0) whole = s.before[0] + kept;
+    }
+    return found;
+}
+
+// Rows whose border may lie behind the candidates. A function of its own, so that
+// its registers do not weigh on the others: the kernel with it inside spilled 77.
+template <bool F32>
+__device__ __noinline__ void sample_many(SampleArgs a, int r, int chunks, const Chunk* info, const uint64_t* steps, float top, float low, double all) {
+    extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+    RowShared& s = *(RowShared*)smem;
+    const void* row = (const uint8_t*)a.logits + (size_t)r * a.stride * (F32 ? 4 : 2);
+    const int V = a.V, t = threadIdx.x, lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(t / 64);
+    const Request q(a, r);
+    const double u = a.u[r];
+    const double zmax = top;
+    auto weight = [&](float x) __attribute__((always_inline)) { return weight_of(x, zmax, q.scale, s.two); };
+    auto mass = [&](float x) __attribute__((always_inline)) { return (uint64_t)__builtin_rint(weight(x) * ONE); };
+    uint64_t border = 0;
+    __syncthreads();
+    // ---- top_p alone, with many tokens: the chunks' weights by steps say in which
+    // step the border lies; that step's tokens, taken from the row, and 2048 equal
+    // parts of them, where. False where the step's tokens are too many, or min_p may
+    // have the border.
+    auto by_steps = [&](uint64_t& border) __attribute__((always_inline)) {
+        const int first = q.step(top);
+        each_chunk(chunks, [&](int c, bool in) __attribute__((always_inline)) {
+            if (wave || !in) return;
+            const Chunk k = info[c];
+            s.share[c] = k.sum > 0.0 ? exp_neg((double)k.top - zmax, q.scale, s.two) * (1.0 / ONE) : 0.0;
+            s.shift[c] = k.sum > 0.0 ? min(first - q.step(k.top), STEPS) : STEPS;
+            s.kept[c] = 0;
+        });
+        for (int i = t; i < BINS; i += ST) s.mass[i] = 0;
+        if (t == 0) s.n = 0, s.at[0] = -1;
+        __syncthreads();
+        // the row's steps (from its largest logit's on), up to the one that reaches `want`
+        const double want = q.top_p * all;
+        double own = 0.0, total;
+        if (t < STEPS)
+            for (int c0 = 0; c0 < chunks; c0 += 8) {             // (loads of eight chunks together)
+                uint64_t w[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int c = min(c0 + i, chunks - 1);
+                    w[i] = steps[(size_t)c * STEPS + max(t - s.shift[c], 0)];
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int c = min(c0 + i, chunks - 1);
+                    if (c0 + i < chunks && t >= s.shift[c]) own += s.share[c] * (double)w[i];
+                }
+            }
+        const double end = block_sums<ST>(own, total, s.s[10]), start = end - own;
+        if (own > 0.0 && start < want && want <= end) {          // (roundings could let two threads do it: the first one)
+            atomicMax(&s.at[0], STEPS - t);
+        }
+        __syncthreads();
+        const int b = STEPS - s.at[0];                           // (none: past the last one)
+        if (b >= STEPS) return false;
+        if (t == b) s.got[0] = start;
+        // each chunk's weight above that step
+        for (int c = wave; c < chunks; c += ST / 64) {
+            double w = 0.0;
+            for (int i = lane; i < b - s.shift[c]; i += 64) w += s.share[c] * (double)steps[(size_t)c * STEPS + i];
+            w = wave_all<Plus>(w);
+            if (lane == 0) s.above[c] = w;
+        }
+        // the step's tokens
+        uint64_t* tokens = s.list;                               // (and s.sorted behind it)
+        const int in_step = first - b;
+        constexpr int D = 8;                                     // loads in flight
+        for (int i = t * 4; i < V; i += D * ST * 4) {
+            float x[D][4];
+            load_fours<F32>(row, i, ST * 4, i - 4 * t, D * ST * 4, V, x);
+#pragma unroll
+            for (int d = 0; d < D; ++d)
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    if (q.step(x[d][v]) != in_step || x[d][v] == -INF) continue;
+                    const int at = atomicAdd(&s.n, 1);
+                    if (at < 2 * LIST) tokens[at] = place_of(x[d][v], i + d * ST * 4 + v);
+                }
+        }
+        __syncthreads();
+        const int n = s.n;
+        if (n > 2 * LIST) return false;
+        // their range, in parts; the part that reaches what is left of `want`
+        uint64_t hi = 0, lo = ~0ull;
+        for (int i = t; i < n; i += ST) {
+            hi = Most::of(hi, tokens[i]);
+            lo = Least::of(lo, tokens[i]);
+        }
+        hi = block_all<ST, Most>(hi, s.s[11]);
+        lo = block_all<ST, Least>(lo, s.s[12]);
+        const Parts<BINS> parts(place_logit(hi), place_logit(lo));
+        for (int i = t; i < n; i += ST) {
+            const float x = place_logit(tokens[i]);
+            atomicAdd((unsigned long long*)&s.mass[parts.of(x)], (unsigned long long)mass(x));
+        }
+        if (t == 0) s.n = 0, s.at[0] = -1;
+        __syncthreads();
+        const double left = __builtin_ceil((want - s.got[0]) * ONE);
+        const uint64_t rest = left < 1.0 ? 1 : (uint64_t)left;
+        constexpr int R = BINS / ST;
+        uint64_t mine = 0, whole;
+#pragma unroll
+        for (int i = 0; i < R; ++i) mine += s.mass[R * t + i];
+        const uint64_t ends = block_sums<ST>(mine, whole, s.s[13]);
+        const uint64_t need = Least::of(rest, whole);            // (roundings; whole > 0: the step has a weight)
+        if (ends - mine < need && need <= ends) {
+            uint64_t upto = ends - mine;
+            int i = R * t;
+            while (upto + s.mass[i] < need) upto += s.mass[i++];
+            s.at[0] = i;
+            s.before[0] = upto;
+        }
+        __syncthreads();
+        const int p = s.at[0];
+        if (p < 0) return false;
+        const uint64_t in_part = need - s.before[0];
+        // that part's tokens in order, as many as a wave holds; more where logits are equal
+        uint64_t* few = s.s[0];
+        constexpr int FEW = 64;
+        for (int i = t; i < n; i += ST)
+            if (parts.of(place_logit(tokens[i])) == p) {
+                const int at = atomicAdd(&s.n, 1);
+                if (at < FEW) few[at] = tokens[i];
+            }
+        __syncthreads();
+        const int m = s.n;
+        if (m <= FEW) {
+            const uint64_t e = lane < m ? few[lane] : 0;
+            const uint64_t w = lane < m ? mass(place_logit(e)) : 0;
+            uint64_t before = 0;
+            for (int i = 0; i < m; ++i) before += of_lane(e, i) > e ? of_lane(w, i) : 0;
+            border = wave_all<Least>(lane < m && (before < in_part || before == 0) ? e : ~0ull);
+        } else {
+            // equal logits (else: the row's): as many of the lowest ids as the mass takes
+            hi = 0, lo = ~0ull;
+            for (int i = t; i < n; i += ST) {
+                const uint64_t e = tokens[i];
+                if (parts.of(place_logit(e)) != p) continue;
+                hi = Most::of(hi, e);
+                lo = Least::of(lo, e);
+            }
+            hi = block_all<ST, Most>(hi, s.s[11]);
+            lo = block_all<ST, Least>(lo, s.s[12]);
+            if (hi >> 32 != lo >> 32) return false;
+            const uint64_t each_one = mass(place_logit(hi));
+            const int ties = each_one ? (int)Least::of((in_part + each_one - 1) / each_one, (uint64_t)m) : m;
+            const int width = (V + BINS - 1) / BINS;             // ids of a bin: 512 at most
+            for (int i = t; i < n; i += ST)
+                if (tokens[i] >> 32 == hi >> 32) atomicAdd(&s.cnt[place_id(tokens[i]) / width], 1u);
+            if (t == 0) s.n = 0;
+            __syncthreads();
+            uint32_t before;
+            const int bin = part_of_count<ST, BINS>(s.cnt, (uint32_t)ties, before, s.s[15], s.at);
+            uint64_t* same = s.mass;
+            for (int i = t; i < n; i += ST)
+                if (tokens[i] >> 32 == hi >> 32 && place_id(tokens[i]) / width == bin) same[atomicAdd(&s.n, 1)] = tokens[i];
+            __syncthreads();
+            const int k = s.n;
+            if (t < k) {
+                int rank = 0;
+                for (int i = 0; i < k; ++i) rank += same[i] > same[t];
+                if (rank == ties - (int)before - 1) s.before[1] = same[t];
+            }
+            __syncthreads();
+            border = s.before[1];
+        }
+        if (q.m_on && weight(place_logit(border)) < q.min_p) return false;
+        for (int i = t; i < n; i += ST)
+            if (tokens[i] >= border) atomicAdd((unsigned long long*)&s.kept[place_id(tokens[i]) / CHUNK], (unsigned long long)mass(place_logit(tokens[i])));
+        __syncthreads();
+        return true;
+    };
+
+    if (q.k == 0 && q.p_on && steps && by_steps(border)) {
+        auto kept = [&](int c, bool in) __attribute__((always_inline)) { return in ? s.above[c] + (double)s.kept[c] * (1.0 / ONE) : 0.0; };
+        double total = 0.0;
+        each_chunk(chunks, [&](int c, bool in) __attribute__((always_inline)) { total += wave_all<Plus>(kept(c, in)); });
+        return draw_by_chunks<F32>(a, r, row, chunks, kept, weight, total, border, s);
+    }
+
+    // ---- the row's logits (but those of 2^-46 of the largest weight and less)
+    __syncthreads();
+    for (int i = t; i < BINS; i += ST) {
+        s.cnt[i] = 0;
+        s.mass[i] = 0;
+    }
+    __syncthreads();
+    const float bottom = fmaxf(q.least(top, 1.0 / 70368744177664.0), low);
+    auto each = [&](auto f) __attribute__((always_inline)) {
+        constexpr int D = 4;                                     // loads in flight
+        for (int i = t * 4; i < V; i += D * ST * 4) {
+            float x[D][4];
+            load_fours<F32>(row, i, ST * 4, i - 4 * t, D * ST * 4, V, x);
+#pragma unroll
+            for (int d = 0; d < D; ++d)
+#pragma unroll
+                for (int v = 0; v < 4; ++v)
+                    if (x[d][v] >= bottom) f(x[d][v], i + d * ST * 4 + v);
+        }
+    };
+    border = 0;
+    if (q.k || q.p_on)
+        find_border<true>(q, top, bottom, 0.0, -INF, mass, each,
+                          [&](const Parts<BINS>& parts) __attribute__((always_inline)) {
+                              each([&](float x, int) __attribute__((always_inline)) {
+                                  const int b = parts.of(x);
+                                  if (q.k) atomicAdd(&s.cnt[b], 1u);
+                                  if (q.p_on) atomicAdd((unsigned long long*)&s.mass[b], (unsigned long long)mass(x));
+                              });
+                          },
+                          [&](uint32_t key, double ties) __attribute__((always_inline)) {
+                              draw<F32>(row, 0, V, [&](float x, int) __attribute__((always_inline)) { return x > -INF && logit_key(x) == key ? 1.0 : 0.0; },
+                                        [&](double sum) { return fmin(ties, sum) - 1.0; }, s);
+                          },
+                          border, s);
+    draw<F32>(row, 0, V, [&](float x, int id) __attribute__((always_inline)) {
+                  const double w = weight(x);
+                  return x >= bottom && place_of(x, id) >= border && w >= q.min_p ? w : 0.0;
+              }, [&](double sum) { return u * sum; }, s);
+    if (t == 0) {
+        a.ids[r] = s.hit[0];
+        if (a.p) a.p[r] = (float)(s.got[0] / s.got[1]);
+    }
+}
+
 // `listed`: the row's one chunk has left its candidates in s.list
 template <bool F32>
-__device__ __forceinline__ void sample_finish(const SampleArgs& a, int r, int chunks, int share, const Chunk* info, const uint64_t* lists, bool listed, RowShared& s) {
+__device__ __forceinline__ void sample_finish(const SampleArgs& a, int r, int chunks, int share, const Chunk* info, const uint64_t* lists, const uint64_t* steps,
+                                              bool listed, RowShared& s) {
     const void* row = (const uint8_t*)a.logits + (size_t)r * a.stride * (F32 ? 4 : 2);
     const int V = a.V, t = threadIdx.x, lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(t / 64);
     // candidates, four of a chunk in a row for each thread (memory behind the last one is the lists' own)
@@ -634,72 +1115,7 @@ __device__ __forceinline__ void sample_finish(const SampleArgs& a, int r, int ch
         return info[c].sum * exp_neg((double)info[c].top - zmax, q.scale, s.two);
     };
     if (q.k == 0 && (q.p_on || pure)) each_chunk(chunks, [&](int c, bool in) __attribute__((always_inline)) { all += wave_all<Plus>(scaled(c, in)); });
-    if (pure) {
-        // no filter: the chunk that the aim falls into (past the sum: the last with a weight), read again
-        const double aim = u * all;
-        double sum = 0.0, before = 0.0;
-        int at = -1;
-        each_chunk(chunks, [&](int c, bool in) __attribute__((always_inline)) {
-            const double w = scaled(c, in), end = sum + wave_scan<Plus>(w);
-            const uint64_t some = __ballot(w > 0.0), hit = some & __ballot(end > aim);
-            if (at < 0 || !(sum > aim)) {
-                const int l = hit ? __ffsll((long long)hit) - 1 : some ? 63 - __clzll((long long)some) : -1;
-                if (l >= 0) {
-                    at = c - lane + l;
-                    before = l ? of_lane(end, l - 1) : sum;
-                }
-            }
-            sum = of_lane(end, 63);
-        });
-        constexpr int NV = CHUNK / (4 * ST);
-        const int id0 = at * CHUNK;
-        float x[NV][4];
-        load_fours<F32>(row, id0 + 4 * t, 4 * ST, id0, CHUNK, V, x);
-        // sums up to and with each lane's four, of each [vector][wave]
-        double w[NV][4], ends[NV];
-#pragma unroll
-        for (int g = 0; g < NV; ++g) {
-            double own = 0.0;
-#pragma unroll
-            for (int v = 0; v < 4; ++v) w[g][v] = 0.0;
-            if (__ballot(x[g][0] > -INF || x[g][1] > -INF || x[g][2] > -INF || x[g][3] > -INF)) {
-#pragma unroll
-                for (int v = 0; v < 4; ++v) own += w[g][v] = weight(x[g][v]);
-            }
-            ends[g] = wave_scan<Plus>(own);
-            if (lane == 63) ((double*)s.s[4])[g * (ST / 64) + wave] = ends[g];
-            ends[g] -= own;
-        }
-        __syncthreads();
-        static_assert(NV * (ST / 64) == 16, "a lane each");
-        const double part = ((const double*)s.s[4])[lane & 15], upto = before + wave_scan<Plus>(lane < 16 ? part : 0.0);
-        int first = 0x7FFFFFFF, last = -1;
-        double pf = 0.0, pl = 0.0;
-#pragma unroll
-        for (int g = 0; g < NV; ++g) {
-            const int i = g * (ST / 64) + wave;
-            double y = (i ? of_lane(upto, i - 1) : before) + ends[g];
-#pragma unroll
-            for (int v = 0; v < 4; ++v) {
-                const int id = 4 * (g * ST + t) + v;
-                y += w[g][v];
-                if (w[g][v] > 0.0) {
-                    last = id;
-                    pl = w[g][v];
-                    if (y > aim && id < first) {
-                        first = id;
-                        pf = w[g][v];
-                    }
-                }
-            }
-        }
-        const int chosen = choose(first, last, s);
-        if (chosen == first || (chosen == last && first == 0x7FFFFFFF)) {            // (the token's thread)
-            a.ids[r] = id0 + chosen;
-            if (a.p) a.p[r] = (float)((chosen == first ? pf : pl) / all);
-        }
-        return;
-    }
+    if (pure) return draw_by_chunks<F32>(a, r, row, chunks, scaled, weight, all, 0, s);          // no filter
 
     // ---- few candidates
     const float least = q.floor(top, all, V), floor = fmaxf(least, low);
@@ -771,192 +1187,32 @@ __device__ __forceinline__ void sample_finish(const SampleArgs& a, int r, int ch
         const int l = hit ? __ffsll((long long)hit) - 1 : 63 - __clzll((long long)some);
         return give(place_id(of_lane(mine, l)), of_lane(w, l) / total);
     }
-    // ---- the border, among the candidates; where it may lie behind one that was
-    // left out, among the row's logits (but those of 2^-46 of the largest weight and less)
-    uint64_t border = 0;                                         // the last kept place (before min_p)
-    const float bottom = fmaxf(q.least(top, 1.0 / 70368744177664.0), low);
-    bool many = false;
-    for (;;) {
-        const float from = many ? bottom : floor, left_out = many || !(cut >= least) ? -INF : cut;
-        const Parts<BINS> parts(top, from);
-        auto each = [&](auto f) __attribute__((always_inline)) {
-            if (!many) {
-                candidates(f);
-                return;
-            }
-            constexpr int D = 4;                                 // loads in flight
-            for (int i = t * 4; i < V; i += D * ST * 4) {
-                float x[D][4];
-                load_fours<F32>(row, i, ST * 4, i - 4 * t, D * ST * 4, V, x);
-#pragma unroll
-                for (int d = 0; d < D; ++d)
-#pragma unroll
-                    for (int v = 0; v < 4; ++v)
-                        if (x[d][v] >= from) f(x[d][v], i + d * ST * 4 + v);
-            }
-        };
-        // counts and masses of the parts
-        const bool both = q.p_on;
-        if (q.k || both) {
-            each([&](float x, int) __attribute__((always_inline)) {
-                const int b = parts.of(x);
-                if (q.k) atomicAdd(&s.cnt[b], 1u);
-                if (both) atomicAdd((unsigned long long*)&s.mass[b], (unsigned long long)mass(x));
-            });
-        }
-        __syncthreads();
-        constexpr int R = BINS / ST;
-        uint64_t own = 0, ends = 0, whole = 0;                   // masses of this thread's parts, up to and with them, of all
-        if (both) {
-#pragma unroll
-            for (int i = 0; i < R; ++i) own += s.mass[R * t + i];
-            ends = block_sums<ST>(own, whole, s.s[5]);
-            if (q.k == 0 && !many) whole = (uint64_t)__builtin_ceil(all * ONE);
-        }
-        bool found = q.k || both || !(left_out > -INF);
-        for (int stage = 0; stage < 2 && found; ++stage) {       // top_k, then top_p
-            if (stage == 0 ? !q.k : !both) continue;
-            // The part, and what lies before it: tokens; masses.
-            int b = -1;
-            uint64_t want;
-            if (stage == 0) {
-                uint32_t before;
-                b = part_of_count<ST, BINS>(s.cnt, (uint32_t)q.k, before, s.s[6], s.at);
-                want = q.k - before;
-                if (b >= 0 && t == b / R) {
-                    uint64_t x = ends - own;
-                    for (int i = R * t; i < b; ++i) x += s.mass[i];
-                    s.before[0] = x;
+    // ---- the border, among the candidates
+    uint64_t border;                                             // the last kept place (before min_p)
+    const float left_out = cut >= least ? cut : -INF;
+    const bool sure = find_border<false>(q, top, floor, q.k == 0 ? all : 0.0, left_out, mass, candidates,
+                                         [&](const Parts<BINS>& parts) __attribute__((always_inline)) {
+                uint64_t w[RUN];                                     // (all of a thread's before its branches)
+                bool any = false;
+    #pragma unroll
+                for (int v = 0; v < RUN; ++v) {
+                    w[v] = 0;
+                    any |= in[v];
                 }
-            } else {
-                const double share_of = __builtin_ceil(q.top_p * (double)whole);
-                want = share_of < 1.0 ? 1 : (uint64_t)share_of;
-                __syncthreads();
-                if (t == 0) s.at[0] = -1;
-                __syncthreads();
-                if (ends - own < want && want <= ends) {
-                    uint64_t start = ends - own;
-                    int i = R * t;
-                    while (start + s.mass[i] < want) start += s.mass[i++];
-                    s.at[0] = i;
-                    s.before[1] = start;
+                if (q.p_on && __ballot(any)) {
+    #pragma unroll
+                    for (int v = 0; v < RUN; ++v) w[v] = mass(in[v] ? place_logit(e[v]) : top);
                 }
-                __syncthreads();
-                b = s.at[0];
-                if (b >= 0) want -= s.before[1];
-            }
-            if (b < 0) {                                         // never reached: all of them, or candidates left out
-                found = !(left_out > -INF);
-                continue;
-            }
-            // In that part: the last token that lies before `want` tokens (the last
-            // one whose masses before it stay below `want`; the first one always),
-            // and the mass up to and with it.
-            uint64_t place, kept;
-            if (t == 0) s.n = 0;
-            __syncthreads();
-            each([&](float x, int id) __attribute__((always_inline)) {
-                if (parts.of(x) == b) {
-                    const int at = atomicAdd(&s.n, 1);
-                    if (at < LIST) s.sorted[at] = place_of(x, id);
-                }
-            });
-            __syncthreads();
-            const int m = s.n;
-            if (m <= 64) {                                       // every wave for itself: each token against all
-                const uint64_t mine = lane < m ? s.sorted[lane] : 0;
-                const uint64_t w = lane < m ? mass(place_logit(mine)) : 0;
-                uint64_t before = 0;
-                for (int i = 0; i < m; ++i) {
-                    const uint64_t wo = stage ? of_lane(w, i) : 1;
-                    before += of_lane(mine, i) > mine ? wo : 0;
-                }
-                const bool in = lane < m && (before < want || before == 0);      // (the first, and others behind masses of zero)
-                kept = wave_all<Plus>(in ? w : 0);
-                place = wave_all<Least>(in ? mine : ~0ull);
-            } else if (m <= LIST) {
-                sort_places(s.sorted, m);
-                uint64_t w[RUN], sum = 0, all_of;
-#pragma unroll
-                for (int i = 0; i < RUN; ++i) {
-                    w[i] = RUN * t + i < m ? mass(place_logit(s.sorted[RUN * t + i])) : 0;
-                    sum += w[i];
-                }
-                uint64_t before = block_sums<ST>(sum, all_of, s.s[1]) - sum, in = 0;
-                int keep = 0;
-#pragma unroll
-                for (int i = 0; i < RUN; ++i) {
-                    const int at = RUN * t + i;
-                    if (at < m && ((stage ? before : (uint64_t)at) < want || at == 0)) {
-                        keep = at + 1;
-                        in += w[i];
+    #pragma unroll
+                for (int v = 0; v < RUN; ++v)
+                    if (in[v]) {
+                        const int b = parts.of(place_logit(e[v]));
+                        if (q.k) atomicAdd(&s.cnt[b], 1u);
+                        if (q.p_on) atomicAdd((unsigned long long*)&s.mass[b], (unsigned long long)w[v]);
                     }
-                    before += w[i];
-                }
-                keep = block_all<ST, Most>(keep, s.s[2]);
-                kept = block_all<ST, Plus>(in, s.s[3]);
-                place = s.sorted[keep - 1];
-            } else {
-                // more than can be sorted (the row's logits, then): halve the range of keys until one is left
-                uint32_t lo = ~0u, hi = 0;
-                each([&](float x, int) __attribute__((always_inline)) {
-                    if (parts.of(x) == b) {
-                        lo = min(lo, logit_key(x));
-                        hi = max(hi, logit_key(x));
-                    }
-                });
-                lo = block_all<ST, Least>(lo, s.s[1]);
-                hi = block_all<ST, Most>(hi, s.s[2]);
-                // the smallest key with less than `want` above it; last of all what lies above that, and its mass
-                uint64_t above, above_mass;
-                if (want == 0) want = 1;
-                for (bool last = false;;) {
-                    last = lo >= hi;
-                    const uint32_t mid = last ? lo : lo + (hi - lo) / 2;
-                    uint64_t n_above = 0, m_above = 0;
-                    each([&](float x, int) __attribute__((always_inline)) {
-                        if (parts.of(x) == b && logit_key(x) > mid) {
-                            ++n_above;
-                            m_above += mass(x);
-                        }
-                    });
-                    __syncthreads();
-                    above = block_all<ST, Plus>(n_above, s.s[3]);
-                    above_mass = block_all<ST, Plus>(m_above, s.s[4]);
-                    if (last) break;
-                    if ((stage ? above_mass : above) < want) hi = mid;
-                    else lo = mid + 1;
-                }
-                // of the tokens with that key the first by id
-                const uint32_t key = lo;
-                const uint64_t each_one = mass(key_logit(key)), left = want - (stage ? above_mass : above);
-                const double ties = !stage ? (double)left : each_one ? (double)((left + each_one - 1) / each_one) : (double)V;
-                draw<F32>(row, 0, V, [&](float x, int) __attribute__((always_inline)) { return x > -INF && logit_key(x) == key ? 1.0 : 0.0; },
-                          [&](double sum) { return fmin(ties, sum) - 1.0; }, s);
-                kept = above_mass + (uint64_t)fmin(ties, s.got[1]) * each_one;
-                place = (uint64_t)key << 32 | (uint32_t)~s.hit[0];
-            }
-            border = Most::of(border, place);
-            found = place_logit(place) > left_out;
-            if (stage == 0) whole = s.before[0] + kept;
-        }
-        if (found) break;
-        many = true;
-        border = 0;
-        __syncthreads();
-        for (int i = t; i < BINS; i += ST) {
-            s.cnt[i] = 0;
-            s.mass[i] = 0;
-        }
-        __syncthreads();
-    }
-    if (many) {
-        draw<F32>(row, 0, V, [&](float x, int id) __attribute__((always_inline)) {
-                      const double w = weight(x);
-                      return x >= bottom && place_of(x, id) >= border && w >= q.min_p ? w : 0.0;
-                  }, [&](double sum) { return u * sum; }, s);
-        return give(s.hit[0], s.got[0] / s.got[1]);
-    }
+            },
+            [](uint32_t, double) {}, border, s);
+    if (!sure) return sample_many<F32>(a, r, chunks, info, steps, top, low, all);
     // the draw by id: a run of the list for each thread
     __syncthreads();
     const int run = (n + ST - 1) / ST, i0 = min(t * run, n), i1 = min(i0 + run, n);
@@ -985,19 +1241,21 @@ __device__ __forceinline__ void sample_finish(const SampleArgs& a, int r, int ch
 
 constexpr int CHUNK_THREADS = 256;
 template <bool F32>
-__global__ void __launch_bounds__(CHUNK_THREADS) sample_chunk_kernel(SampleArgs a, int chunks, int share, Chunk* info, uint64_t* lists) {
+__global__ void __launch_bounds__(CHUNK_THREADS) sample_chunk_kernel(SampleArgs a, int chunks, int share, Chunk* info, uint64_t* lists, uint64_t* steps) {
     __shared__ ChunkShared s;
     const long long n = (long long)a.B * chunks;
     for (long long i = blockIdx.x; i < n; i += gridDim.x) {
-        sample_chunk<F32, CHUNK_THREADS, CHUNK / CHUNK_THREADS>(a, (int)(i / chunks), (int)(i % chunks), share, info + i, lists + i * share, s);
+        sample_chunk<F32, CHUNK_THREADS, CHUNK / CHUNK_THREADS>(a, (int)(i / chunks), (int)(i % chunks), share, info + i, lists + i * share,
+                                                               steps + i * STEPS, s);
         __syncthreads();
     }
 }
 template <bool F32>
-__global__ void __launch_bounds__(ST) sample_finish_kernel(SampleArgs a, int chunks, int share, const Chunk* info, const uint64_t* lists) {
+__global__ void __launch_bounds__(ST) sample_finish_kernel(SampleArgs a, int chunks, int share, const Chunk* info, const uint64_t* lists,
+                                                           const uint64_t* steps) {
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
     const size_t i = (size_t)blockIdx.x * chunks;
-    sample_finish<F32>(a, blockIdx.x, chunks, share, info + i, lists + i * share, false, *(RowShared*)smem);
+    sample_finish<F32>(a, blockIdx.x, chunks, share, info + i, lists + i * share, steps + i * STEPS, false, *(RowShared*)smem);
 }
 // rows of one chunk
 struct OneShared {
@@ -1009,9 +1267,9 @@ template <bool F32>
 __global__ void __launch_bounds__(ST) sample_row_kernel(SampleArgs a) {
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
     OneShared& s = *(OneShared*)smem;
-    sample_chunk<F32, ST, CHUNK / ST>(a, blockIdx.x, 0, LIST, &s.info, s.row.list, s.chunk);
+    sample_chunk<F32, ST, CHUNK / ST>(a, blockIdx.x, 0, LIST, &s.info, s.row.list, nullptr, s.chunk);
     __syncthreads();
-    sample_finish<F32>(a, blockIdx.x, 1, LIST, &s.info, nullptr, true, s.row);
+    sample_finish<F32>(a, blockIdx.x, 1, LIST, &s.info, nullptr, nullptr, true, s.row);
 }
 
 static int chunks_of(int V) { return (V + CHUNK - 1) / CHUNK; }
@@ -1020,7 +1278,7 @@ static size_t info_bytes(int B, int V) { return ((size_t)B * chunks_of(V) * size
 size_t sample_workspace_bytes(int B, int V) {
     const int chunks = chunks_of(V);
     if (chunks == 1) return 0;
-    return info_bytes(B, V) + (size_t)B * chunks * share_of(chunks) * 8;
+    return info_bytes(B, V) + (size_t)B * chunks * (share_of(chunks) + STEPS) * 8;
 }
 
 template <bool F32>
@@ -1028,6 +1286,7 @@ static hipError_t launch(const SampleArgs& a, void* ws, hipStream_t stream) {
     const int chunks = chunks_of(a.V), share = share_of(chunks);
     Chunk* info = (Chunk*)ws;
     uint64_t* lists = (uint64_t*)((uint8_t*)ws + info_bytes(a.B, a.V));
+    uint64_t* steps = lists + (size_t)a.B * chunks * share;
     static_assert(sizeof(OneShared) <= 163840, "LDS");
     int dev = 0;
     hipError_t e = hipGetDevice(&dev);
@@ -1042,10 +1301,10 @@ static hipError_t launch(const SampleArgs& a, void* ws, hipStream_t stream) {
     if (e != hipSuccess) return e;
     const long long n = (long long)a.B * chunks;
     e = launch_kernel(K_SAMPLE, stream, sample_chunk_kernel<F32>, dim3((unsigned)(n < (1 << 20) ? n : 1 << 20)), dim3(CHUNK_THREADS), 0, a,
-                      chunks, share, info, lists);
+                      chunks, share, info, lists, steps);
     if (e != hipSuccess) return e;
     return launch_kernel(K_SAMPLE, stream, sample_finish_kernel<F32>, dim3((unsigned)a.B), dim3(ST), sizeof(RowShared), a, chunks, share,
-                         (const Chunk*)info, (const uint64_t*)lists);
+                         (const Chunk*)info, (const uint64_t*)lists, (const uint64_t*)steps);
 }
 hipError_t launch_sample(const SampleArgs& a, bool f32, void* ws, hipStream_t stream) {
     return f32 ? launch<true>(a, ws, stream) : launch<false>(a, ws, stream);

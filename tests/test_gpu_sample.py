@@ -106,7 +106,7 @@ def test_many_kept_tokens(gpu, V, bf16):
     l[4:8] = -np.sort(-l[4:8], axis=1)
     l[8:] = np.where(r.random((4, V)) < 0.9, np.array([-1e4, -65504.0, -3e38, -30.0])[:, None], l[8:])
     l = torch.from_numpy(l.astype(np.float32)).to(torch.bfloat16 if bf16 else torch.float32)
-    for k, pp, mp in ((2000, None, None), (5000, 0.9, None), (V - 7, 0.5, 0.001), (0, 0.99, None), (0, 0.3, None), (300, None, None), (0, None, 1e-4),
+    for k, pp, mp in ((2000, None, None), (5000, 0.9, None), (0, 0.9, None), (0, 0.97, 1e-6), (0, 0.8, 0.02), (0, 0.9999, None), (V - 7, 0.5, 0.001), (0, 0.99, None), (0, 0.3, None), (300, None, None), (0, None, 1e-4),
                       (V + 5, None, None), (700, 0.999, None)):
         u = r.random(B).astype(np.float32)
         t = (0.2 + 2 * r.random(B)).astype(np.float32)
