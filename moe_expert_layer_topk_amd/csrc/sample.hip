@@ -678,7 +678,7 @@ __device__ __forceinline__ void draw_by_chunks(const SampleArgs& a, int r, const
 template <bool ALL, typename M, typename E, typename F, typename N>
 __device__ __forceinline__ bool find_border(const Request& q, float top, float from, double share_of, float left_out, M mass, E each, F fill, N nth,
                                             uint64_t& border, RowShared& s) {
-    const int t = threadIdx.x, lane = lane_id();
+    const int t = threadIdx.x, lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(t / 64);
     const Parts<BINS> parts(top, from);
     border = 0;
     // counts and masses of the parts
@@ -743,17 +743,26 @@ __device__ __forceinline__ bool find_border(const Request& q, float top, float f
         });
         __syncthreads();
         const int m = s.n;
-        if (m <= 64) {                                       // every wave for itself: each token against all
-            const uint64_t mine = lane < m ? s.sorted[lane] : 0;
-            const uint64_t w = lane < m ? mass(place_logit(mine)) : 0;
-            uint64_t before = 0;
-            for (int i = 0; i < m; ++i) {
-                const uint64_t wo = stage ? of_lane(w, i) : 1;
-                before += of_lane(mine, i) > mine ? wo : 0;
+        if (m <= 64) {                                           // one wave: each token against all
+            if (wave == 0) {
+                const uint64_t mine = lane < m ? s.sorted[lane] : 0;
+                const uint64_t w = lane < m ? mass(place_logit(mine)) : 0;
+                uint64_t before = 0;
+                for (int i = 0; i < m; ++i) {
+                    const uint64_t wo = stage ? of_lane(w, i) : 1;
+                    before += of_lane(mine, i) > mine ? wo : 0;
+                }
+                const bool in = lane < m && (before < want || before == 0);      // (the first, and others behind masses of zero)
+                kept = wave_all<Plus>(in ? w : 0);
+                place = wave_all<Least>(in ? mine : ~0ull);
+                if (lane == 0) {
+                    s.s[1][0] = kept;
+                    s.s[1][1] = place;
+                }
             }
-            const bool in = lane < m && (before < want || before == 0);      // (the first, and others behind masses of zero)
-            kept = wave_all<Plus>(in ? w : 0);
-            place = wave_all<Least>(in ? mine : ~0ull);
+            __syncthreads();
+            kept = s.s[1][0];
+            place = s.s[1][1];
         } else if (m <= LIST) {
             sort_places(s.sorted, m);
             uint64_t w[RUN], sum = 0, all_of;
@@ -890,18 +899,28 @@ __device__ __noinline__ void sample_many(SampleArgs a, int r, int chunks, const 
         // the step's tokens
         uint64_t* tokens = s.list;                               // (and s.sorted behind it)
         const int in_step = first - b;
-        constexpr int D = 8;                                     // loads in flight
-        for (int i = t * 4; i < V; i += D * ST * 4) {
+        constexpr int D = 8;                                     // loads in flight; one addition for a wave's tokens of them
+        for (int base = 0; base < V; base += D * ST * 4) {
             float x[D][4];
-            load_fours<F32>(row, i, ST * 4, i - 4 * t, D * ST * 4, V, x);
+            load_fours<F32>(row, base + 4 * t, ST * 4, base, D * ST * 4, V, x);
+            uint32_t mine = 0;
 #pragma unroll
             for (int d = 0; d < D; ++d)
 #pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    if (q.step(x[d][v]) != in_step || x[d][v] == -INF) continue;
-                    const int at = atomicAdd(&s.n, 1);
-                    if (at < 2 * LIST) tokens[at] = place_of(x[d][v], i + d * ST * 4 + v);
-                }
+                for (int v = 0; v < 4; ++v) mine |= (uint32_t)(q.step(x[d][v]) == in_step && x[d][v] > -INF) << (4 * d + v);
+            const int count = __popc(mine), upto = wave_scan<Plus>(count), all_of = of_lane(upto, 63);
+            if (all_of == 0) continue;
+            int at = 0;
+            if (lane == 0) at = atomicAdd(&s.n, all_of);
+            at = of_lane(at, 0) + upto - count;
+#pragma unroll
+            for (int d = 0; d < D; ++d)
+#pragma unroll
+                for (int v = 0; v < 4; ++v)
+                    if (mine >> (4 * d + v) & 1) {
+                        if (at < 2 * LIST) tokens[at] = place_of(x[d][v], base + 4 * t + d * ST * 4 + v);
+                        ++at;
+                    }
         }
         __syncthreads();
         const int n = s.n;
@@ -1119,6 +1138,7 @@ __device__ __forceinline__ void sample_finish(const SampleArgs& a, int r, int ch
 
     // ---- few candidates
     const float least = q.floor(top, all, V), floor = fmaxf(least, low);
+    float from = floor;                                          // (about) the least candidate
     bool in[RUN];
     int n;
     // those that f(i) names of the thread's, into s.list in the order of their ids (barriers before and behind)
@@ -1164,6 +1184,7 @@ __device__ __forceinline__ void sample_finish(const SampleArgs& a, int r, int ch
         uint32_t before;
         const int last = part_of_count<ST, BINS>(s.cnt, (uint32_t)q.k, before, s.s[10], s.at);
         collect([&](int v) __attribute__((always_inline)) { return in[v] && parts.of(place_logit(e[v])) <= last; });
+        from = fmaxf(floor, top - (float)(last + 1) / parts.scale);
         for (int i = t; i < BINS; i += ST) s.cnt[i] = 0;
     }
     __syncthreads();
@@ -1190,7 +1211,7 @@ __device__ __forceinline__ void sample_finish(const SampleArgs& a, int r, int ch
     // ---- the border, among the candidates
     uint64_t border;                                             // the last kept place (before min_p)
     const float left_out = cut >= least ? cut : -INF;
-    const bool sure = find_border<false>(q, top, floor, q.k == 0 ? all : 0.0, left_out, mass, candidates,
+    const bool sure = find_border<false>(q, top, from, q.k == 0 ? all : 0.0, left_out, mass, candidates,
                                          [&](const Parts<BINS>& parts) __attribute__((always_inline)) {
                 uint64_t w[RUN];                                     // (all of a thread's before its branches)
                 bool any = false;
