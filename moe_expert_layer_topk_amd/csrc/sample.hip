@@ -77,7 +77,9 @@ __device__ const double g_two[32] = {
 // far below 2^-1022. `two`: the table in LDS (32 entries, 64 banks), where it saves
 // six of the eleven steps that a whole power of two would leave to the polynomial.
 __device__ __forceinline__ double exp_neg(double d, double scale, const double* two) {
-    const double y = d * scale, n = __builtin_rint(y);
+    // (bounded first: y - n of an unbounded product may be contracted to what the product's
+    // rounding left, 1e70 and more, and r^5 of that to infinity)
+    const double y = fmax(d * scale, -40000.0), n = __builtin_rint(y);
     const double r = (y - n) * 0.0216608493924982909;            // ln 2 / 32
     double f = 1.0 / 120.0;
     f = __builtin_fma(f, r, 1.0 / 24.0);
@@ -85,7 +87,7 @@ __device__ __forceinline__ double exp_neg(double d, double scale, const double* 
     f = __builtin_fma(f, r, 0.5);
     f = __builtin_fma(f, r, 1.0);
     f = __builtin_fma(f, r, 1.0);
-    const int e = (int)fmax(n, -40000.0);
+    const int e = (int)n;
     return __builtin_ldexp(f * two[e & 31], e >> 5);
 }
 
@@ -374,7 +376,7 @@ __device__ __forceinline__ void sample_chunk(const SampleArgs& a, int r, int c, 
                 double w[4];
 #pragma unroll
                 for (int v = 0; v < 4; ++v) sum += w[v] = weight_of(x[j][v], top, q.scale, s.two);
-                if (q.p_on) {
+                if (q.p_on && steps) {
 #pragma unroll
                     for (int v = 0; v < 4; ++v) {
                         const int i = first - q.step(x[j][v]);
@@ -602,7 +604,7 @@ __device__ __forceinline__ void draw_by_chunks(const SampleArgs& a, int r, const
                                                RowShared& s) {
     const int V = a.V, t = threadIdx.x, lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(t / 64);
     const double u = a.u[r];
-        const double aim = u * total;
+    const double aim = u * total;
     double sum = 0.0, before = 0.0;
     int at = -1;
     each_chunk(chunks, [&](int c, bool in) __attribute__((always_inline)) {
@@ -618,7 +620,7 @@ __device__ __forceinline__ void draw_by_chunks(const SampleArgs& a, int r, const
         sum = of_lane(end, 63);
     });
     constexpr int NV = CHUNK / (4 * ST);
-    const int id0 = at * CHUNK;
+    const int id0 = max(at, 0) * CHUNK;                          // (there is a weight: the largest logit's is 1)
     float x[NV][4];
     load_fours<F32>(row, id0 + 4 * t, 4 * ST, id0, CHUNK, V, x);
     // sums up to each lane's four, of each [vector][wave]
@@ -1213,26 +1215,26 @@ __device__ __forceinline__ void sample_finish(const SampleArgs& a, int r, int ch
     const float left_out = cut >= least ? cut : -INF;
     const bool sure = find_border<false>(q, top, from, q.k == 0 ? all : 0.0, left_out, mass, candidates,
                                          [&](const Parts<BINS>& parts) __attribute__((always_inline)) {
-                uint64_t w[RUN];                                     // (all of a thread's before its branches)
-                bool any = false;
-    #pragma unroll
-                for (int v = 0; v < RUN; ++v) {
-                    w[v] = 0;
-                    any |= in[v];
-                }
-                if (q.p_on && __ballot(any)) {
-    #pragma unroll
-                    for (int v = 0; v < RUN; ++v) w[v] = mass(in[v] ? place_logit(e[v]) : top);
-                }
-    #pragma unroll
-                for (int v = 0; v < RUN; ++v)
-                    if (in[v]) {
-                        const int b = parts.of(place_logit(e[v]));
-                        if (q.k) atomicAdd(&s.cnt[b], 1u);
-                        if (q.p_on) atomicAdd((unsigned long long*)&s.mass[b], (unsigned long long)w[v]);
-                    }
-            },
-            [](uint32_t, double) {}, border, s);
+                                             uint64_t w[RUN];    // (all of a thread's before its branches)
+                                             bool any = false;
+#pragma unroll
+                                             for (int v = 0; v < RUN; ++v) {
+                                                 w[v] = 0;
+                                                 any |= in[v];
+                                             }
+                                             if (q.p_on && __ballot(any)) {
+#pragma unroll
+                                                 for (int v = 0; v < RUN; ++v) w[v] = mass(in[v] ? place_logit(e[v]) : top);
+                                             }
+#pragma unroll
+                                             for (int v = 0; v < RUN; ++v)
+                                                 if (in[v]) {
+                                                     const int b = parts.of(place_logit(e[v]));
+                                                     if (q.k) atomicAdd(&s.cnt[b], 1u);
+                                                     if (q.p_on) atomicAdd((unsigned long long*)&s.mass[b], (unsigned long long)w[v]);
+                                                 }
+                                         },
+                                         [](uint32_t, double) {}, border, s);
     if (!sure) return sample_many<F32>(a, r, chunks, info, steps, top, low, all);
     // the draw by id: a run of the list for each thread
     __syncthreads();
