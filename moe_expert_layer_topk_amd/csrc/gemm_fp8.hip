@@ -664,16 +664,13 @@ static hipError_t launch_split(const Fp8Args& p, int dev, int kid, hipStream_t s
                          dim3(64 * WK), SMEM, p, tm, tn);
 }
 
-#ifndef MOE_SHAPE
-#define MOE_SHAPE(picked) (picked)
-#endif
 template <bool GLU, bool F32>
 static hipError_t launch_any(const Fp8Args& p, int kid, hipStream_t stream) {
     int dev = 0;
     const hipError_t e = hipGetDevice(&dev);
     if (e != hipSuccess) return e;
     const long long cus = device_cus(dev), rows_b = (long long)p.N * (GLU ? 2 : 1);
-    const int shape = MOE_SHAPE(pick_shape(F32 ? kShapesFp8F32 : kShapesFp8, p.M, rows_b, p.K, cus));
+    const int shape = pick_shape(F32 ? kShapesFp8F32 : kShapesFp8, p.M, rows_b, p.K, cus);
     const bool few = shape_tiles(shape, p.M, rows_b) <= cus;             // at most one tile a CU
     if constexpr (!F32) {
         if (shape == S_256x256)
