@@ -91,12 +91,15 @@ __device__ __forceinline__ double exp_neg(double d, double scale, const double* 
     return __builtin_ldexp(f * two[e & 31], e >> 5);
 }
 
-// e^((x - top) inv), 0 for -inf. (Without a branch: in one for each element the
-// chains of a thread's elements wait for themselves; 16 of them 5600 -> 3100 clocks.)
+// e^((x - top) inv), 0 for -inf (below the bound, also times 0). (Without a branch: in
+// one for each element the chains of a thread's elements wait for themselves; 16 of
+// them 5600 -> 3100 clocks.)
 __device__ __forceinline__ double weight_of(float x, double top, double scale, const double* two) {
-    const bool none = x == -INF;
-    const double w = exp_neg(none ? 0.0 : (double)x - top, scale, two);
-    return none ? 0.0 : w;
+    return exp_neg((double)x - top, scale, two);
+}
+// a weight's mass: the nearest multiple of 2^-42, from where 2^52 + w 2^42 has its bits
+__device__ __forceinline__ uint64_t mass_of(double w) {
+    return __builtin_bit_cast(uint64_t, __builtin_fma(w, ONE, 4503599627370496.0)) & 0xFFFFFFFFFFFFFull;
 }
 
 // a row's parameters
@@ -178,46 +181,74 @@ __device__ __forceinline__ void load_fours(const void* row, int i, int step, int
 }
 
 // ---- over a wave by lane moves in the vector unit
-template <int CTRL, int ROWS, typename T>
+// (lanes that get nothing: `none`; ZERO: 0, which a move within rows gives by itself)
+template <int CTRL, int ROWS, bool ZERO, typename T>
 __device__ __forceinline__ T moved(T v, T none) {
+    constexpr bool FILL = ZERO && ROWS == 0xF;
     if constexpr (sizeof(T) == 4) {
-        return __builtin_bit_cast(T, __builtin_amdgcn_update_dpp(__builtin_bit_cast(int, none), __builtin_bit_cast(int, v), CTRL, ROWS, 0xF, false));
+        return __builtin_bit_cast(T, __builtin_amdgcn_update_dpp(__builtin_bit_cast(int, none), __builtin_bit_cast(int, v), CTRL, ROWS, 0xF, FILL));
     } else {
         const int2 a = __builtin_bit_cast(int2, v), b = __builtin_bit_cast(int2, none);
-        return __builtin_bit_cast(T, make_int2(__builtin_amdgcn_update_dpp(b.x, a.x, CTRL, ROWS, 0xF, false),
-                                               __builtin_amdgcn_update_dpp(b.y, a.y, CTRL, ROWS, 0xF, false)));
+        return __builtin_bit_cast(T, make_int2(__builtin_amdgcn_update_dpp(b.x, a.x, CTRL, ROWS, 0xF, FILL),
+                                               __builtin_amdgcn_update_dpp(b.y, a.y, CTRL, ROWS, 0xF, FILL)));
     }
 }
 struct Plus {
+    static constexpr bool ZERO = true;
     template <typename T>
     __device__ __forceinline__ static T of(T x, T y) { return x + y; }
     template <typename T>
     __device__ __forceinline__ static T none() { return (T)0; }
 };
 struct Most {
+    static constexpr bool ZERO = false;
     template <typename T>
     __device__ __forceinline__ static T of(T x, T y) { return x > y ? x : y; }
     template <typename T>
     __device__ __forceinline__ static T none() { return __is_same(T, float) ? (T)-INF : (T)(__is_same(T, int) ? -0x7FFFFFFF - 1 : 0); }
 };
 struct Least {
+    static constexpr bool ZERO = false;
     template <typename T>
     __device__ __forceinline__ static T of(T x, T y) { return x < y ? x : y; }
     template <typename T>
     __device__ __forceinline__ static T none() { return __is_same(T, float) ? (T)INF : __is_same(T, int) ? (T)0x7FFFFFFF : (T)~0ull; }
 };
-// over the lanes up to and with this one
-template <typename F, typename T>
+// over the lanes (ROW: the lanes of a row of 16) up to and with this one. Largest and
+// smallest floats in one instruction a step: a lane that gets nothing keeps its value.
+// (A lane move may read a register two wait states after it is written.)
+#define MOE_SCAN(OP, CTRL, ROWS) asm("s_nop 1\n\t" OP " %0, %0, %0 " CTRL " row_mask:" ROWS " bank_mask:0xf" : "+v"(v))
+template <typename F, bool ROW = false, typename T>
 __device__ __forceinline__ T wave_scan(T v) {
+    if constexpr (__is_same(T, float) && __is_same(F, Most)) {
+        MOE_SCAN("v_max_f32_dpp", "row_shr:1", "0xf");
+        MOE_SCAN("v_max_f32_dpp", "row_shr:2", "0xf");
+        MOE_SCAN("v_max_f32_dpp", "row_shr:4", "0xf");
+        MOE_SCAN("v_max_f32_dpp", "row_shr:8", "0xf");
+        if (!ROW) MOE_SCAN("v_max_f32_dpp", "row_bcast:15", "0xa");
+        if (!ROW) MOE_SCAN("v_max_f32_dpp", "row_bcast:31", "0xc");
+        return v;
+    }
+    if constexpr (__is_same(T, float) && __is_same(F, Least)) {
+        MOE_SCAN("v_min_f32_dpp", "row_shr:1", "0xf");
+        MOE_SCAN("v_min_f32_dpp", "row_shr:2", "0xf");
+        MOE_SCAN("v_min_f32_dpp", "row_shr:4", "0xf");
+        MOE_SCAN("v_min_f32_dpp", "row_shr:8", "0xf");
+        if (!ROW) MOE_SCAN("v_min_f32_dpp", "row_bcast:15", "0xa");
+        if (!ROW) MOE_SCAN("v_min_f32_dpp", "row_bcast:31", "0xc");
+        return v;
+    }
     const T none = F::template none<T>();
-    v = F::of(moved<0x111, 0xF>(v, none), v);                    // from 1, 2, 4, 8 lanes below in the row of 16
-    v = F::of(moved<0x112, 0xF>(v, none), v);
-    v = F::of(moved<0x114, 0xF>(v, none), v);
-    v = F::of(moved<0x118, 0xF>(v, none), v);
-    v = F::of(moved<0x142, 0xA>(v, none), v);                    // rows 0 and 2 into 1 and 3
-    v = F::of(moved<0x143, 0xC>(v, none), v);                    // the lower half's into the upper
+    v = F::of(moved<0x111, 0xF, F::ZERO>(v, none), v);           // from 1, 2, 4, 8 lanes below in the row of 16
+    v = F::of(moved<0x112, 0xF, F::ZERO>(v, none), v);
+    v = F::of(moved<0x114, 0xF, F::ZERO>(v, none), v);
+    v = F::of(moved<0x118, 0xF, F::ZERO>(v, none), v);
+    if (ROW) return v;
+    v = F::of(moved<0x142, 0xA, F::ZERO>(v, none), v);           // rows 0 and 2 into 1 and 3
+    v = F::of(moved<0x143, 0xC, F::ZERO>(v, none), v);           // the lower half's into the upper
     return v;
 }
+#undef MOE_SCAN
 template <typename T>
 __device__ __forceinline__ T of_lane(T v, int lane) {
     if constexpr (sizeof(T) == 4) return __builtin_bit_cast(T, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
@@ -231,13 +262,24 @@ __device__ __forceinline__ T wave_all(T v) { return of_lane(wave_scan<F>(v), 63)
 
 // ---- over a workgroup of NT threads. A value a wave goes through `s`, which no
 // call may use that is less than one barrier away.
+// `s` holds a value for each wave: those of all
+template <int NT, typename F, typename T>
+__device__ __forceinline__ T of_waves(const T* s) {
+    if constexpr (NT / 64 <= 4) {
+        T v = s[0];
+#pragma unroll
+        for (int i = 1; i < NT / 64; ++i) v = F::of(v, s[i]);
+        return v;
+    }
+    const int l = lane_id() & 15;
+    return of_lane(wave_scan<F, true>(l < NT / 64 ? s[l] : F::template none<T>()), 15);
+}
 template <int NT, typename F, typename T>
 __device__ __forceinline__ T block_all(T v, void* s) {
     v = wave_scan<F>(v);
     if (lane_id() == 63) ((T*)s)[threadIdx.x / 64] = v;
     __syncthreads();
-    const int l = lane_id() & 15;
-    return of_lane(wave_scan<F>(l < NT / 64 ? ((const T*)s)[l] : F::template none<T>()), 15);
+    return of_waves<NT, F>((const T*)s);
 }
 // sum over the threads up to and with this one; that of all
 template <int NT, typename T>
@@ -246,8 +288,19 @@ __device__ __forceinline__ T block_sums(T v, T& all, void* s) {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     if (lane_id() == 63) ((T*)s)[wave] = v;
     __syncthreads();
+    if constexpr (NT / 64 <= 4) {
+        T before = 0;
+        all = 0;
+#pragma unroll
+        for (int i = 0; i < NT / 64; ++i) {
+            const T w = ((const T*)s)[i];
+            if (i < wave) before += w;
+            all += w;
+        }
+        return before + v;
+    }
     const int l = lane_id() & 15;
-    const T w = wave_scan<Plus>(l < NT / 64 ? ((const T*)s)[l] : (T)0);
+    const T w = wave_scan<Plus, true>(l < NT / 64 ? ((const T*)s)[l] : (T)0);
     all = of_lane(w, 15);
     return wave ? of_lane(w, wave - 1) + v : v;
 }
@@ -302,15 +355,27 @@ __device__ __forceinline__ void sort_places(uint64_t* p, int n) {
     __syncthreads();
 }
 
+// (fmaxf first makes its operands quiet, one instruction each)
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+    return r;
+}
+__device__ __forceinline__ float min3(float a, float b, float c) {
+    float r;
+    asm("v_min3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+    return r;
+}
+
 // ------------------------------------------------------------------ a chunk
 constexpr int CHUNK_BINS = 1024;
 struct ChunkShared {
     double two[32];
     uint64_t mass[STEPS];
     uint32_t cnt[CHUNK_BINS];
-    uint64_t s[8][16];
+    uint64_t s[7][16];
     int at[2];
-    int part[4][16];
+    int part[16];
 };
 
 // NT threads with E logits each; `share`: how many candidates may be written
@@ -326,15 +391,28 @@ __device__ __forceinline__ void sample_chunk(const SampleArgs& a, int r, int c, 
     for (int i = t; i < CHUNK_BINS; i += NT) s.cnt[i] = 0;
     for (int i = t; i < STEPS; i += NT) s.mass[i] = 0;
     if (t < 32) s.two[t] = g_two[t];
+    const bool filter = q.k || q.p_on || q.m_on;
     float top = -INF, low = INF;
+    bool nan = false;
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
+    for (int j = 0; j < NV; ++j) {
+        top = max3(top, max3(x[j][0], x[j][1], x[j][2]), x[j][3]);
+        nan |= __builtin_isunordered(x[j][0], x[j][1]) || __builtin_isunordered(x[j][2], x[j][3]);
+    }
+    if (nan) top = INF;
+    const float mine_top = top;
+    if (filter) {
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-            const float y = x[j][v] == x[j][v] ? x[j][v] : INF;
-            top = fmaxf(top, y);
-            if (y > -INF) low = fminf(low, y);
+        for (int j = 0; j < NV; ++j) low = min3(low, min3(x[j][0], x[j][1], x[j][2]), x[j][3]);
+        if (__ballot(low == -INF)) {
+            low = INF;
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+#pragma unroll
+                for (int v = 0; v < 4; ++v)
+                    if (x[j][v] > -INF) low = fminf(low, x[j][v]);
         }
+    }
     {
         const float wt = wave_scan<Most>(top), wl = wave_scan<Least>(low);
         if (lane_id() == 63) {
@@ -342,9 +420,8 @@ __device__ __forceinline__ void sample_chunk(const SampleArgs& a, int r, int c, 
             ((float*)s.s[1])[wave] = wl;
         }
         __syncthreads();
-        const int l = lane_id() & 15;
-        top = of_lane(wave_scan<Most>(l < SW ? ((const float*)s.s[0])[l] : -INF), 15);
-        low = of_lane(wave_scan<Least>(l < SW ? ((const float*)s.s[1])[l] : INF), 15);
+        top = of_waves<NT, Most>((const float*)s.s[0]);
+        low = of_waves<NT, Least>((const float*)s.s[1]);
     }
     Chunk out{0.0, top, low, -INF, 0};
     if (q.bad || !(top < INF) || top == -INF) {
@@ -380,8 +457,7 @@ __device__ __forceinline__ void sample_chunk(const SampleArgs& a, int r, int c, 
 #pragma unroll
                     for (int v = 0; v < 4; ++v) {
                         const int i = first - q.step(x[j][v]);
-                        if (x[j][v] > -INF && i < STEPS)
-                            atomicAdd((unsigned long long*)&s.mass[i], (unsigned long long)__builtin_rint(w[v] * ONE));
+                        if (i < STEPS) atomicAdd((unsigned long long*)&s.mass[i], (unsigned long long)mass_of(w[v]));
                     }
                 }
             }
@@ -389,73 +465,84 @@ __device__ __forceinline__ void sample_chunk(const SampleArgs& a, int r, int c, 
         if (q.p_on && steps)
             for (int i = t; i < STEPS; i += NT) steps[i] = s.mass[i];
     }
-    if (q.k == 0 && !q.p_on && !q.m_on) {
+    if (!filter) {
         if (t == 0) *info = out;
         return;
     }
-    const float floor = fmaxf(q.floor(top, out.sum, V), low);
-    // Candidates: from `least` on. More than the share, or than a few times k:
-    // those of the parts up to the k-th (what is left out then is out), or of as
-    // many parts as fit the share.
-    auto count = [&](auto f) __attribute__((always_inline)) {
-        int n = 0;
+    float floor = fmaxf(q.floor(top, out.sum, V), low);
+    // top_k: k threads' largest logits are k tokens, so what lies below the k-th
+    // largest of these is out (about as much as below the k-th token, for a
+    // sixteenth of the additions that all tokens would take)
+    if (q.k && q.k <= NT / 2) {
+        const Parts<CHUNK_BINS> part(top, floor);
+        const int b = part.of(mine_top);
+        const bool one = mine_top >= floor;
+        if (one) atomicAdd(&s.cnt[b], 1u);
+        __syncthreads();
+        uint32_t before;
+        const int last = part_of_count<NT, CHUNK_BINS>(s.cnt, (uint32_t)q.k, before, s.s[4], s.at);
+        if (one) s.cnt[b] = 0;                                   // (counted again below; every thread has read)
+        if (last >= 0 && last < CHUNK_BINS - 1) {                // (the last part has all that lies lower, or all of a range too small for a scale)
+            const float d = (float)(last + 1) / part.scale;
+            floor = fmaxf(floor, top - d - (fabsf(top) + d) * 1e-6f);
+        }
+    }
+    // Candidates: from `floor` on, bit 4 j + v. In the order of their ids: [vector][wave][lane][element].
+    uint32_t mine = 0;
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
+    for (int j = 0; j < NV; ++j)
 #pragma unroll
-            for (int v = 0; v < 4; ++v) n += f(x[j][v]);
-        return n;
+        for (int v = 0; v < 4; ++v) mine |= (uint32_t)(x[j][v] >= floor) << (4 * j + v);
+    int at[NV], total;
+    auto places = [&]() __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < NV; j += 2) {                        // (counts of two vectors in one scan: 256 at most)
+            const uint32_t c = __popc(mine >> (4 * j) & 15) | (j + 1 < NV ? __popc(mine >> (4 * j + 4) & 15) << 16 : 0), e = wave_scan<Plus>(c);
+            at[j] = (e - c) & 0xFFFF;
+            if (lane_id() == 63) s.part[j * SW + wave] = e & 0xFFFF;
+            if (j + 1 < NV) {
+                at[j + 1 < NV ? j + 1 : 0] = (e - c) >> 16;
+                if (lane_id() == 63) s.part[(j + 1 < NV ? j + 1 : 0) * SW + wave] = e >> 16;
+            }
+        }
+        __syncthreads();
+        static_assert(NV * SW == 16, "a lane each");
+        const int end = wave_scan<Plus, true>(s.part[lane_id() & 15]);
+        total = of_lane(end, 15);
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int i = j * SW + wave;
+            at[j] += i ? of_lane(end, i - 1) : 0;
+        }
     };
-    const int all = block_all<NT, Plus>(count([&](float y) { return y >= floor; }), s.s[3]);
-    const Parts<CHUNK_BINS> part(top, floor);
-    int last = CHUNK_BINS;
-    if (all > share || (q.k && all > 2 * q.k + 64)) {
+    places();
+    // More than the share, or than a few times k: those of the parts up to the k-th
+    // (what is left out then is out), or of as many parts as fit the share.
+    if (total > share || (q.k && total > 2 * q.k + 64)) {
+        const Parts<CHUNK_BINS> part(top, floor);
 #pragma unroll
         for (int j = 0; j < NV; ++j)
 #pragma unroll
             for (int v = 0; v < 4; ++v)
-                if (x[j][v] >= floor) atomicAdd(&s.cnt[part.of(x[j][v])], 1u);
+                if (mine >> (4 * j + v) & 1) atomicAdd(&s.cnt[part.of(x[j][v])], 1u);
         __syncthreads();
         uint32_t before;
         const int want = q.k ? min(q.k, share) : share;
-        last = part_of_count<NT, CHUNK_BINS>(s.cnt, (uint32_t)want, before, s.s[4], s.at);
-        if (last < 0) last = CHUNK_BINS;
-        else {
+        int last = part_of_count<NT, CHUNK_BINS>(s.cnt, (uint32_t)want, before, s.s[6], s.at);
+        if (last >= 0) {
             const bool fits = (int)(before + s.cnt[last]) <= share;
             if (!fits) --last;
-            if (!fits || !q.k || q.k > share) {
-                float cut = -INF;
+            float cut = -INF;
 #pragma unroll
-                for (int j = 0; j < NV; ++j)
+            for (int j = 0; j < NV; ++j)
 #pragma unroll
-                    for (int v = 0; v < 4; ++v)
-                        if (x[j][v] >= floor && part.of(x[j][v]) > last) cut = fmaxf(cut, x[j][v]);
-                out.cut = block_all<NT, Most>(cut, s.s[5]);
-            }
-        }
-    }
-    // in the order of their ids: [vector][wave][lane][element]
-    auto in = [&](float y) __attribute__((always_inline)) { return y >= floor && part.of(y) <= last; };
-    int at[NV];
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        int before = 0, n = 0;
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-            const uint64_t b = __ballot(in(x[j][v]));
-            before += __popcll(b & lanemask_lt());
-            n += __popcll(b);
-        }
-        at[j] = before;
-        if (lane_id() == 0) s.part[j][wave] = n;
-    }
-    __syncthreads();
-    int total = 0;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-#pragma unroll
-        for (int w = 0; w < SW; ++w) {
-            if (w == wave) at[j] += total;
-            total += s.part[j][w];
+                for (int v = 0; v < 4; ++v)
+                    if ((mine >> (4 * j + v) & 1) && part.of(x[j][v]) > last) {
+                        cut = fmaxf(cut, x[j][v]);
+                        mine &= ~(1u << (4 * j + v));
+                    }
+            if (!fits || !q.k || q.k > share) out.cut = block_all<NT, Most>(cut, s.s[5]);
+            places();
         }
     }
 #pragma unroll
@@ -463,7 +550,7 @@ __device__ __forceinline__ void sample_chunk(const SampleArgs& a, int r, int c, 
         int to = at[j];
 #pragma unroll
         for (int v = 0; v < 4; ++v)
-            if (in(x[j][v])) list[to++] = place_of(x[j][v], c0 + (j * NT + t) * 4 + v);
+            if (mine >> (4 * j + v) & 1) list[to++] = place_of(x[j][v], c0 + (j * NT + t) * 4 + v);
     }
     out.n = total;
     if (t == 0) *info = out;
@@ -496,9 +583,8 @@ __device__ __forceinline__ int choose(int first, int last, RowShared& s) {
         ((int*)s.s[9])[wave] = last;
     }
     __syncthreads();
-    const int l = lane_id() & 15;
-    first = of_lane(wave_scan<Least>(l < ST / 64 ? ((const int*)s.s[8])[l] : 0x7FFFFFFF), 15);
-    last = of_lane(wave_scan<Most>(l < ST / 64 ? ((const int*)s.s[9])[l] : -1), 15);
+    first = of_waves<ST, Least>((const int*)s.s[8]);
+    last = of_waves<ST, Most>((const int*)s.s[9]);
     return first != 0x7FFFFFFF ? first : last;
 }
 
@@ -643,7 +729,7 @@ __device__ __forceinline__ void draw_by_chunks(const SampleArgs& a, int r, const
     }
     __syncthreads();
     static_assert(NV * (ST / 64) == 16, "a lane each");
-    const double part = ((const double*)s.s[4])[lane & 15], upto = before + wave_scan<Plus>(lane < 16 ? part : 0.0);
+    const double part = ((const double*)s.s[4])[lane & 15], upto = before + wave_scan<Plus, true>(part);
     int first = 0x7FFFFFFF, last = -1;
     double pf = 0.0, pl = 0.0;
 #pragma unroll
@@ -847,7 +933,7 @@ __device__ __noinline__ void sample_many(SampleArgs a, int r, int chunks, const 
     const double u = a.u[r];
     const double zmax = top;
     auto weight = [&](float x) __attribute__((always_inline)) { return weight_of(x, zmax, q.scale, s.two); };
-    auto mass = [&](float x) __attribute__((always_inline)) { return (uint64_t)__builtin_rint(weight(x) * ONE); };
+    auto mass = [&](float x) __attribute__((always_inline)) { return mass_of(weight(x)); };
     uint64_t border = 0;
     __syncthreads();
     // ---- top_p alone, with many tokens: the chunks' weights by steps say in which
@@ -1119,7 +1205,7 @@ __device__ __forceinline__ void sample_finish(const SampleArgs& a, int r, int ch
     if (q.bad || !(top < INF) || top == -INF) return give(-1, 0.0);
     const double zmax = top;
     auto weight = [&](float x) __attribute__((always_inline)) { return weight_of(x, zmax, q.scale, s.two); };
-    auto mass = [&](float x) __attribute__((always_inline)) { return (uint64_t)__builtin_rint(weight(x) * ONE); };
+    auto mass = [&](float x) __attribute__((always_inline)) { return mass_of(weight(x)); };
 
     if (q.k == 1) {
         uint64_t best = 0;
@@ -1161,7 +1247,7 @@ __device__ __forceinline__ void sample_finish(const SampleArgs& a, int r, int ch
         }
         __syncthreads();
         static_assert(RUN / 4 * (ST / 64) == 16, "a lane each");
-        const int end = wave_scan<Plus>(lane < 16 ? s.part[lane] : 0);
+        const int end = wave_scan<Plus, true>(s.part[lane & 15]);
         n = of_lane(end, 15);
 #pragma unroll
         for (int g = 0; g < RUN / 4; ++g) {
