@@ -953,22 +953,28 @@ __device__ __noinline__ void sample_many(SampleArgs a, int r, int chunks, const 
         if (t == 0) s.n = 0, s.at[0] = -1;
         __syncthreads();
         // the row's steps (from its largest logit's on), up to the one that reaches `want`
+        // (a fourth of the chunks a thread, eight loads together)
         const double want = q.top_p * all;
         double own = 0.0, total;
-        if (t < STEPS)
-            for (int c0 = 0; c0 < chunks; c0 += 8) {             // (loads of eight chunks together)
-                uint64_t w[8];
+        double* parts_of = (double*)s.sorted;
+        for (int c0 = t / STEPS; c0 < chunks; c0 += 32) {
+            uint64_t w[8];
+            const int i = t % STEPS;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int c = min(c0 + i, chunks - 1);
-                    w[i] = steps[(size_t)c * STEPS + max(t - s.shift[c], 0)];
-                }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int c = min(c0 + i, chunks - 1);
-                    if (c0 + i < chunks && t >= s.shift[c]) own += s.share[c] * (double)w[i];
-                }
+            for (int d = 0; d < 8; ++d) {
+                const int c = min(c0 + 4 * d, chunks - 1);
+                w[d] = steps[(size_t)c * STEPS + max(i - s.shift[c], 0)];
             }
+#pragma unroll
+            for (int d = 0; d < 8; ++d) {
+                const int c = min(c0 + 4 * d, chunks - 1);
+                if (c0 + 4 * d < chunks && i >= s.shift[c]) own += s.share[c] * (double)w[d];
+            }
+        }
+        static_assert(ST == 4 * STEPS, "a fourth of the chunks each");
+        parts_of[t] = own;
+        __syncthreads();
+        own = t < STEPS ? (parts_of[t] + parts_of[STEPS + t]) + (parts_of[2 * STEPS + t] + parts_of[3 * STEPS + t]) : 0.0;
         const double end = block_sums<ST>(own, total, s.s[10]), start = end - own;
         if (own > 0.0 && start < want && want <= end) {          // (roundings could let two threads do it: the first one)
             atomicMax(&s.at[0], STEPS - t);
@@ -977,16 +983,33 @@ __device__ __noinline__ void sample_many(SampleArgs a, int r, int chunks, const 
         const int b = STEPS - s.at[0];                           // (none: past the last one)
         if (b >= STEPS) return false;
         if (t == b) s.got[0] = start;
-        // each chunk's weight above that step
-        for (int c = wave; c < chunks; c += ST / 64) {
-            double w = 0.0;
-            for (int i = lane; i < b - s.shift[c]; i += 64) w += s.share[c] * (double)steps[(size_t)c * STEPS + i];
-            w = wave_all<Plus>(w);
-            if (lane == 0) s.above[c] = w;
+        const int in_step = first - b;
+        if (in_step <= -1000000000 || in_step >= 1000000000) return false;       // (step()'s bounds)
+        // each chunk's weight above that step: four of a lane's steps, of four chunks together
+        for (int c0 = wave; c0 < chunks; c0 += 4 * (ST / 64)) {
+            typedef uint64_t u64x2 __attribute__((ext_vector_type(2)));
+            u64x2 w[4][2];
+#pragma unroll
+            for (int d = 0; d < 4; ++d) {
+                const u64x2* at = (const u64x2*)(steps + (size_t)min(c0 + d * (ST / 64), chunks - 1) * STEPS + 4 * lane);
+                w[d][0] = at[0];
+                w[d][1] = at[1];
+            }
+#pragma unroll
+            for (int d = 0; d < 4; ++d) {
+                const int c = c0 + d * (ST / 64);
+                if (c >= chunks) break;
+                const int n = b - s.shift[c] - 4 * lane;
+                uint64_t sum = 0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sum += i < n ? w[d][i / 2][i % 2] : 0;
+                sum = wave_all<Plus>(sum);
+                if (lane == 0) s.above[c] = s.share[c] * (double)sum;
+            }
         }
         // the step's tokens
         uint64_t* tokens = s.list;                               // (and s.sorted behind it)
-        const int in_step = first - b;
+        const float slope = 8.f / q.temperature, in_this = (float)in_step;
         constexpr int D = 8;                                     // loads in flight; one addition for a wave's tokens of them
         for (int base = 0; base < V; base += D * ST * 4) {
             float x[D][4];
@@ -995,7 +1018,7 @@ __device__ __noinline__ void sample_many(SampleArgs a, int r, int chunks, const 
 #pragma unroll
             for (int d = 0; d < D; ++d)
 #pragma unroll
-                for (int v = 0; v < 4; ++v) mine |= (uint32_t)(q.step(x[d][v]) == in_step && x[d][v] > -INF) << (4 * d + v);
+                for (int v = 0; v < 4; ++v) mine |= (uint32_t)(floorf(x[d][v] * slope) == in_this) << (4 * d + v);   // (step(), within its bounds)
             const int count = __popc(mine), upto = wave_scan<Plus>(count), all_of = of_lane(upto, 63);
             if (all_of == 0) continue;
             int at = 0;
@@ -1350,7 +1373,7 @@ __device__ __forceinline__ void sample_finish(const SampleArgs& a, int r, int ch
 
 constexpr int CHUNK_THREADS = 256;
 template <bool F32>
-__global__ void __launch_bounds__(CHUNK_THREADS) sample_chunk_kernel(SampleArgs a, int chunks, int share, Chunk* info, uint64_t* lists, uint64_t* steps) {
+__global__ void __launch_bounds__(CHUNK_THREADS, 6) sample_chunk_kernel(SampleArgs a, int chunks, int share, Chunk* info, uint64_t* lists, uint64_t* steps) {
     __shared__ ChunkShared s;
     const long long n = (long long)a.B * chunks;
     for (long long i = blockIdx.x; i < n; i += gridDim.x) {
