@@ -414,9 +414,10 @@ int moe_glu_fp8(const uint8_t* d_a, const uint8_t* d_sa, const uint8_t* d_w13, c
  * temperature 0 is greedy: the first token of the order, whatever the rest
  * say. d_ids[r] gets the id, d_p[r] its weight divided by the kept weight of
  * all (1 if greedy).
- * Weights are formed in fp64 and summed as integers, in multiples of 2^-42
- * of the row's largest: sums have no order, results repeat bit for bit, and
- * a token of less than half of that is never drawn.
+ * Weights are formed in fp64 and summed in fp64 in a fixed order, or as
+ * integers in multiples of 2^-42 of a largest weight: results repeat bit for
+ * bit, and no sum is off by more than cols * 2^-43 of the row's largest
+ * weight. With a filter, a token of less than 2^-46 of that may be left out.
  *  d_logits f32 (MOE_OUT_F32) or bf16 (MOE_OUT_BF16) [rows, cols], rows
  *  row_stride >= cols elements apart (a head padded to a larger vocabulary);
  *  d_u f32 [rows] in [0, 1]; d_temperature f32 [rows], d_top_k i32 [rows],

@@ -938,8 +938,9 @@ __device__ __noinline__ void sample_many(SampleArgs a, int r, int chunks, const 
     __syncthreads();
     // ---- top_p alone, with many tokens: the chunks' weights by steps say in which
     // step the border lies; that step's tokens, taken from the row, and 2048 equal
-    // parts of them, where. False where the step's tokens are too many, or min_p may
-    // have the border.
+    // parts of them, where. min_p's border lies in a step as well: the kept tokens are
+    // those of the steps above the first of the two steps, and some of its own. False
+    // where the step's tokens are too many.
     auto by_steps = [&](uint64_t& border) __attribute__((always_inline)) {
         const int first = q.step(top);
         each_chunk(chunks, [&](int c, bool in) __attribute__((always_inline)) {
@@ -980,7 +981,15 @@ __device__ __noinline__ void sample_many(SampleArgs a, int r, int chunks, const 
             atomicMax(&s.at[0], STEPS - t);
         }
         __syncthreads();
-        const int b = STEPS - s.at[0];                           // (none: past the last one)
+        const int bp = STEPS - s.at[0];                          // (none: past the last one)
+        int b = bp;
+        if (q.m_on) {
+            // logits on both sides of min_p's border, by more than their own roundings; in one step, or not certain
+            const float below = q.least(top, q.min_p), above = below + 2.f * (top - below + fabsf(top) + q.temperature) * 1e-5f;
+            const int bm = first - q.step(fminf(above, top));
+            if (bm < first - q.step(below)) return false;
+            b = min(b, bm);
+        }
         if (b >= STEPS) return false;
         if (t == b) s.got[0] = start;
         const int in_step = first - b;
@@ -1036,6 +1045,19 @@ __device__ __noinline__ void sample_many(SampleArgs a, int r, int chunks, const 
         __syncthreads();
         const int n = s.n;
         if (n > 2 * LIST) return false;
+        auto sum_kept = [&](uint64_t border) __attribute__((always_inline)) {
+            for (int i = t; i < n; i += ST) {
+                const double w = weight(place_logit(tokens[i]));
+                if (tokens[i] >= border && w >= q.min_p)
+                    atomicAdd((unsigned long long*)&s.kept[place_id(tokens[i]) / CHUNK], (unsigned long long)mass_of(w));
+            }
+            __syncthreads();
+        };
+        if (b < bp) {                                            // (min_p's alone)
+            border = 0;
+            sum_kept(border);
+            return true;
+        }
         // their range, in parts; the part that reaches what is left of `want`
         uint64_t hi = 0, lo = ~0ull;
         for (int i = t; i < n; i += ST) {
@@ -1120,10 +1142,7 @@ __device__ __noinline__ void sample_many(SampleArgs a, int r, int chunks, const 
             __syncthreads();
             border = s.before[1];
         }
-        if (q.m_on && weight(place_logit(border)) < q.min_p) return false;
-        for (int i = t; i < n; i += ST)
-            if (tokens[i] >= border) atomicAdd((unsigned long long*)&s.kept[place_id(tokens[i]) / CHUNK], (unsigned long long)mass(place_logit(tokens[i])));
-        __syncthreads();
+        sum_kept(border);
         return true;
     };
 
@@ -1131,7 +1150,11 @@ __device__ __noinline__ void sample_many(SampleArgs a, int r, int chunks, const 
         auto kept = [&](int c, bool in) __attribute__((always_inline)) { return in ? s.above[c] + (double)s.kept[c] * (1.0 / ONE) : 0.0; };
         double total = 0.0;
         each_chunk(chunks, [&](int c, bool in) __attribute__((always_inline)) { total += wave_all<Plus>(kept(c, in)); });
-        return draw_by_chunks<F32>(a, r, row, chunks, kept, weight, total, border, s);
+        auto kept_weight = [&](float x) __attribute__((always_inline)) {
+            const double w = weight(x);
+            return w >= q.min_p ? w : 0.0;
+        };
+        return draw_by_chunks<F32>(a, r, row, chunks, kept, kept_weight, total, border, s);
     }
 
     // ---- the row's logits (but those of 2^-46 of the largest weight and less)

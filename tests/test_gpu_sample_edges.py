@@ -63,6 +63,23 @@ def test_chunks_without_a_token(gpu, V, masked):
         assert _against_oracle(gpu, l, u, par).mean() > 0.6
 
 
+@pytest.mark.parametrize("V", [20000, 131072, 300007])
+def test_min_p_among_many(gpu, V):
+    """Rows from flat to peaked whose last kept token is top_p's or min_p's, thousands of tokens behind the first, near it, or the first."""
+    f = np.float32
+    B = 12
+    r = np.random.default_rng([14, V])
+    l = (r.normal(size=(B, V)) * np.array([0.02, 0.3, 0.8, 1.2, 2, 3] * 2)[:, None]).astype(f)
+    l[6:] += f(100)
+    for pp, mp in ((0.97, 1e-4), (0.99, 1e-3), (0.9, 0.01), (0.999, 0.05), (0.6, 0.3), (0.95, 0.9), (0.9, 1.0), (0.9999, 1e-9), (0.8, 1e-30)):
+        _say(f"[min_p] V={V} p={pp} m={mp}")
+        par = [(0.7 + 0.8 * r.random(B)).astype(f), None, np.full(B, pp, f), np.full(B, mp, f)]
+        # (A demand on the rows, not on the call. Some decide nothing: 2^-45 on both sides of a min_p of 1e-9 is 5.7e-5 of
+        # it, and rows of 131072 have some 2000 tokens for each factor of e there; V 2^-42 = 7e-8 on both sides of top_p's
+        # border reaches the next token where the border's weights are 1e-6 and less, as in long peaked rows with 0.999.)
+        assert _against_oracle(gpu, l, r.random(B).astype(f), par).mean() >= 0.5
+
+
 def test_workspaces(gpu):
     """The caller's: exact, larger, with anything in it; too small or off its alignment is refused. Calls on two streams at once have one each."""
     import torch
