@@ -921,12 +921,10 @@ __device__ __forceinline__ bool find_border(const Request& q, float top, float f
     return found;
 }
 
-// Rows whose border may lie behind the candidates. A function of its own, so that
-// its registers do not weigh on the others: the kernel with it inside spilled 77.
+// Rows whose border may lie behind the candidates.
 template <bool F32>
-__device__ __noinline__ void sample_many(SampleArgs a, int r, int chunks, const Chunk* info, const uint64_t* steps, float top, float low, double all) {
-    extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-    RowShared& s = *(RowShared*)smem;
+__device__ __forceinline__ void sample_many_row(const SampleArgs& a, int r, int chunks, const Chunk* info, const uint64_t* steps, float top, float low, double all,
+                                                RowShared& s) {
     const void* row = (const uint8_t*)a.logits + (size_t)r * a.stride * (F32 ? 4 : 2);
     const int V = a.V, t = threadIdx.x, lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(t / 64);
     const Request q(a, r);
@@ -1020,9 +1018,15 @@ __device__ __noinline__ void sample_many(SampleArgs a, int r, int chunks, const 
         uint64_t* tokens = s.list;                               // (and s.sorted behind it)
         const float slope = 8.f / q.temperature, in_this = (float)in_step;
         constexpr int D = 8;                                     // loads in flight; one addition for a wave's tokens of them
+        float x[D][4], next[D][4];
+        load_fours<F32>(row, 4 * t, ST * 4, 0, D * ST * 4, V, next);
         for (int base = 0; base < V; base += D * ST * 4) {
-            float x[D][4];
-            load_fours<F32>(row, base + 4 * t, ST * 4, base, D * ST * 4, V, x);
+#pragma unroll
+            for (int d = 0; d < D; ++d)
+#pragma unroll
+                for (int v = 0; v < 4; ++v) x[d][v] = next[d][v];
+            const int ahead = base + D * ST * 4;
+            if (ahead < V) load_fours<F32>(row, ahead + 4 * t, ST * 4, ahead, D * ST * 4, V, next);
             uint32_t mine = 0;
 #pragma unroll
             for (int d = 0; d < D; ++d)
@@ -1202,6 +1206,22 @@ __device__ __noinline__ void sample_many(SampleArgs a, int r, int chunks, const 
     }
 }
 
+// (parameters arrive in a lane's registers)
+template <typename T>
+__device__ __forceinline__ T uniform(T v) { return of_lane(v, 0); }
+using KernelArgs = const __attribute__((address_space(4))) SampleArgs;
+// A function of its own, so that its registers do not weigh on the others (the kernel
+// with it inside spilled 77), and the program's end, so that it saves none of them
+// (with a return it began with 8 us of stores). From `args`, the kernel's arguments.
+template <bool F32>
+__device__ __noinline__ __attribute__((noreturn)) void sample_many(const KernelArgs* args, int r, int chunks, const Chunk* info, const uint64_t* steps,
+                                                                   float top, float low, double all) {
+    extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+    const SampleArgs a = *(const SampleArgs*)uniform(args);
+    sample_many_row<F32>(a, uniform(r), uniform(chunks), uniform(info), uniform(steps), uniform(top), uniform(low), uniform(all), *(RowShared*)smem);
+    __builtin_amdgcn_endpgm();
+}
+
 // `listed`: the row's one chunk has left its candidates in s.list
 template <bool F32>
 __device__ __forceinline__ void sample_finish(const SampleArgs& a, int r, int chunks, int share, const Chunk* info, const uint64_t* lists, const uint64_t* steps,
@@ -1367,7 +1387,7 @@ __device__ __forceinline__ void sample_finish(const SampleArgs& a, int r, int ch
                                                  }
                                          },
                                          [](uint32_t, double) {}, border, s);
-    if (!sure) return sample_many<F32>(a, r, chunks, info, steps, top, low, all);
+    if (!sure) sample_many<F32>((KernelArgs*)__builtin_amdgcn_kernarg_segment_ptr(), r, chunks, info, steps, top, low, all);
     // the draw by id: a run of the list for each thread
     __syncthreads();
     const int run = (n + ST - 1) / ST, i0 = min(t * run, n), i1 = min(i0 + run, n);
