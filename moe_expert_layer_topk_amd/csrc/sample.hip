@@ -21,13 +21,26 @@
 // finish kernel: one workgroup a row. Counts and weights of 2048 equal parts of
 // the candidates' range say which part holds a border, and its tokens, put in
 // order, where. It holds if it lies before every logit that was left out
-// (nearly always, with a filter); else (a top_p that keeps thousands of tokens)
-// the same is done with all of the row's logits, read again. No filter: the
-// chunk that the draw falls into is read again.
+// (nearly always, with a filter); else (a top_p or min_p that keeps thousands of
+// tokens) the chunks' weights by steps of an eighth of the temperature say in
+// which step it lies, and the row is read again for that step's tokens; and where
+// these are too many (equal logits), the same is done with all of the row's. No
+// filter: the chunk that the draw falls into is read again.
 //
-// Weights are fp64, sums of them fp64 in a fixed order; the parts' weights are
-// summed with atomics, and therefore as integers (multiples of 2^-42 of the
-// largest weight).
+// Weights are fp64, sums of them fp64 in a fixed order; the parts' and the steps'
+// weights are summed with atomics, and therefore as integers (multiples of 2^-42 of
+// the largest weight).
+//
+// What bounds it: rows x 131072 logits want the copy's rate, 5 TB/s, and the chunk
+// kernel's vector unit is busy 90% of the time before that: an exponential in
+// fp64 takes 20 instructions a logit, the rest some 20. 256 x 131072 fp32 (134 MB):
+// without a filter 39 us (3.4 TB/s), with all four 52..57 (chunks 43, rows 14; 67..70
+// where one of the rows keeps thousands of tokens), with top_p alone 108 (chunks 77,
+// half of it the weights by steps; then such rows). One row of 131072 is launch and
+// latency: 12 us with top_k of 20 (chunks 7, row 5..12), 19 with several hundred, 40
+// where thousands are kept; up to 4096 logits are one kernel, 6 us. (One workgroup
+// of 1024 threads for a row of any length took 1580 us at 131072, chunks of
+// 16384 logits 26 us where those of 4096 take 19.)
 #include "moe_common.h"
 #include "moe_kernels.h"
 #include "gemm_tile.h"
