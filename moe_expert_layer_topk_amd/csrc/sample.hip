@@ -966,7 +966,8 @@ __device__ __forceinline__ void sample_many_row(const SampleArgs& a, int r, int 
         __syncthreads();
         // the row's steps (from its largest logit's on), up to the one that reaches `want`
         // (a fourth of the chunks a thread, eight loads together)
-        const double want = q.top_p * all;
+        // (more than nothing, so that with top_p of 0 the border is the first token too: its weight is 1)
+        const double want = fmax(q.top_p * all, 1.0 / ONE);
         double own = 0.0, total;
         double* parts_of = (double*)s.sorted;
         for (int c0 = t / STEPS; c0 < chunks; c0 += 32) {
