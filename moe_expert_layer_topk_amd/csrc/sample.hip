@@ -44,6 +44,7 @@
 #include "moe_common.h"
 #include "moe_kernels.h"
 #include "gemm_tile.h"
+#include "sample_plan.h"
 
 namespace moe {
 
@@ -126,7 +127,7 @@ struct Request {
         const float u = a.u[r], tp = a.top_p ? a.top_p[r] : 1.f, mp = a.min_p ? a.min_p[r] : 0.f;
         bad = !(u >= 0.f && u <= 1.f) || !(temperature >= 0.f) || tp != tp || !(mp <= 1.f);
         scale = temperature > 0.f ? 46.16624130844682903552 / (double)temperature : 0.0;
-        k = temperature == 0.f ? 1 : a.top_k ? max(a.top_k[r], 0) : 0;
+        k = temperature == 0.f ? 1 : a.top_k ? kept_by_count(a.top_k[r]) : 0;
         top_p = tp > 0.f ? tp : 0.f;
         min_p = mp > 0.f ? mp : 0.f;
         p_on = tp < 1.f && k != 1;
@@ -531,7 +532,7 @@ __device__ __forceinline__ void sample_chunk(const SampleArgs& a, int r, int c, 
     places();
     // More than the share, or than a few times k: those of the parts up to the k-th
     // (what is left out then is out), or of as many parts as fit the share.
-    if (total > share || (q.k && total > 2 * q.k + 64)) {
+    if (total > share || worth_parts(total, q.k)) {
         const Parts<CHUNK_BINS> part(top, floor);
 #pragma unroll
         for (int j = 0; j < NV; ++j)
