@@ -7,10 +7,15 @@
 // bf16 outputs: a block's sum is one FP8 matrix instruction (K = 128), which
 // takes A's scale as an operand. It aligns the products of each group of its K
 // at the largest one's exponent and drops what lies 14 bits and more below
-// (measured: 2^16 - 2^16 + 2^3 gives 2^3, + 2^2 gives 0), which is well below
-// bf16's own step: 1.1e-4 of the output's norm, where bf16 rounds 1.7e-3 off.
-// fp32 outputs would show it (1.1e-5 .. 1.5e-5 of the norm), so their codes are
-// widened to bf16, exactly, for the bf16 instruction, which drops 25 bits below.
+// (measured: 2^16 - 2^16 + 2^3 gives 2^3, + 2^2 gives 0). Before their rounding the
+// sums are 1.5e-5 of the outputs' norm off on codes of normal values and 5.8e-5 on
+// codes with heavy tails (normal values times e^(1.5 n)); rounding to bf16 costs
+// 1.7e-3, and the error of the rounded outputs is the same in three digits with
+// exact sums: a few outputs in a thousand are the neighbouring bf16 value, which is
+// 1.9e-4 .. 4.8e-4 of the norm. The bf16 instruction's sums would take four
+// instructions for one (16384 x 2048 x 2048 145 us for 66). fp32 outputs would show
+// the loss (theirs are 1e-7 off), so their codes are widened to bf16, exactly, for
+// the bf16 instruction, which drops 25 bits below.
 // The running sum over the blocks is fp32, one fused multiply-add per block.
 //
 // A step of 128 K bytes is a block of the scales. Tiles start at multiples of
@@ -79,18 +84,23 @@ __device__ __forceinline__ f32x4 mfma_block(const i32x8& a, const i32x8& b, int 
 // Scales: rows' bytes and blocks' floats for 16 steps at a time, loaded two steps
 // ahead, in LDS by the barrier before they are read. [step][64 rows][m] is a
 // dword with rows m, 16 + m, 32 + m and 48 + m, the instruction's four byte places.
-// What it reaches (us, one call after another; the rate of 2 M N K operations):
-// 4096 x 8192 x 8192 230 (2390 TFLOP/s), 16384 x 2048 x 2048 67 (2050), gated
-// 16384 x 512 x 2048 33 (2090), 8192^3 456 (2410). A library product of the same
-// codes with one scale for the whole tensor takes 207, 63.5, (32 without the gate)
-// and 416. The difference is the multiply-add that a block's scale costs: 4 for an
-// instruction of 32 clocks, and power: matrix pipes are busy 58% of the clocks at
-// 1.8 GHz, on codes of zero the same kernel takes 198 us instead of 230. 256 x 256
-// tiles read 411 MB of L2 misses there for 101 MB of operands (last-level cache).
+// What it reaches (us, one call after another, medians; the rate of 2 M N K
+// operations): 4096 x 8192 x 8192 235 (2340 TFLOP/s; 226..246 over all runs), 16384 x
+// 2048 x 2048 66 (2090), gated 16384 x 512 x 2048 32.4 (2120), 8192^3 463 (2370). A
+// library product of the same codes with one scale for the whole tensor takes
+// 173, 54.5, (29 without the gate) and 341 in windows of 50 ms and more (its first
+// milliseconds are slower). Matrix pipes are busy 58% of the clocks, at 1.9 GHz. Power
+// is a part of it (198 us instead of 235 on codes of zero, at 2.4 GHz), not
+// all: the library takes 130 there. The rest stands between the matrix
+// instructions and is not told apart: four multiply-adds that a block's scale costs
+// for each of 32 clocks, reads of fragments, a barrier a step. 256 x 256 tiles read
+// 411 MB of L2 misses there for 101 MB of operands (last-level cache).
 // Tried without gain: the multiply-add 2 or 4 instructions behind, B's next
 // fragment one instruction earlier (233 us), wave priorities on this tile, steps with
 // their branches taken out into copies (spills). fp32 outputs on 128 x 128 tiles:
-// 4096 x 2048 x 2048 40 us (860 TFLOP/s), four bf16 instructions for one.
+// 4096 x 2048 x 2048 40 us (865 TFLOP/s), 16384 x 2048 x 2048 145 (945), four bf16
+// instructions for one; a library bf16 product reaches 1470 at the second size. The codes
+// are widened again in every wave and tile that reads them.
 // K's end: chunks past it are set to zero in LDS by the lanes that loaded them
 // (zero times a NaN code from the next row would be NaN).
 constexpr int SCALE_STEPS = 16;
@@ -476,7 +486,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gemm_fp8_tile_kernel(Fp8Args 
 // waves' order. The instruction's rows are columns of the output here and its
 // columns rows: a lane then has one row of A, whose scale byte it loads with the stage.
 // 1 x 2048 x 2048 3.6 us (launch and first latency), 8 x 131072 x 2048 with fp32
-// outputs 53 us from memory (5.1 TB/s, a copy's rate), 333 x 1000 x 4112 fp32 10.2 us:
+// outputs 53.5 us from memory (5.1 TB/s, a copy's rate), 333 x 1000 x 4112 fp32 10.8 us:
 // 176 tiles of 32 x 64 on 256 CUs, 66 MB from L2 to LDS, 26% of the vector unit for
 // the widening.
 template <int TM, int TN, int WK, bool GLU, bool F32>

@@ -24,15 +24,18 @@ constexpr int records(size_t n) { return n > 0x7FFFFFF0u ? 0x7FFFFFF0 : (int)n; 
 constexpr int NOWHERE = 0x7FFFFFF0;
 constexpr int records_from(int all, int k0) { return all - k0 > 0 ? all - k0 : 0; }
 
-// The tile shapes, and what they cost (us): a K step of 128 with at most one
-// workgroup on each CU (`one`) and with all `per_cu` of them (`full`), and a
-// round's prologue and epilogue (`round`). K <= 128 counts as one step; the
-// persistent tiles run a second one there, of zeros. One `round` stands for plain
-// and gated epilogues, with and without addends, on rows of every
-// kind. Large tiles move fewer bytes per output, small ones reach more CUs. The
-// figures are a fit to 1100 products
-// with random sizes (1..16384 rows, 64..8192 columns, K 128..8192), each timed
-// with every shape: where the best takes 5.5 us and more, the shape picked by
+// The tile shapes, and weights for choosing among them: a K step of 128 with at
+// most one workgroup on each CU (`one`) and with all `per_cu` of them (`full`), and
+// a round's prologue and epilogue (`round`). They are no times: the fit makes the
+// picked shape's measured time least, which only the shapes' sums beside one
+// another decide (e4m3 4096 x 8192 x 8192: a sum of 163, measured 235 us; 4096 x
+// 2048 x 2048 with fp32 outputs: 16 and 40 us), so a new shape is fitted with the
+// others, not added by its own time. K <= 128 counts as one step; the persistent
+// tiles run a second one there, of zeros. One `round` stands for plain and gated
+// epilogues, with and without addends, on rows of every kind. Large tiles move
+// fewer bytes per output, small ones reach more CUs. The weights are a fit to 1100
+// products with random sizes (1..16384 rows, 64..8192 columns, K 128..8192), each
+// timed with every shape: where the best takes 5.5 us and more, the shape picked by
 // them is 0.6% slower than it on average (below, the five differ by little more
 // than two runs of one). E.g. 333 x 1000 x 4112: 32x64 8.9 us, 64x64 11.4,
 // 128x128 22; 400 x 2048 x 2048: 64x64 6.7, 32x32 8.3, 128x128 11; 2048^3:
@@ -63,7 +66,7 @@ constexpr int split_waves(int shape, bool few) {
     return shape == S_32x32 ? 8 : shape == S_64x64 || shape == S_32x64 ? (few ? 8 : 4) : 0;
 }
 
-// The shape that a table's costs make the fastest for this many output rows
+// The shape with the least sum of a table's weights for this many output rows
 // and B rows. Small tiles have a workgroup each, and a launch holds fewer than
 // 2^32 threads: where theirs would hold more (2^23 tiles of eight waves, 2^24 of
 // four: some 2^29 rows on one side) they are left out; a persistent grid takes
@@ -88,7 +91,7 @@ constexpr int pick_shape(const Shape (&table)[S_COUNT], int M, long long rows_b,
 }
 constexpr int pick_shape(int M, long long rows_b, int K, long long cus) { return pick_shape(kShapes, M, rows_b, K, cus); }
 
-// The e4m3 products (gemm_fp8.hip) have the same shapes at costs of their own;
+// The e4m3 products (gemm_fp8.hip) have the same shapes with weights of their own;
 // with fp32 outputs, whose codes are widened to bf16 in registers, no 256 x 256
 // tile. Fits to 4300 products with bf16 outputs, plain and gated, and 5300 with
 // fp32 outputs (1..16384 rows, 64..16384 columns, fp32 to 32768, K 128..8192),

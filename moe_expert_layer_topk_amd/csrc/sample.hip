@@ -32,11 +32,22 @@
 // the largest weight).
 //
 // What bounds it: rows x 131072 logits want the copy's rate, 5 TB/s, and the chunk
-// kernel's vector unit is busy 90% of the time before that: an exponential in
-// fp64 takes 20 instructions a logit, the rest some 20. 256 x 131072 fp32 (134 MB):
-// without a filter 39 us (3.4 TB/s), with all four 52..57 (chunks 43, rows 14; 67..70
-// where one of the rows keeps thousands of tokens), with top_p alone 108 (chunks 77,
-// half of it the weights by steps; then such rows). One row of 131072 is launch and
+// kernel's vector unit is busy before that. 256 x 131072 fp32 (134 MB, 26.6 us to
+// copy), vector instructions of a wave for its 16 logits a lane, us of the two kernels:
+//   greedy              334   25 +  5   the logit's place in the order, a largest one in 64 bits
+//   no filter           521   37 +  7   an exponential, 20 instructions a logit (14 of them fp64)
+//   top_k of 50         486   34 + 10   no exponential but the choice of candidates: by the listing 190 for
+//                                       their writes (one predicated for each element), 100 for the bound by the
+//                                       threads' largest, 60 for the mask, 36 for the places, 37 for the row's parameters
+//   top_p alone        1358   81 + 43   exponentials, a 64-bit addition in LDS for each logit's step, then candidates
+//   all four            614   42 + 14   four fifths of these rows have top_k: as that, and parts where candidates are many
+// The row kernels of top_p alone wait for one workgroup that reads a row again
+// (thousands of kept tokens); likewise 52..57 us with all four, and 62..70 where one of
+// the rows keeps thousands. The bf16 row kernels spill 8 vector registers (224 bytes of
+// scratch a lane; the fp32 ones spill scalars alone, 160 bytes): 256 x 131072 with
+// top_k and top_p, rows without top_k among them, 48 + 43 us, fp32 48 + 36. More rows
+// than CUs are a second round of workgroups that have a CU each (100 KB of LDS): 512 x
+// 16000 21 + 36. One row of 131072 is launch and
 // latency: 12 us with top_k of 20 (chunks 7, row 5..12), 19 with several hundred, 40
 // where thousands are kept; up to 4096 logits are one kernel, 6 us. (One workgroup
 // of 1024 threads for a row of any length took 1580 us at 131072, chunks of
