@@ -10,7 +10,7 @@
 // (measured: 2^16 - 2^16 + 2^3 gives 2^3, + 2^2 gives 0). Before their rounding the
 // sums are 1.5e-5 of the outputs' norm off on codes of normal values and 5.8e-5 on
 // codes with heavy tails (normal values times e^(1.5 n)); rounding to bf16 costs
-// 1.7e-3, and the error of the rounded outputs is the same in three digits with
+// 1.7e-3, and the error of the rounded outputs is within 1% of what it is with
 // exact sums: a few outputs in a thousand are the neighbouring bf16 value, which is
 // 1.9e-4 .. 4.8e-4 of the norm. The bf16 instruction's sums would take four
 // instructions for one (16384 x 2048 x 2048 145 us for 66). fp32 outputs would show
@@ -84,9 +84,10 @@ __device__ __forceinline__ f32x4 mfma_block(const i32x8& a, const i32x8& b, int 
 // Scales: rows' bytes and blocks' floats for 16 steps at a time, loaded two steps
 // ahead, in LDS by the barrier before they are read. [step][64 rows][m] is a
 // dword with rows m, 16 + m, 32 + m and 48 + m, the instruction's four byte places.
-// What it reaches (us, one call after another, medians; the rate of 2 M N K
-// operations): 4096 x 8192 x 8192 235 (2340 TFLOP/s; 226..246 over all runs), 16384 x
-// 2048 x 2048 66 (2090), gated 16384 x 512 x 2048 32.4 (2120), 8192^3 463 (2370). A
+// What it reaches (us; the rate of 2 M N K operations; medians of calls on a few
+// inputs in turn): 4096 x 8192 x 8192 235 (2340 TFLOP/s; 226 .. 247 over all runs, 247
+// with new inputs before each call), 16384 x 2048 x 2048 66 (2090; 66 .. 70), gated
+// 16384 x 512 x 2048 32.4 (2120; 32 .. 34), 8192^3 463 (2370). A
 // library product of the same codes with one scale for the whole tensor takes
 // 173, 54.5, (29 without the gate) and 341 in windows of 50 ms and more (its first
 // milliseconds are slower). Matrix pipes are busy 58% of the clocks, at 1.9 GHz. Power
